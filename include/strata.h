@@ -76,13 +76,20 @@ typedef enum {
    again before reusing it with this flag. */
 #define STRATA_WS_REUSE 0x8u
 
+/* Flag of strata_kv_append. */
+#define STRATA_ROPE_NEIGHBOURS 0x1u /* the rotation pairs elements (2i, 2i + 1) instead of
+                                       (i, i + rot_dim / 2) */
+
 /* Bits of the device status word. */
 #define STRATA_DEV_NONFINITE 0x1u /* a quantized group held inf/nan (its scale is written as NaN,
-                                     its codes as 0) */
+                                     its codes as 0); strata_kv_append: a row of K or V held inf/nan */
 #define STRATA_DEV_BAD_ID 0x2u    /* an expert id outside [0, E) reached the permutation */
 #define STRATA_DEV_TIMEOUT 0x4u   /* a bounded device wait gave up */
 #define STRATA_DEV_BAD_TOKENS 0x8u /* strata_moe_forward_padded: the device token count was outside
                                       [0, T_max]; the call ran with no live token */
+#define STRATA_DEV_BAD_SLOT 0x10u /* strata_kv_append: a slot or a position out of range (the row was
+                                     skipped); strata_attention_forward: a page index, row range or
+                                     length out of range (what it names was left out) */
 
 #define STRATA_GROUP 128     /* [tuning-moe] §2.1: 128 weights share one scale */
 #define STRATA_MAX_EXPERTS 1024
@@ -336,6 +343,128 @@ size_t strata_moe_host_staging_size(const strata_moe_layer* layer, int64_t T_max
 strata_status strata_moe_forward_host(const strata_moe_layer* layer, const void* x_host,
                                       int64_t T, void* out_host, void* workspace, size_t ws_bytes,
                                       strata_stream stream);
+
+/*
+ * The attention half of a decoder block around the MoE layer: quantized projections, a paged cache
+ * of 8-bit keys and values, and attention over it ([tuning-moe] §2.1: the engine keeps its
+ * attention projections at 8 bits in the same group format, the output projection at 4). The pages
+ * do not describe the cache; its format and the calls are this library's own.
+ */
+
+/* One dense projection: codes and scales are outputs of strata_quantize_groups_bits. */
+typedef struct {
+  int64_t N;           /* output features, 1 .. 2^20 */
+  int64_t K;           /* input features, % group_size == 0, up to 2^16 */
+  int32_t group_size;  /* 128 (0 means 128), 64 or 256 */
+  int32_t bits;        /* 4 (0 means 4) or 8 */
+  const uint8_t* codes; /* [N, K/2] (4 bits) or [N, K] int8 (8 bits), 16-byte aligned */
+  const void* scales;  /* [N, K/group_size] fp16 */
+  const float* bias;   /* [N] fp32 or NULL */
+} strata_linear;
+
+/*
+ * strata_linear_forward — out[t,n] = sum_c x[t,c] * q[n,c] * scale[n, c / group_size] + bias[n]
+ * (+ residual[t,n]), summed in fp32 and rounded once to bf16.
+ * x_bf16 [T,K], out_bf16 [T,N], residual_bf16 [T,N] or NULL: bf16, device, consecutive elements in a
+ * row; *_stride: elements from one row to the next (>= the row's length; x: a multiple of 8, and x
+ * 16-byte aligned). out may be the residual itself (same address and stride); otherwise out
+ * overlaps no input. T == 0 is a no-op.
+ * Up to STRATA_LINEAR_STREAM_T tokens the codes are multiplied as exact integers and scaled in fp32;
+ * longer batches multiply weights rounded once to bf16 (2^-9 relative) on the tensor cores.
+ * workspace >= strata_linear_workspace_size(w, T) bytes (0: the projection or T is invalid),
+ * 256-byte aligned, device; it needs no initialisation. strata_workspace_status reads its status.
+ */
+#define STRATA_LINEAR_STREAM_T 32
+size_t strata_linear_workspace_size(const strata_linear* w, int64_t T_max);
+strata_status strata_linear_forward(const strata_linear* w, const void* x_bf16, int64_t x_stride,
+                                    int64_t T, const void* residual_bf16, int64_t residual_stride,
+                                    void* out_bf16, int64_t out_stride, void* workspace,
+                                    size_t ws_bytes, strata_stream stream);
+
+/*
+ * A paged cache of keys and values in 8 bits. A page holds page_size consecutive tokens of one
+ * sequence for every head. Values are e4m3 codes times one fp32 scale per (page, head), one for K
+ * and one for V. strata_kv_append writes power-of-two scales: a floating code loses nothing by
+ * that, and a page whose range grows later is rescaled exactly (but for e4m3 subnormals).
+ * Slot s of the cache is token s % page_size of page s / page_size. No initialisation is needed: a
+ * page counts from the token that is put at its start.
+ */
+typedef struct {
+  int32_t n_kv_heads; /* 1 .. 256 */
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t page_size;  /* 16, 32, 64 or 128 */
+  int64_t n_pages;    /* n_pages * page_size <= 2^31 - 1 */
+  uint8_t* k_codes;   /* [n_pages, n_kv_heads, page_size, head_dim] e4m3, 16-byte aligned */
+  uint8_t* v_codes;   /* the same */
+  float* k_scales;    /* [n_pages, n_kv_heads] */
+  float* v_scales;    /* the same */
+} strata_kv_cache;
+
+/*
+ * strata_kv_append — rotates the T rows of k (and of q) by their positions and stores k and v in the
+ * cache. Row t goes to slot slots[t]; a negative slot marks a padding row, of which nothing is
+ * read or written.
+ *   rotation of pair (a, b) of a head's first rot_dim elements, in fp32:
+ *     a' = a*cos - b*sin, b' = b*cos + a*sin,   cos = rope[pos][i], sin = rope[pos][rot_dim/2 + i]
+ *     with a, b = elements i and i + rot_dim/2, or 2i and 2i + 1 with STRATA_ROPE_NEIGHBOURS
+ *   scale of a page and head: 2^e, e the smallest integer >= -100 with absmax <= 448 * 2^e over
+ *     the tokens of the page. Rows that begin inside a page (slot % page_size > 0) keep the tokens
+ *     before them: the scale never falls, and if it grows the older codes are rewritten.
+ *   codes: value / scale rounded to e4m3, nearest-even, once.
+ * A (row, head) whose rotated k or v holds inf or nan sets STRATA_DEV_NONFINITE, gets k codes nan
+ * and v codes 0, and has no part in the scale: the nan reaches the queries that see the token and
+ * no others.
+ * k, v [T, n_kv_heads * head_dim], q and q_out [T, n_heads * head_dim] bf16, device; rows
+ * 16-byte aligned, strides in elements, multiples of 8. q, q_out NULL: keys and values only. q_out
+ * may be q itself (same stride).
+ * slots, positions [T] int32 (device); rope [n_pos, rot_dim] fp32, 16-byte aligned (device).
+ * rot_dim: 0 (no rotation: rope and positions may be NULL) or a multiple of 16 up to head_dim.
+ * The rows of a call that fall into one page must be consecutive rows with consecutive slots. A
+ * slot >= n_pages * page_size or a position outside [0, n_pos) sets STRATA_DEV_BAD_SLOT and the row
+ * is skipped. dev_status: device uint32 or NULL. T == 0 is a no-op; T <= 2^22.
+ */
+strata_status strata_kv_append(const strata_kv_cache* cache, const void* q_bf16, int64_t q_stride,
+                               int32_t n_heads, const void* k_bf16, int64_t k_stride,
+                               const void* v_bf16, int64_t v_stride, int64_t T,
+                               const int32_t* slots, const int32_t* positions, const float* rope,
+                               int64_t n_pos, int32_t rot_dim, uint32_t flags, void* q_out,
+                               int64_t q_out_stride, uint32_t* dev_status, strata_stream stream);
+
+/* The sequences of one attention call. Arrays are on the device, int32. */
+typedef struct {
+  int32_t n_seq;            /* 0 .. 65535 */
+  int32_t max_q;            /* at least the most query rows of one sequence */
+  int64_t T;                /* rows of q and out, up to 2^22 */
+  int64_t max_kv;           /* at least the largest kv_len; up to table_stride * page_size */
+  const int32_t* q_start;   /* [n_seq + 1]: rows q_start[s] .. q_start[s+1] - 1 belong to sequence s */
+  const int32_t* kv_len;    /* [n_seq]: tokens of the sequence in the cache, those of this call among them */
+  const int32_t* page_table; /* [n_seq, table_stride]: the sequence's pages in order */
+  int64_t table_stride;
+} strata_kv_batch;
+
+/*
+ * strata_attention_forward — causal attention of q over the cache. Query i of a sequence with n
+ * query rows and kv_len = L stands at position p = L - n + i and sees tokens j <= p, and
+ * j > p - window when window > 0:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j     (statistics and sums in fp32; no token: zeros)
+ * Head h reads K/V head h / (n_heads / n_kv_heads). q, out [T, n_heads * head_dim] bf16 (device,
+ * 16-byte aligned rows, strides in elements, multiples of 8); rows of no sequence are not written.
+ * Any lengths may be mixed in one call. What the cache holds past kv_len is not used, whatever it
+ * is. A page index outside [0, n_pages) sets STRATA_DEV_BAD_SLOT and its tokens count as unseen;
+ * so does a row range outside [0, T], a length below 0 or above max_kv, or more rows than max_q:
+ * they are cut to the limit.
+ * flags: STRATA_WS_REUSE (the workspace is zero-filled, or was left by a completed call of this
+ * function: it is then not cleared first, and its status word accumulates).
+ * workspace >= strata_attention_workspace_size(cache, batch, n_heads), 256-byte aligned (0: an
+ * argument is invalid). n_seq == 0 or T == 0 is a no-op.
+ */
+size_t strata_attention_workspace_size(const strata_kv_cache* cache, const strata_kv_batch* batch,
+                                       int32_t n_heads);
+strata_status strata_attention_forward(const strata_kv_cache* cache, const strata_kv_batch* batch,
+                                       const void* q_bf16, int64_t q_stride, int32_t n_heads,
+                                       float scale, int32_t window, uint32_t flags, void* out_bf16,
+                                       int64_t out_stride, void* workspace, size_t ws_bytes,
+                                       strata_stream stream);
 
 /*
  * Device status of a route/forward workspace: synchronizes `stream`, returns the status word in

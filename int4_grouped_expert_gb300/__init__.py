@@ -24,14 +24,17 @@ STRATA_ROUTER_FP16 = 0x4
 STRATA_FORCE_WARP_PATH = 0x100
 STRATA_FORCE_TC_PATH = 0x200
 STRATA_WS_REUSE = 0x8
+STRATA_ROPE_NEIGHBOURS = 0x1
 STRATA_DEV_NONFINITE = 0x1
 STRATA_DEV_BAD_ID = 0x2
 STRATA_DEV_TIMEOUT = 0x4
 STRATA_DEV_BAD_TOKENS = 0x8
+STRATA_DEV_BAD_SLOT = 0x10
 STRATA_ERR_DEVICE_STATUS = 6
 STRATA_ERR_TIMEOUT = 7
 GROUP_WORKSPACE_BYTES = 256
 GROUP = 128
+LINEAR_STREAM_T = 32  # STRATA_LINEAR_STREAM_T
 
 
 class StrataError(RuntimeError):
@@ -54,8 +57,32 @@ class strata_moe_layer(ctypes.Structure):
     ]
 
 
+class strata_linear(ctypes.Structure):
+    """Mirror of the C struct strata_linear."""
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("group_size", ctypes.c_int32),
+                ("bits", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class strata_kv_cache(ctypes.Structure):
+    """Mirror of the C struct strata_kv_cache."""
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class strata_kv_batch(ctypes.Structure):
+    """Mirror of the C struct strata_kv_batch."""
+    _fields_ = [("n_seq", ctypes.c_int32), ("max_q", ctypes.c_int32), ("T", ctypes.c_int64),
+                ("max_kv", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64)]
+
+
 _lib = None
 _P = ctypes.c_void_p
+_F32 = ctypes.c_float
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _U32 = ctypes.c_uint32
@@ -89,6 +116,16 @@ _SIGNATURES = {
     "strata_moe_host_staging_size": (_SZ, [ctypes.POINTER(strata_moe_layer), _I64]),
     "strata_moe_forward_host": (ctypes.c_int, [ctypes.POINTER(strata_moe_layer), _P, _I64, _P, _P,
                                                _SZ, _P]),
+    "strata_linear_workspace_size": (_SZ, [ctypes.POINTER(strata_linear), _I64]),
+    "strata_linear_forward": (ctypes.c_int, [ctypes.POINTER(strata_linear), _P, _I64, _I64, _P, _I64,
+                                             _P, _I64, _P, _SZ, _P]),
+    "strata_kv_append": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache), _P, _I64, _I32, _P, _I64, _P,
+                                        _I64, _I64, _P, _P, _P, _I64, _I32, _U32, _P, _I64, _P, _P]),
+    "strata_attention_workspace_size": (_SZ, [ctypes.POINTER(strata_kv_cache),
+                                              ctypes.POINTER(strata_kv_batch), _I32]),
+    "strata_attention_forward": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache),
+                                                ctypes.POINTER(strata_kv_batch), _P, _I64, _I32,
+                                                _F32, _I32, _U32, _P, _I64, _P, _SZ, _P]),
     "strata_workspace_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(_U32)]),
     "strata_read_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(_U32)]),
 }
@@ -252,6 +289,47 @@ def strata_moe_forward_host(layer, x_host, T, out_host, workspace, ws_bytes, str
                                          ptr(workspace), ws_bytes, stream_handle(stream))
 
 
+def strata_linear_workspace_size(lin: strata_linear, T_max: int) -> int:
+    return lib().strata_linear_workspace_size(ctypes.byref(lin), T_max)
+
+
+def strata_linear_forward(lin: strata_linear, x, T, out, workspace, ws_bytes, x_stride=None,
+                          residual=None, residual_stride=None, out_stride=None, stream=None):
+    """Strides in elements; None: rows follow one another."""
+    return lib().strata_linear_forward(
+        ctypes.byref(lin), ptr(x), lin.K if x_stride is None else x_stride, T, ptr(residual),
+        lin.N if residual_stride is None else residual_stride, ptr(out),
+        lin.N if out_stride is None else out_stride, ptr(workspace), ws_bytes, stream_handle(stream))
+
+
+def strata_kv_append(cache: strata_kv_cache, k, v, T, slots, positions=None, rope=None, n_pos=0,
+                     rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
+                     q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
+    """Strides in elements; None: rows follow one another."""
+    kv = cache.n_kv_heads * cache.head_dim
+    qd = n_heads * cache.head_dim
+    return lib().strata_kv_append(
+        ctypes.byref(cache), ptr(q), qd if q_stride is None else q_stride, n_heads, ptr(k),
+        kv if k_stride is None else k_stride, ptr(v), kv if v_stride is None else v_stride, T,
+        ptr(slots), ptr(positions), ptr(rope), n_pos, rot_dim, flags, ptr(q_out),
+        qd if q_out_stride is None else q_out_stride, ptr(dev_status), stream_handle(stream))
+
+
+def strata_attention_workspace_size(cache: strata_kv_cache, batch: strata_kv_batch, n_heads) -> int:
+    return lib().strata_attention_workspace_size(ctypes.byref(cache), ctypes.byref(batch), n_heads)
+
+
+def strata_attention_forward(cache: strata_kv_cache, batch: strata_kv_batch, q, n_heads, scale, out,
+                             workspace, ws_bytes, window=0, flags=0, q_stride=None, out_stride=None,
+                             stream=None):
+    """Strides in elements; None: rows follow one another."""
+    qd = n_heads * cache.head_dim
+    return lib().strata_attention_forward(
+        ctypes.byref(cache), ctypes.byref(batch), ptr(q), qd if q_stride is None else q_stride,
+        n_heads, scale, window, flags, ptr(out), qd if out_stride is None else out_stride,
+        ptr(workspace), ws_bytes, stream_handle(stream))
+
+
 def strata_workspace_status(workspace, stream=None):
     v = _U32(0)
     st = lib().strata_workspace_status(ptr(workspace), stream_handle(stream), ctypes.byref(v))
@@ -265,3 +343,4 @@ def strata_read_status(dev_status, stream=None):
 
 
 from .layer import MoELayer  # noqa: E402,F401
+from .attention import PagedKVCache, QuantLinear, kv_batch, rope_table  # noqa: E402,F401

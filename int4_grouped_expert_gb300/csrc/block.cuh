@@ -1,0 +1,65 @@
+// Launchers and argument blocks of the attention half of a decoder block: quantized projections, the
+// paged 8-bit cache and attention over it.
+#pragma once
+
+#include "common.cuh"
+
+namespace strata {
+
+// Up to this many tokens a projection streams its codes through registers (linear.cu).
+constexpr int kLinearStreamT = STRATA_LINEAR_STREAM_T;
+
+struct LinearArgs {
+  const uint8_t* codes;   // [N, K/2] or [N, K]
+  const __half* scales;   // [N, K/group]
+  const float* bias;      // [N] or null
+  const __nv_bfloat16* x; // [T, K], x_stride elements from row to row
+  const __nv_bfloat16* residual;  // [T, N] or null
+  __nv_bfloat16* out;     // [T, N]
+  int64_t x_stride, residual_stride, out_stride;
+  int64_t T;
+  int N, K, group, bits;
+  uint32_t* status;
+};
+cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t stream);
+
+struct KvAppendArgs {
+  strata_kv_cache c;
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t *slots, *positions;
+  const float* rope;
+  int64_t n_pos;
+  int T, n_heads, rot_dim, neighbours;
+  int rows_per_block;     // rows whose runs one K/V block starts
+  uint32_t* status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, int num_sms, cudaStream_t stream);
+
+struct AttnArgs {
+  strata_kv_cache c;
+  strata_kv_batch b;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  int64_t q_stride, out_stride;
+  int n_heads, group;     // query heads; query heads per K/V head
+  float scale_log2;       // softmax scale * log2(e)
+  int window;             // 0: none
+  int n_split;            // contraction splits of a (sequence, K/V head, row block)
+  int split_tokens;       // tokens of one split
+  int row_blocks;         // blocks of query rows per (sequence, K/V head)
+  float* part;            // partial results of the splits
+  uint32_t* counters;     // one per (sequence, K/V head, row block), zero between calls
+  uint32_t* status;
+};
+// How one attention call is laid out: chosen on the host from the limits the caller gives.
+struct AttnPlan {
+  int nt;                 // 8-row tiles of query rows per block: 1 or 2
+  int row_blocks, n_split, split_tokens;
+  size_t part_floats, n_counters;
+};
+AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_heads);
+cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
+
+}  // namespace strata
