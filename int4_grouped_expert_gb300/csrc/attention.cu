@@ -45,13 +45,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// The power of two that a row of f16 queries is divided by, for its largest bf16 magnitude (key as
-// bf16x8_mag): it brings the row's largest entry to [8, 16), so that rows of any size keep their
-// precision. A row of zeros takes 0.
-__device__ __forceinline__ int query_exp(uint32_t mag_key) {
-  return mag_key == 0 ? 0 : min(max(static_cast<int>(mag_key >> 7) - 127 - 3, -120), 120);
-}
-
 // The rows and tokens of one sequence, cut to the call's limits.
 struct SeqView {
   int q0, n;  // first row, rows
@@ -121,7 +114,7 @@ __global__ void __launch_bounds__(kAttWarps * 32) attention_kernel(AttnArgs a) {
     }
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    const int e = query_exp(mag);
+    const int e = row_exp(mag);
     const float sc = exp2i(-e);
 #pragma unroll
     for (int i = 0; i < 2 * KW; ++i) {

@@ -9,6 +9,13 @@ namespace strata {
 // Up to this many tokens a projection streams its codes through registers (linear.cu).
 constexpr int kLinearStreamT = STRATA_LINEAR_STREAM_T;
 
+// The power of two that a row of f16 operands is divided by, for its largest bf16 magnitude (key as
+// bf16x8_mag): it brings the row's largest entry to [8, 16), so that rows of any size keep their
+// precision (entries below 2^-17 of the largest begin to lose bits). A row of zeros takes 0.
+__device__ __forceinline__ int row_exp(uint32_t mag_key) {
+  return mag_key == 0 ? 0 : min(max(static_cast<int>(mag_key >> 7) - 127 - 3, -120), 120);
+}
+
 struct LinearArgs {
   const uint8_t* codes;   // [N, K/2] or [N, K]
   const __half* scales;   // [N, K/group]
@@ -20,8 +27,12 @@ struct LinearArgs {
   int64_t T;
   int N, K, group, bits;
   uint32_t* status;
+  // many tokens (linear_tc.cu): scratch for the f16 copy of x [T, K] and the exponents of its rows
+  __half* xh;
+  int* xexp;
 };
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream);
 
 struct KvAppendArgs {
   strata_kv_cache c;

@@ -34,6 +34,18 @@ strata_status check_linear(const strata_linear* w) {
   return STRATA_OK;
 }
 
+struct LinearLayout {
+  size_t xexp, xh, total;
+};
+LinearLayout linear_layout(const strata_linear* w, int64_t T) {
+  LinearLayout L{};
+  L.xexp = sizeof(WsHeader);
+  const int64_t rows = T > kLinearStreamT ? T : 0;
+  L.xh = round_up(L.xexp + sizeof(int) * rows);
+  L.total = round_up(L.xh + sizeof(uint16_t) * rows * w->K);
+  return L;
+}
+
 strata_status check_cache(const strata_kv_cache* c) {
   if (!c) return STRATA_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return STRATA_ERR_UNSUPPORTED;
@@ -88,7 +100,7 @@ extern "C" {
 
 size_t strata_linear_workspace_size(const strata_linear* w, int64_t T_max) {
   if (check_linear(w) != STRATA_OK || T_max < 0 || T_max > kMaxRows) return 0;
-  return sizeof(WsHeader);
+  return linear_layout(w, T_max).total;
 }
 
 strata_status strata_linear_forward(const strata_linear* w, const void* x_bf16, int64_t x_stride,
@@ -104,8 +116,8 @@ strata_status strata_linear_forward(const strata_linear* w, const void* x_bf16, 
   if (residual_bf16 && (!on(residual_bf16, 2) || residual_stride < w->N)) return STRATA_ERR_INVALID_ARG;
   if (residual_bf16 == out_bf16 && residual_stride != out_stride) return STRATA_ERR_INVALID_ARG;
   if (out_bf16 == x_bf16) return STRATA_ERR_INVALID_ARG;
-  if (!workspace || !on(workspace, kWsAlign) || ws_bytes < strata_linear_workspace_size(w, T))
-    return STRATA_ERR_WORKSPACE;
+  const LinearLayout L = linear_layout(w, T);
+  if (!workspace || !on(workspace, kWsAlign) || ws_bytes < L.total) return STRATA_ERR_WORKSPACE;
   LinearArgs a{};
   a.codes = w->codes;
   a.scales = static_cast<const __half*>(w->scales);
@@ -121,8 +133,16 @@ strata_status strata_linear_forward(const strata_linear* w, const void* x_bf16, 
   a.K = static_cast<int>(w->K);
   a.group = w->group_size == 0 ? STRATA_GROUP : w->group_size;
   a.bits = w->bits == 0 ? 4 : w->bits;
-  a.status = static_cast<uint32_t*>(workspace);
-  return of(launch_linear_stream(a, reinterpret_cast<cudaStream_t>(stream)));
+  char* base = static_cast<char*>(workspace);
+  a.status = &reinterpret_cast<WsHeader*>(base)->status;
+  a.xexp = reinterpret_cast<int*>(base + L.xexp);
+  a.xh = reinterpret_cast<__half*>(base + L.xh);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T <= kLinearStreamT) return of(launch_linear_stream(a, st));
+  if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st) != cudaSuccess) return STRATA_ERR_CUDA;
+  int sms = 0;
+  if (!sm_count(&sms)) return STRATA_ERR_CUDA;
+  return of(launch_linear_tc(a, sms, st));
 }
 
 strata_status strata_kv_append(const strata_kv_cache* cache, const void* q_bf16, int64_t q_stride,
