@@ -156,12 +156,24 @@ def ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None      # (device index) -> handle of torch's current stream, once CUDA is in use
+_current_device = None  # () -> device index
+
+
 def stream_handle(stream) -> int | None:
+    global _raw_stream, _current_device
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         try:
             import torch
             if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
+                h = torch.cuda.current_stream().cuda_stream
+                # the same lookup without building a Stream object: 0.3 us against 7 us a call
+                if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+                    _current_device = torch.cuda.current_device
+                    _raw_stream = torch._C._cuda_getCurrentRawStream
+                return h
         except Exception:  # pragma: no cover
             pass
         return None
