@@ -16,53 +16,18 @@
 // of the splits.
 #include <algorithm>
 
-#include "block.cuh"
+#include "attention.cuh"
 
 namespace strata {
 
 constexpr int kAttWarps = 8;
 constexpr int kAttStep = 32;  // tokens of one warp step
 
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(v)));
-  return d;
-}
 // Transposes an 8x8 matrix of 16-bit elements held one row per quad.
 __device__ __forceinline__ uint32_t movm_trans(uint32_t v) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The rows and tokens of one sequence, cut to the call's limits.
-struct SeqView {
-  int q0, n;  // first row, rows
-  int len;    // tokens in the cache
-};
-__device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s, bool flag) {
-  SeqView v;
-  int q0 = a.b.q_start[s], q1 = a.b.q_start[s + 1], len = a.b.kv_len[s];
-  const int T = static_cast<int>(a.b.T);
-  bool bad = q0 < 0 || q1 < q0 || q1 > T || len < 0 || len > a.b.max_kv;
-  q0 = min(max(q0, 0), T);
-  q1 = min(max(q1, q0), T);
-  bad |= q1 - q0 > a.b.max_q;
-  v.q0 = q0;
-  v.n = min(q1 - q0, a.b.max_q);
-  v.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), a.b.max_kv));
-  if (bad && flag) set_status(a.status, STRATA_DEV_BAD_SLOT);
-  return v;
 }
 
 template <int kD, int kNT>
@@ -80,7 +45,7 @@ __global__ void __launch_bounds__(kAttWarps * 32) attention_kernel(AttnArgs a) {
   const SeqView sv = seq_view(a, s, threadIdx.x == 0 && split == 0 && rb == 0 && h == 0);
   const int G = a.group, rows = sv.n * G;
   const int row0 = rb * COLS;
-  if (row0 >= rows) return;
+  if (rows > a.rows_above || row0 >= rows) return;
   const int last_row = min(row0 + COLS, rows) - 1;
   // positions of the block's first and last query, and the tokens any of them sees
   const int p_lo = sv.len - sv.n + row0 / G, p_hi = sv.len - sv.n + last_row / G;
@@ -431,9 +396,22 @@ __global__ void __launch_bounds__(kAttWarps * 32) attention_kernel(AttnArgs a) {
   }
 }
 
+// Rows of a sequence and K/V head up to which its cache is streamed through this kernel; more go to
+// the tensor-core kernel.
+constexpr int kAttStreamRows = 16;
+
 AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_heads) {
   AttnPlan p{};
-  const int64_t rows = static_cast<int64_t>(b.max_q) * (n_heads / c.n_kv_heads);
+  const int64_t G = n_heads / c.n_kv_heads, most_rows = b.max_q * G;
+  if (most_rows > kAttStreamRows) {
+    p.tc_blocks = static_cast<int>((most_rows + 255) / 256);
+    // sequences of equal length: none is below the limit
+    if (b.T == static_cast<int64_t>(b.n_seq) * b.max_q) return p;
+    p.stream_rows = kAttStreamRows;
+  } else {
+    p.stream_rows = 0x7FFFFFFF;
+  }
+  const int64_t rows = std::min<int64_t>(most_rows, kAttStreamRows);
   p.nt = rows <= 8 ? 1 : 2;
   p.row_blocks = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
   // enough blocks for four on each of 152 SMs, but no split shorter than 256 tokens

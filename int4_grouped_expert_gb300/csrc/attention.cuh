@@ -1,0 +1,45 @@
+// Device helpers shared by the attention kernels.
+#pragma once
+
+#include "block.cuh"
+
+namespace strata {
+
+// Two e4m3 codes (low byte first) as f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(v)));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The rows and tokens of one sequence, cut to the call's limits.
+struct SeqView {
+  int q0, n;  // first row, rows
+  int len;    // tokens in the cache
+};
+__device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s, bool flag) {
+  SeqView v;
+  int q0 = a.b.q_start[s], q1 = a.b.q_start[s + 1], len = a.b.kv_len[s];
+  const int T = static_cast<int>(a.b.T);
+  bool bad = q0 < 0 || q1 < q0 || q1 > T || len < 0 || len > a.b.max_kv;
+  q0 = min(max(q0, 0), T);
+  q1 = min(max(q1, q0), T);
+  bad |= q1 - q0 > a.b.max_q;
+  v.q0 = q0;
+  v.n = min(q1 - q0, a.b.max_q);
+  v.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), a.b.max_kv));
+  if (bad && flag) set_status(a.status, STRATA_DEV_BAD_SLOT);
+  return v;
+}
+
+}  // namespace strata

@@ -57,6 +57,8 @@ struct AttnArgs {
   int n_heads, group;     // query heads; query heads per K/V head
   float scale_log2;       // softmax scale * log2(e)
   int window;             // 0: none
+  int rows_above;         // attention.cu takes the sequences with at most so many rows per K/V head,
+  int rows_below;         // attention_tc.cu those with more
   int n_split;            // contraction splits of a (sequence, K/V head, row block)
   int split_tokens;       // tokens of one split
   int row_blocks;         // blocks of query rows per (sequence, K/V head)
@@ -69,8 +71,11 @@ struct AttnPlan {
   int nt;                 // 8-row tiles of query rows per block: 1 or 2
   int row_blocks, n_split, split_tokens;
   size_t part_floats, n_counters;
+  int stream_rows;        // rows up to which a sequence goes to attention.cu: 0 none, INT_MAX all
+  int tc_blocks;          // 256-row blocks of attention_tc.cu per (sequence, K/V head); 0: not launched
 };
 AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_heads);
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
+cudaError_t launch_attention_tc(const AttnArgs& a, int blocks, cudaStream_t stream);
 
 }  // namespace strata
