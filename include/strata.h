@@ -436,7 +436,8 @@ typedef struct {
   int32_t n_seq;            /* 0 .. 65535 */
   int32_t max_q;            /* at least the most query rows of one sequence */
   int64_t T;                /* rows of q and out, up to 2^22 */
-  int64_t max_kv;           /* at least the largest kv_len; up to table_stride * page_size */
+  int64_t max_kv;           /* at least the largest kv_len; up to table_stride * page_size;
+                               (max_kv / 32 + 1) * n_seq * n_kv_heads < 2^31 */
   const int32_t* q_start;   /* [n_seq + 1]: rows q_start[s] .. q_start[s+1] - 1 belong to sequence s */
   const int32_t* kv_len;    /* [n_seq]: tokens of the sequence in the cache, those of this call among them */
   const int32_t* page_table; /* [n_seq, table_stride]: the sequence's pages in order */

@@ -1,27 +1,39 @@
 // Causal attention over the paged cache of e4m3 codes with one scale per (page, K/V head):
 //   o_i = sum_j softmax_j(scale * q_i . k_j) v_j   over the tokens j that query i sees,
-// by one pass over the cache with the running maximum and sum of the softmax.
+// by one pass over the cache with a running reference and sum of the softmax.
 //
-// The rows of a K/V head (query rows x query heads that share it) are the N side of mma.sync
-// m16n8k16 and 16 tokens its M side: S^T = K Q^T, then O^T += V^T P^T. Codes go from global memory
-// straight into registers and become f16 there, exactly (cvt e4m3x2 -> f16x2): each lane takes 16
-// consecutive bytes of a K row (the order of the contraction over the head's elements is free) or of
-// V rows, whose bytes are paired token by token with PRMT. The products use f16 queries (exact from
-// bf16; rows of large entries are held times a power of two) and f16 probabilities (2^-11); sums, the
-// statistics and the scales of the pages are fp32.
+// For few query rows the cache is the traffic, so the kernel streams it: each warp copies its own
+// 32-token steps with cp.async into two private slots of shared memory (no block-wide waits) and
+// multiplies one while the other fills. Rows of a K/V head (query rows x query heads that share it) are
+// the N side of mma.sync m16n8k16 and 16 tokens its M side: S^T = K Q^T, then O^T += V^T P^T. Codes become
+// f16 in registers, exactly (cvt e4m3x2 -> f16x2). The order of the contraction over a head's elements
+// is free, so a lane takes 16 consecutive bytes of a K row; V bytes are paired token by token with
+// PRMT, and the weights turn from S^T's layout to P^T's with movmatrix.
 //
-// A block's 8 warps take alternate 32-token steps of its range of the cache and join their results in
-// shared memory. With few (sequence, head) pairs the cache is split over more blocks: each leaves
-// its maximum, sum and fp32 rows in the workspace, and the last to arrive joins them in the order
-// of the splits.
+// Queries are f16, exact from bf16 (rows are held times a power of two); weights are f16 (2^-11); sums,
+// statistics and scales are fp32. The reference that is subtracted in the exponent moves only when a
+// score exceeds it by 2^8: weights up to 2^8 are as exact in f16 and the sums fp32, and the common step
+// needs no reduction across lanes and no rescaling of O. A page's V scale, relative to the largest
+// that the warp has met, multiplies the weights.
+//
+// The work is cut by the lengths that the call finds on the device: a (sequence, K/V head) whose steps
+// exceed an even share of all steps is cut into equal pieces, and a block takes one piece. So the blocks
+// run in one wave where the batch allows it, whatever the mix of lengths. (Blocks that start in a
+// later wave cost the time to find their work, fill their slots and join: about 8 us a wave measured.)
+// A block's warps join their results in shared memory; pieces leave reference, sum and fp32 rows in the
+// workspace, the last piece to arrive in a group of up to 16 (or the root of the count) joins the group's,
+// and the last group the groups'. All sums are in the order of the pieces.
 #include <algorithm>
 
 #include "attention.cuh"
 
 namespace strata {
 
-constexpr int kAttWarps = 8;
+constexpr int kAttWarps = 4;
 constexpr int kAttStep = 32;  // tokens of one warp step
+constexpr int kAttSlots = 2;  // steps of a warp in shared memory
+constexpr int kAttMinSteps = 8;      // steps that a piece has at least: two a warp
+constexpr int kAttResident = 456;    // blocks that run at once: three on each of 152 SMs
 
 // Transposes an 8x8 matrix of 16-bit elements held one row per quad.
 __device__ __forceinline__ uint32_t movm_trans(uint32_t v) {
@@ -29,42 +41,178 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
 }
+// D += A * B, m16n8k16, f16 inputs, fp32 sums. (Not volatile: the compiler may interleave independent chains.)
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes to shared memory, or zeros when there is nothing to copy.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+// Which token of a 16-token tile is row i (< 8) of an MMA tile, and i + 8 the one 8 further: chosen with
+// the swizzle of the slots so that the lanes of a shared-memory phase read different banks, for K (rows i
+// of a quad pair) and for V (rows 2t of the quads) alike.
+template <int kD>
+__device__ __forceinline__ int tile_token(int i) {
+  // 128-wide: rows {0,4} {2,6} {5,1} {7,3}; 64-wide: {0,1} {3,2} {4,5} {7,6}
+  return (kD == 128 ? 0x37156240u : 0x67542310u) >> (4 * i) & 15;
+}
+// Byte offset of 16-byte piece c of token row r in a slot.
+template <int kD>
+__device__ __forceinline__ int slot_offset(int r, int c) {
+  return r * kD + ((c ^ (kD == 128 ? r & 7 : (r >> 1) & 2)) << 4);
+}
+
+// First step of 32 tokens that a sequence's rows see, and how many; none if this kernel skips it.
+struct SeqSteps {
+  int first, n;
+};
+__device__ __forceinline__ SeqSteps seq_steps(const AttnArgs& a, const SeqView& v) {
+  const int64_t rows = static_cast<int64_t>(v.n) * a.group;
+  if (rows == 0 || rows > a.rows_above) return {0, 0};
+  const int lo = a.window > 0 ? max(0, v.len - v.n - a.window + 1) / kAttStep : 0;
+  return {lo, max(1, (v.len + kAttStep - 1) / kAttStep - lo)};  // (no tokens: one empty step, zeros)
+}
+
+// This block's piece: found by a scan over the sequences, the same in every block.
+struct Piece {
+  int seq, head, index, of;  // piece `index` of `of`
+  int slot0;                 // workspace slot of the (sequence, head)'s piece 0, if of > 1
+};
+__device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
+  // every warp scans for itself: a lane takes consecutive sequences
+  const int lane = threadIdx.x & 31;
+  const int per_lane = (a.b.n_seq + 31) / 32;
+  const int s0 = min(a.b.n_seq, lane * per_lane), s1 = min(a.b.n_seq, s0 + per_lane);
+  const bool flag = blockIdx.x == 0 && threadIdx.x < 32;
+  int mine = 0;
+  for (int s = s0; s < s1; ++s) mine += seq_steps(a, seq_view(a, s, flag)).n;
+  const int kept = mine;  // per_lane == 1: the lane's steps
+  const int heads = a.c.n_kv_heads;
+  const unsigned total = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)) * heads;  // < 2^31 (host)
+  const int per = max(kAttMinSteps, static_cast<int>((total + a.pieces - 1) / a.pieces));
+  // blocks and workspace slots that a sequence's steps come to
+  auto count = [&](int steps, int& blocks, int& slots) {
+    const int k = (steps + per - 1) / per * heads;
+    blocks += k;
+    slots += k > heads ? k : 0;
+  };
+  int blocks = 0, slots = 0;
+  for (int s = s0; s < s1; ++s) count(per_lane == 1 ? kept : seq_steps(a, seq_view(a, s, false)).n, blocks, slots);
+  int b_at = blocks, s_at = slots;  // inclusive scans
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, b_at, d), y = __shfl_up_sync(0xffffffffu, s_at, d);
+    if (lane >= d) b_at += x, s_at += y;
+  }
+  const int id = blockIdx.x;
+  const unsigned here = __ballot_sync(0xffffffffu, id < b_at);
+  if (here == 0) return false;
+  const int owner = __ffs(here) - 1;
+  int seq = 0, local = 0, k = 1, slot0 = 0;
+  if (lane == owner) {
+    int b0 = b_at - blocks, l0 = s_at - slots;
+    for (int s = s0; s < s1; ++s) {
+      const int steps = per_lane == 1 ? kept : seq_steps(a, seq_view(a, s, false)).n;
+      int nb = 0, ns = 0;
+      count(steps, nb, ns);
+      if (id < b0 + nb) {
+        seq = s;
+        local = id - b0;
+        k = (steps + per - 1) / per;
+        slot0 = l0;
+        break;
+      }
+      b0 += nb;
+      l0 += ns;
+    }
+  }
+  seq = __shfl_sync(0xffffffffu, seq, owner);
+  local = __shfl_sync(0xffffffffu, local, owner);
+  k = __shfl_sync(0xffffffffu, k, owner);
+  slot0 = __shfl_sync(0xffffffffu, slot0, owner);
+  p = {seq, local / k, local % k, k, slot0 + local / k * k};
+  return true;
+}
 
 template <int kD, int kNT>
-__global__ void __launch_bounds__(kAttWarps * 32) attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a) {
   constexpr int COLS = 8 * kNT;
   constexpr int KW = kD / 64;       // 16-byte pieces of a K row per lane
-  constexpr int VB = kD / 8;        // bytes of a V row per lane: 16 or 8
-  constexpr int VW = VB / 4;        // words of them
+  constexpr int VW = kD / 32;       // words of a V row per lane
   constexpr int NJ = 2 * VW;        // output MMAs per token tile
-  extern __shared__ float att_smem[];
+  constexpr int KB = kAttStep * kD; // bytes of a step's K (and V)
+  constexpr float kLag = 8.0f;      // how far a score may exceed the reference (log2)
+  extern __shared__ __align__(1024) uint8_t att_smem[];
   griddep_wait();
+  griddep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x % a.n_split, rb = blockIdx.x / a.n_split;
-  const int h = blockIdx.y, s = blockIdx.z;
-  const SeqView sv = seq_view(a, s, threadIdx.x == 0 && split == 0 && rb == 0 && h == 0);
-  const int G = a.group, rows = sv.n * G;
-  const int row0 = rb * COLS;
-  if (rows > a.rows_above || row0 >= rows) return;
-  const int last_row = min(row0 + COLS, rows) - 1;
-  // positions of the block's first and last query, and the tokens any of them sees
-  const int p_lo = sv.len - sv.n + row0 / G, p_hi = sv.len - sv.n + last_row / G;
-  const int tok_hi = min(sv.len, p_hi + 1);
-  const int tok_lo = a.window > 0 ? max(0, p_lo - a.window + 1) : 0;
-  const int first = tok_lo / a.split_tokens;
-  const int last = tok_hi > tok_lo ? (tok_hi - 1) / a.split_tokens : first;  // splits with tokens
-  if (split < first || split > last) return;
-  const int n_here = last - first + 1;
-  const int lo = max(tok_lo, split * a.split_tokens) / kAttStep * kAttStep;
-  const int hi = min(tok_hi, (split + 1) * a.split_tokens);
+  Piece pc;
+  if (!find_piece(a, pc)) return;
+  const int h = pc.head, s = pc.seq;
+  const SeqView sv = seq_view(a, s, false);
+  const SeqSteps st = seq_steps(a, sv);
+  const int G = a.group, rows = sv.n * G;  // <= COLS
+  // positions of the first and last query; the tokens of the piece
+  const int p_lo = sv.len - sv.n, p_hi = sv.len - 1;
+  const int lo = (st.first + static_cast<int>(static_cast<int64_t>(st.n) * pc.index / pc.of)) * kAttStep;
+  const int hi = min(sv.len, (st.first + static_cast<int>(static_cast<int64_t>(st.n) * (pc.index + 1) / pc.of)) * kAttStep);
 
-  // the queries of column g of each tile as f16 B fragments, times 2^-e
+  // ---- copies: a lane moves piece lane % PIECES of rows lane / PIECES, + 32 / PIECES, ...
+  constexpr int PIECES = kD / 16, RPI = 32 / PIECES, NI = kAttStep / RPI;
+  const int pshift = 31 - __clz(a.c.page_size), pmask = a.c.page_size - 1;
+  const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
+  uint8_t* ring = att_smem + warp * (kAttSlots * 2 * KB);
+  const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  float ks[kAttSlots][2], vs[kAttSlots][2];
+  int gone[kAttSlots];  // bit u: tile u of the step lies in a page that does not exist
+  auto issue = [&](int j0, float (&k_scale)[2], float (&v_scale)[2], int& lost, uint32_t slot) {
+    lost = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = j0 + 16 * u;
+      int page = -1;
+      if (j < hi) {
+        page = table[j >> pshift];
+        if (page < 0 || page >= a.c.n_pages) {
+          if (lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
+          page = -1;
+          lost |= 1 << u;
+        }
+      }
+      const int64_t ph = page < 0 ? 0 : static_cast<int64_t>(page) * a.c.n_kv_heads + h;
+      k_scale[u] = page < 0 ? 0.f : a.c.k_scales[ph];
+      v_scale[u] = page < 0 ? 0.f : a.c.v_scales[ph];
+      const int64_t base = ((ph << pshift) + (j & pmask)) * kD + lane * 16;
+      const int n = page < 0 ? 0 : hi - j;  // tokens of the tile from here on; past them: zeros
+#pragma unroll
+      for (int i = 0; i < NI / 2; ++i) {
+        const int r = lane / PIECES + RPI * i;
+        const uint32_t dst = slot + slot_offset<kD>(16 * u + r, lane % PIECES);
+        const int64_t at = r < n ? base + i * 512 : 0;
+        copy16(dst, a.c.k_codes + at, r < n);
+        copy16(dst + KB, a.c.v_codes + at, r < n);
+      }
+    }
+  };
+  int j_next = lo + warp * kAttStep;
+#pragma unroll
+  for (int i = 0; i < kAttSlots; ++i) {
+    if (j_next < hi) issue(j_next, ks[i], vs[i], gone[i], ring_addr + i * 2 * KB);
+    cp_async_commit();
+    j_next += kAttWarps * kAttStep;
+  }
+
+  // ---- the queries of column g of each tile as f16 B fragments, times 2^-e
   uint32_t qf[kNT][4 * KW][2];
   float cmul[kNT][2];   // columns 2t, 2t+1: what turns a product into the exponent of 2
   int pos[kNT][2];      // their positions
 #pragma unroll
   for (int n = 0; n < kNT; ++n) {
-    const int r = row0 + n * 8 + g;
+    const int r = n * 8 + g;
     uint4 v[2 * KW];
     uint32_t mag = 0;
 #pragma unroll
@@ -92,72 +240,37 @@ __global__ void __launch_bounds__(kAttWarps * 32) attention_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       cmul[n][i] = __shfl_sync(0xffffffffu, m, (2 * t + i) * 4);
-      pos[n][i] = sv.len - sv.n + (row0 + n * 8 + 2 * t + i) / G;
+      pos[n][i] = sv.len - sv.n + (n * 8 + 2 * t + i) / G;
     }
   }
 
   float o[kNT][NJ][4];
-  float mx[kNT][2], sum[kNT][2];
+  // ref: the reference in use, or 0 before any score; limit: how much of a score above it moves it
+  float ref[kNT][2], limit[kNT][2], sum[kNT][2];
+  float v_ref = 1.17549435e-38f, v_inv = 8.50705917e37f;  // largest V scale met, and its inverse
 #pragma unroll
   for (int n = 0; n < kNT; ++n) {
-    mx[n][0] = mx[n][1] = -INFINITY;
+    ref[n][0] = ref[n][1] = 0.f;
+    limit[n][0] = limit[n][1] = -INFINITY;
     sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
   }
+  const int tok_g = tile_token<kD>(g);
+  // addresses of this lane's K rows and V rows in a slot, 16 tokens apart for the second tile
+  int k_at[KW], v_at[2];
+#pragma unroll
+  for (int w = 0; w < KW; ++w) k_at[w] = slot_offset<kD>(tok_g, t + 4 * w);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = tile_token<kD>(2 * t + i);
+    v_at[i] = KB + (kD == 128 ? slot_offset<kD>(r, g) : slot_offset<kD>(r, g >> 1) + (g & 1) * 8);
+  }
 
-  const int P = a.c.page_size;
-  const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
-  for (int j0 = lo + warp * kAttStep; j0 < hi; j0 += kAttWarps * kAttStep) {
-    // two tiles of 16 tokens, each within one page
-    uint4 kr[2][2][KW];
-    uint32_t vr[2][4][VW];
-    float ks[2], vs[2];
-    int end[2];  // tokens of the tile that may be read
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int j = j0 + 16 * u;
-      int64_t page = -1;
-      end[u] = 0;
-      if (j < hi) {
-        page = table[j / P];
-        if (page >= 0 && page < a.c.n_pages) end[u] = min(16, sv.len - j);
-        else if (lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
-      }
-      const bool on = end[u] > 0;
-      const int64_t ph = on ? page * a.c.n_kv_heads + h : 0;
-      const int64_t base = (ph * P + j % P) * kD;
-      ks[u] = on ? a.c.k_scales[ph] : 0.f;
-      vs[u] = on ? a.c.v_scales[ph] : 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          kr[u][i][w] = make_uint4(0u, 0u, 0u, 0u);
-          if (g + 8 * i < end[u])
-            kr[u][i][w] = __ldcg(reinterpret_cast<const uint4*>(a.c.k_codes + base + (g + 8 * i) * kD + t * 16 + w * 64));
-        }
-      // V rows past the end are zero, whatever the cache holds there
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * t + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-        for (int w = 0; w < VW; ++w) vr[u][i][w] = 0u;
-        if (r < end[u]) {
-          const uint8_t* p = a.c.v_codes + base + r * kD + g * VB;
-          if (VB == 16) {
-            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
-            vr[u][i][0] = v.x; vr[u][i][1] = v.y; vr[u][i][VW - 2] = v.z; vr[u][i][VW - 1] = v.w;
-          } else {
-            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
-            vr[u][i][0] = v.x; vr[u][i][1] = v.y;
-          }
-        }
-      }
-    }
-    // S^T: tokens g, g + 8 of each tile x columns 2t, 2t+1
+  auto step = [&](int j0, const float (&k_scale)[2], const float (&v_scale)[2], int lost, const uint8_t* slot) {
+    // S^T: tokens tok_g, tok_g + 8 of each tile x columns 2t, 2t+1
     float sc[kNT][2][4];
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
@@ -166,101 +279,146 @@ __global__ void __launch_bounds__(kAttWarps * 32) attention_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[n][u][i] = 0.f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int w = 0; w < KW; ++w) {
+      uint32_t w0[2][4], w1[2][4];
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const uint32_t w0[4] = {kr[u][0][w].x, kr[u][0][w].y, kr[u][0][w].z, kr[u][0][w].w};
-        const uint32_t w1[4] = {kr[u][1][w].x, kr[u][1][w].y, kr[u][1][w].z, kr[u][1][w].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t A[4] = {e4m3x2_f16x2(w0[j]), e4m3x2_f16x2(w1[j]), e4m3x2_f16x2(w0[j] >> 16),
-                                 e4m3x2_f16x2(w1[j] >> 16)};
-#pragma unroll
-          for (int n = 0; n < kNT; ++n)
-            mma_f16_16816(sc[n][u], A, qf[n][4 * w + j][0], qf[n][4 * w + j][1], sc[n][u]);
-        }
+      for (int u = 0; u < 2; ++u) {
+        // (8 and 16 rows further the swizzle is the same)
+        const uint4 x = *reinterpret_cast<const uint4*>(slot + k_at[w] + 16 * u * kD);
+        const uint4 y = *reinterpret_cast<const uint4*>(slot + k_at[w] + (16 * u + 8) * kD);
+        w0[u][0] = x.x; w0[u][1] = x.y; w0[u][2] = x.z; w0[u][3] = x.w;
+        w1[u][0] = y.x; w1[u][1] = y.y; w1[u][2] = y.z; w1[u][3] = y.w;
       }
-    // exponents, masked to -inf, and the new maxima
-    const bool whole = j0 >= (a.window > 0 ? p_hi - a.window + 1 : 0) && j0 + kAttStep - 1 <= p_lo &&
-                       j0 + kAttStep <= sv.len && end[0] == 16 && end[1] == 16;
-    float corr[kNT][2];
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      float top[2] = {-INFINITY, -INFINITY};
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t A[4] = {e4m3x2_f16x2(w0[u][j]), e4m3x2_f16x2(w1[u][j]), e4m3x2_f16x2(w0[u][j] >> 16),
+                                 e4m3x2_f16x2(w1[u][j] >> 16)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = i & 1, r = g + 8 * (i >> 1);
-          float v = sc[n][u][i] * (cmul[n][c] * ks[u]);
-          if (!whole) {
-            const int j = j0 + 16 * u + r;
-            const bool seen = r < end[u] && j <= pos[n][c] && (a.window <= 0 || j > pos[n][c] - a.window);
-            if (!seen) v = -INFINITY;
-          }
-          sc[n][u][i] = v;
-          // a nan has to reach the sum, so it must not be lost in the maximum: exp2(nan - m) is nan
-          top[c] = fmaxf(top[c], v);
+          for (int n = 0; n < kNT; ++n) mma_add(sc[n][u], A, qf[n][4 * w + j][0], qf[n][4 * w + j][1]);
         }
+    }
+    const bool whole = j0 >= (a.window > 0 ? p_hi - a.window + 1 : 0) && j0 + kAttStep - 1 <= p_lo &&
+                       j0 + kAttStep <= hi && !lost;
+    // exponents relative to the reference (in use or 0)
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 4));
-        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 8));
-        top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], 16));
-        const float m = fmaxf(mx[n][c], top[c]);
-        // a column that has seen nothing yet keeps 0: its sums are zero, and so is exp2(-inf - 0)
-        const float ref = m == -INFINITY ? 0.f : m;
-        corr[n][c] = exp2_approx(mx[n][c] - ref);
-        mx[n][c] = m;
-        float add = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          const float f = cmul[n][c] * k_scale[u];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p = exp2_approx(sc[n][u][2 * i + c] - ref);
-            sc[n][u][2 * i + c] = p;
-            add += p;
+            float x = fmaf(sc[n][u][2 * i + c], f, -ref[n][c]);
+            if (!whole) {
+              const int r = tok_g + 8 * i, j = j0 + 16 * u + r;
+              const bool seen = j < hi && j <= pos[n][c] && (a.window <= 0 || j > pos[n][c] - a.window) &&
+                                !(lost >> u & 1);
+              if (!seen) x = -INFINITY;
+            }
+            sc[n][u][2 * i + c] = x;
+            over |= x > limit[n][c];
           }
-        sum[n][c] = fmaf(sum[n][c], corr[n][c], add);
+        }
       }
+    if (__any_sync(0xffffffffu, over)) {  // some column's reference moves to its largest score so far
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        o[n][j][0] *= corr[n][0]; o[n][j][1] *= corr[n][1];
-        o[n][j][2] *= corr[n][0]; o[n][j][3] *= corr[n][1];
-      }
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float up = fmaxf(fmaxf(sc[n][0][c], sc[n][0][2 + c]), fmaxf(sc[n][1][c], sc[n][1][2 + c]));
+          up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+          up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+          up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
+          const bool had = limit[n][c] == kLag;
+          if (had) up = fmaxf(up, 0.f);   // a reference never falls
+          if (up == -INFINITY) up = 0.f;  // nothing seen yet
+          else limit[n][c] = kLag;
+          ref[n][c] += up;
+          const float f = had ? exp2_approx(-up) : 1.f;  // (without a reference the sums are 0, or nan)
+          sum[n][c] *= f;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            o[n][j][c] *= f;
+            o[n][j][2 + c] *= f;
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            sc[n][u][c] -= up;
+            sc[n][u][2 + c] -= up;
+          }
+        }
     }
     // O^T += vs * V^T P^T, tile by tile (the scale is the page's)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      if (v_scale[u] > v_ref) {
+        const float f = v_ref / v_scale[u];
+        v_ref = v_scale[u];
+        v_inv = 1.0f / v_ref;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
+      }
+      const float vf = v_scale[u] * v_inv;
       uint32_t pf[kNT][2];
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        pf[n][0] = movm_trans(pack_f16x2(sc[n][u][0], sc[n][u][1]));
-        pf[n][1] = movm_trans(pack_f16x2(sc[n][u][2], sc[n][u][3]));
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = exp2_approx(sc[n][u][i]);
+        sum[n][0] += p[0] + p[2];
+        sum[n][1] += p[1] + p[3];
+        pf[n][0] = movm_trans(pack_f16x2(p[0] * vf, p[1] * vf));
+        pf[n][1] = movm_trans(pack_f16x2(p[2] * vf, p[3] * vf));
+      }
+      uint32_t vr[4][VW];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the MMA's order
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* at = slot + v_at[i & 1] + (16 * u + 8 * (i >> 1)) * kD;
+        if (kD == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(at);
+          vr[i][0] = v.x; vr[i][1] = v.y; vr[i][VW - 2] = v.z; vr[i][VW - 1] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(at);
+          vr[i][0] = v.x; vr[i][1] = v.y;
+        }
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;  // bytes 0,1 or 2,3 of two tokens' words
-        const uint32_t x0 = prmt(vr[u][0][j >> 1], vr[u][1][j >> 1], sel);
-        const uint32_t x1 = prmt(vr[u][2][j >> 1], vr[u][3][j >> 1], sel);
+        const uint32_t x0 = prmt(vr[0][j >> 1], vr[1][j >> 1], sel);
+        const uint32_t x1 = prmt(vr[2][j >> 1], vr[3][j >> 1], sel);
         const uint32_t A[4] = {e4m3x2_f16x2(x0), e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1),
                                e4m3x2_f16x2(x1 >> 16)};
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16_16816(d, A, pf[n][0], pf[n][1], d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][j][i] = fmaf(vs[u], d[i], o[n][j][i]);
-        }
+        for (int n = 0; n < kNT; ++n) mma_add(o[n][j], A, pf[n][0], pf[n][1]);
       }
+    }
+  };
+  for (int j0 = lo + warp * kAttStep; j0 < hi;) {
+#pragma unroll
+    for (int i = 0; i < kAttSlots; ++i) {
+      if (j0 >= hi) break;
+      cp_async_wait<kAttSlots - 1>();
+      __syncwarp();
+      step(j0, ks[i], vs[i], gone[i], ring + i * 2 * KB);
+      __syncwarp();  // every lane has read the slot
+      if (j_next < hi) issue(j_next, ks[i], vs[i], gone[i], ring_addr + i * 2 * KB);
+      cp_async_commit();
+      j_next += kAttWarps * kAttStep;
+      j0 += kAttWarps * kAttStep;
     }
   }
 
-  // join the warps: the common maximum of a column, then the sums pairwise, in a fixed order
-  float* s_mx = att_smem;                        // [kAttWarps][COLS]
-  float* s_sum = s_mx + kAttWarps * COLS;        // [kAttWarps][COLS]
-  float* s_o = s_sum + kAttWarps * COLS;         // [kAttWarps / 2][32 lanes][kNT * NJ * 4 + pad]
-  constexpr int OL = kNT * NJ * 4;
+  // ---- join the warps: every column to the largest reference, then the sums in the warps' order
+  __shared__ float s_ref[kAttWarps][COLS], s_sum[kAttWarps][COLS];
 #pragma unroll
   for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -270,130 +428,145 @@ __global__ void __launch_bounds__(kAttWarps * 32) attention_kernel(AttnArgs a) {
       v += __shfl_xor_sync(0xffffffffu, v, 8);
       v += __shfl_xor_sync(0xffffffffu, v, 16);
       if (g == 0) {
-        s_mx[warp * COLS + n * 8 + 2 * t + c] = mx[n][c];
-        s_sum[warp * COLS + n * 8 + 2 * t + c] = v;
+        // (a column that has seen nothing but nan keeps its sum: nan)
+        s_ref[warp][n * 8 + 2 * t + c] = limit[n][c] == kLag ? ref[n][c] : -INFINITY;
+        s_sum[warp][n * 8 + 2 * t + c] = v;
       }
     }
-  __syncthreads();
-  float m_all[kNT][2], l_all[kNT][2];
+  cp_async_wait<0>();
+  __syncthreads();  // (and every warp is done with its slots)
+  float* s_o = reinterpret_cast<float*>(att_smem);  // [kAttWarps][COLS][kD + 4]
+  constexpr int OS = kD + 4;
 #pragma unroll
   for (int n = 0; n < kNT; ++n)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int col = n * 8 + 2 * t + c;
-      float m = -INFINITY;
+      float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) m = fmaxf(m, s_mx[w * COLS + col]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      float l = 0.f;
+      for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
+      const float f = (top == -INFINITY ? 1.f : exp2_approx(s_ref[warp][col] - top)) * v_ref;
+      float* dst = s_o + (warp * COLS + col) * OS + g * (4 * VW);
 #pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) l += s_sum[w * COLS + col] * exp2_approx(s_mx[w * COLS + col] - ref);
-      m_all[n][c] = m;
-      l_all[n][c] = l;
-      const float f = exp2_approx(mx[n][c] - ref);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        o[n][j][c] *= f;
-        o[n][j][2 + c] *= f;
-      }
+      for (int j = 0; j < NJ; ++j)
+        *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[n][j][c] * f, o[n][j][2 + c] * f);
     }
+  __syncthreads();
+  auto write = [&](int r, int e, const float (&y)[4], float l) {
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const __nv_bfloat162 b0 = __floats2bfloat162_rn(y[0] * inv, y[1] * inv);
+    const __nv_bfloat162 b1 = __floats2bfloat162_rn(y[2] * inv, y[3] * inv);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t*>(&b0);
+    w.y = *reinterpret_cast<const uint32_t*>(&b1);
+    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(sv.q0 + r / G) * a.out_stride + (h * G + r % G) * kD + e) = w;
+  };
+  // four elements of one column per thread
+  constexpr int64_t PART = COLS * (kD + 2);  // floats of a slot: rows, then (reference, sum) per column
+  float* part = a.part + (pc.slot0 + pc.index) * PART;
+  for (int i = threadIdx.x; i < rows * kD / 4; i += kAttWarps * 32) {
+    const int col = i / (kD / 4), e = i % (kD / 4) * 4;
+    float top = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int half = kAttWarps / 2; half > 0; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-      float* dst = s_o + (warp - half) * OL * 32 + lane;
+    for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[((n * NJ + j) * 4 + i) * 32] = o[n][j][i];
+    for (int w = 0; w < kAttWarps; ++w) {
+      l = fmaf(s_sum[w][col], top == -INFINITY ? 1.f : exp2_approx(s_ref[w][col] - top), l);
+      const float4 v = *reinterpret_cast<const float4*>(s_o + (w * COLS + col) * OS + e);
+      y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
     }
-    __syncthreads();
-    if (warp < half) {
-      const float* src = s_o + warp * OL * 32 + lane;
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][j][i] += src[((n * NJ + j) * 4 + i) * 32];
+    if (pc.of == 1) {
+      write(col, e, y, l);
+    } else {
+      *reinterpret_cast<float4*>(part + col * kD + e) = make_float4(y[0], y[1], y[2], y[3]);
+      if (e == 0) *reinterpret_cast<float2*>(part + COLS * kD + 2 * col) = make_float2(top, l);
     }
-    __syncthreads();
   }
+  if (pc.of == 1) return;
 
-  const int64_t slot = (static_cast<int64_t>(s) * a.c.n_kv_heads + h) * a.row_blocks + rb;
-  if (n_here > 1) {
-    // leave (o, maximum, sum) in the workspace; the last split to arrive joins them all
-    float* part = a.part + (slot * a.n_split + split) * (COLS * (kD + 2));
-    if (warp == 0) {
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col = n * 8 + 2 * t + c;
-          float* dst = part + col * kD + g * VB;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[n][j][c], o[n][j][2 + c]);
-          if (g == 0) {
-            part[COLS * kD + 2 * col] = m_all[n][c];
-            part[COLS * kD + 2 * col + 1] = l_all[n][c];
-          }
-        }
+  // ---- pieces meet in groups, then the groups
+  __shared__ int s_last;
+  // true in the last of n blocks to arrive at a counter, with what the others wrote visible
+  auto arrive_last = [&](uint32_t* counter, int n) {
+    __syncthreads();
+    if (threadIdx.x == 0) {  // wraps to zero at the last arrival: ready for the next call
+      uint32_t old;
+      asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(n - 1) : "memory");
+      s_last = old == static_cast<uint32_t>(n - 1);
     }
-    __threadfence();
-    __shared__ int s_last;
     __syncthreads();
-    if (threadIdx.x == 0)  // wraps to zero at the last arrival: ready for the next call
-      s_last = atomicInc(a.counters + slot, n_here - 1) == static_cast<unsigned>(n_here - 1);
+    return s_last != 0;
+  };
+  // joins n slots, `step` apart from slot `from` on, into that slot, or into the output
+  float* s_w = s_o;  // [n][COLS]
+  auto join = [&](int from, int n, int step, bool final) {
+    float* base = a.part + from * PART;
+    const int64_t stride = step * PART;
+    constexpr int U = 16;  // loads in flight per thread
+    float4 v[U];
+    auto load = [&](int i, int k0) {
+      const float* src = base + i / (kD / 4) * kD + i % (kD / 4) * 4;
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        v[k] = k0 + k < n ? __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (threadIdx.x < rows * kD / 4) load(threadIdx.x, 0);
+    for (int i = threadIdx.x; i < n * COLS; i += kAttWarps * 32) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + i / COLS * stride + COLS * kD + 2 * (i % COLS)));
+      s_w[2 * i] = ml.x;
+      s_w[2 * i + 1] = ml.y;
+    }
     __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const float* base = a.part + (slot * a.n_split + first) * (COLS * (kD + 2));
-    const int64_t stride = static_cast<int64_t>(COLS) * (kD + 2);
-    // four elements of one column per thread
-    for (int i = threadIdx.x; i < COLS * kD / 4; i += kAttWarps * 32) {
-      const int col = i / (kD / 4), e = i % (kD / 4) * 4, r = row0 + col;
-      if (r >= rows) continue;
-      float m = -INFINITY;
-      for (int k = 0; k < n_here; ++k) m = fmaxf(m, __ldcg(base + k * stride + COLS * kD + 2 * col));
-      const float ref = m == -INFINITY ? 0.f : m;
-      float l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < n_here; ++k) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + k * stride + COLS * kD + 2 * col));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(base + k * stride + col * kD + e));
-        const float f = exp2_approx(ml.x - ref);
-        l = fmaf(ml.y, f, l);
-        y[0] = fmaf(v.x, f, y[0]); y[1] = fmaf(v.y, f, y[1]);
-        y[2] = fmaf(v.z, f, y[2]); y[3] = fmaf(v.w, f, y[3]);
+    for (int col = warp; col < rows; col += kAttWarps) {
+      float top = -INFINITY, l = 0.f;
+      for (int k = lane; k < n; k += 32) top = fmaxf(top, s_w[2 * (k * COLS + col)]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      for (int k = lane; k < n; k += 32) {
+        const float f = top == -INFINITY ? 1.f : exp2_approx(s_w[2 * (k * COLS + col)] - top);
+        s_w[2 * (k * COLS + col)] = f;
+        l = fmaf(s_w[2 * (k * COLS + col) + 1], f, l);
       }
-      const float inv = l == 0.f ? 0.f : 1.0f / l;
-      const __nv_bfloat162 b0 = __floats2bfloat162_rn(y[0] * inv, y[1] * inv);
-      const __nv_bfloat162 b1 = __floats2bfloat162_rn(y[2] * inv, y[3] * inv);
-      uint2 w;
-      w.x = *reinterpret_cast<const uint32_t*>(&b0);
-      w.y = *reinterpret_cast<const uint32_t*>(&b1);
-      *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(sv.q0 + r / G) * a.out_stride +
-                                (h * G + r % G) * kD + e) = w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (lane == 0) {
+        s_sum[0][col] = l;
+        s_ref[0][col] = top;
+      }
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * kD / 4; i += kAttWarps * 32) {
+      const int col = i / (kD / 4), e = i % (kD / 4) * 4;
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k0 = 0; k0 < n; k0 += U) {
+        if (i != threadIdx.x || k0) load(i, k0);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float f = k0 + k < n ? s_w[2 * ((k0 + k) * COLS + col)] : 0.f;
+          y[0] = fmaf(v[k].x, f, y[0]); y[1] = fmaf(v[k].y, f, y[1]);
+          y[2] = fmaf(v[k].z, f, y[2]); y[3] = fmaf(v[k].w, f, y[3]);
+        }
+      }
+      if (final) {
+        write(col, e, y, s_sum[0][col]);
+      } else {  // (this thread has read these elements of the slot)
+        *reinterpret_cast<float4*>(base + col * kD + e) = make_float4(y[0], y[1], y[2], y[3]);
+        if (e == 0)
+          *reinterpret_cast<float2*>(base + COLS * kD + 2 * col) = make_float2(s_ref[0][col], s_sum[0][col]);
+      }
+    }
+  };
+  int gs = min(16, pc.of);
+  while (gs * gs < pc.of) ++gs;
+  const int groups = (pc.of + gs - 1) / gs, gi = pc.index / gs, g0 = gi * gs, gn = min(gs, pc.of - g0);
+  if (!arrive_last(a.counters + pc.slot0 + g0, gn)) return;
+  if (groups == 1) {
+    join(pc.slot0, pc.of, 1, true);
     return;
   }
-  if (warp == 0) {
-#pragma unroll
-    for (int n = 0; n < kNT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = row0 + n * 8 + 2 * t + c;
-        if (r >= rows) continue;
-        const float inv = l_all[n][c] == 0.f ? 0.f : 1.0f / l_all[n][c];
-        __nv_bfloat16* dst = a.out + static_cast<int64_t>(sv.q0 + r / G) * a.out_stride +
-                             (h * G + r % G) * kD + g * VB;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          *reinterpret_cast<__nv_bfloat162*>(dst + 2 * j) =
-              __floats2bfloat162_rn(o[n][j][c] * inv, o[n][j][2 + c] * inv);
-      }
-  }
+  join(pc.slot0 + g0, gn, 1, false);
+  // (the second counter of piece 0's slot counts the groups)
+  if (arrive_last(a.counters + a.n_slots + pc.slot0, groups)) join(pc.slot0, groups, gs, true);
 }
 
 // Rows of a sequence and K/V head up to which its cache is streamed through this kernel; more go to
@@ -411,40 +584,35 @@ AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_hea
   } else {
     p.stream_rows = 0x7FFFFFFF;
   }
-  const int64_t rows = std::min<int64_t>(most_rows, kAttStreamRows);
-  p.nt = rows <= 8 ? 1 : 2;
-  p.row_blocks = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
-  // enough blocks for four on each of 152 SMs, but no split shorter than 256 tokens
-  const int64_t blocks = std::max<int64_t>(1, static_cast<int64_t>(p.row_blocks) * c.n_kv_heads * b.n_seq);
-  const int64_t unit = kAttWarps * kAttStep;
-  const int64_t most = std::max<int64_t>(1, (b.max_kv + unit - 1) / unit);
-  const int64_t want = std::min(most, (4 * 152 + blocks - 1) / blocks);
-  const int64_t per = (most + want - 1) / want;
-  p.split_tokens = static_cast<int>(per * unit);
-  p.n_split = static_cast<int>((most + per - 1) / per);
-  if (p.n_split > 1) {
-    p.n_counters = static_cast<size_t>(blocks);
-    p.part_floats = static_cast<size_t>(blocks) * p.n_split * (8 * p.nt) * (c.head_dim + 2);
-  }
+  p.nt = std::min<int64_t>(most_rows, kAttStreamRows) <= 8 ? 1 : 2;
+  // An even share of the steps for each resident block, less half a block per (sequence, head), which
+  // rounding the pieces up adds; with many pairs, several waves of smaller pieces, which end evenly.
+  const int64_t heads = static_cast<int64_t>(c.n_kv_heads) * b.n_seq;
+  p.pieces = static_cast<int>(heads <= kAttResident / 2 ? kAttResident - heads / 2 : 3 * kAttResident);
+  p.grid = heads + p.pieces;               // sum of ceil(x) <= n + sum of x
+  p.n_slots = 2 * p.pieces;                // where x > 1, ceil(x) <= 2 x
+  const int64_t most_pieces = (b.max_kv + kAttStep * kAttMinSteps - 1) / (kAttStep * kAttMinSteps) + 1;
+  if (most_pieces * heads < p.grid) p.grid = most_pieces * heads;
+  p.part_floats = static_cast<size_t>(p.n_slots) * (8 * p.nt) * (c.head_dim + 2);
   return p;
 }
 
 template <int kD, int kNT>
-static cudaError_t launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(float) * (2 * kAttWarps * 8 * kNT + kAttWarps / 2 * 32 * kNT * (kD / 16) * 4);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(attention_kernel<kD, kNT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  const dim3 grid(static_cast<unsigned>(a.n_split * a.row_blocks), a.c.n_kv_heads, a.b.n_seq);
-  return launch_kernel(attention_kernel<kD, kNT>, grid, dim3(kAttWarps * 32), smem, stream, true, a);
+static cudaError_t launch_attention_t(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
+  constexpr size_t slots = static_cast<size_t>(kAttWarps) * kAttSlots * 2 * kAttStep * kD;
+  constexpr size_t join = sizeof(float) * kAttWarps * 8 * kNT * (kD + 4);
+  constexpr size_t smem = slots > join ? slots : join;
+  const cudaError_t e = cudaFuncSetAttribute(attention_kernel<kD, kNT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(attention_kernel<kD, kNT>, dim3(static_cast<unsigned>(grid)), dim3(kAttWarps * 32), smem, stream,
+                       true, a);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream) {
   if (a.c.head_dim == 64)
-    return p.nt == 1 ? launch_attention_t<64, 1>(a, stream) : launch_attention_t<64, 2>(a, stream);
-  return p.nt == 1 ? launch_attention_t<128, 1>(a, stream) : launch_attention_t<128, 2>(a, stream);
+    return p.nt == 1 ? launch_attention_t<64, 1>(a, p.grid, stream) : launch_attention_t<64, 2>(a, p.grid, stream);
+  return p.nt == 1 ? launch_attention_t<128, 1>(a, p.grid, stream) : launch_attention_t<128, 2>(a, p.grid, stream);
 }
 
 }  // namespace strata

@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   griddep_wait();
+  griddep_launch();
   const int h = blockIdx.y, s = blockIdx.z;
   const SeqView sv = seq_view(a, s, threadIdx.x == 0 && blockIdx.x == 0 && h == 0);
   const int G = a.group, rows = sv.n * G;

@@ -59,18 +59,19 @@ struct AttnArgs {
   int window;             // 0: none
   int rows_above;         // attention.cu takes the sequences with at most so many rows per K/V head,
   int rows_below;         // attention_tc.cu those with more
-  int n_split;            // contraction splits of a (sequence, K/V head, row block)
-  int split_tokens;       // tokens of one split
-  int row_blocks;         // blocks of query rows per (sequence, K/V head)
-  float* part;            // partial results of the splits
-  uint32_t* counters;     // one per (sequence, K/V head, row block), zero between calls
+  // attention.cu
+  int pieces;             // blocks that an even share of the steps is meant for
+  int n_slots;            // workspace slots
+  float* part;            // partial results, a slot per piece of a cut (sequence, K/V head)
+  uint32_t* counters;     // two per slot, zero between calls
   uint32_t* status;
 };
 // How one attention call is laid out: chosen on the host from the limits the caller gives.
 struct AttnPlan {
-  int nt;                 // 8-row tiles of query rows per block: 1 or 2
-  int row_blocks, n_split, split_tokens;
-  size_t part_floats, n_counters;
+  int nt;                 // attention.cu: 8-row tiles of query rows per block, 1 or 2
+  int pieces, n_slots;
+  int64_t grid;
+  size_t part_floats;
   int stream_rows;        // rows up to which a sequence goes to attention.cu: 0 none, INT_MAX all
   int tc_blocks;          // 256-row blocks of attention_tc.cu per (sequence, K/V head); 0: not launched
 };

@@ -74,6 +74,7 @@ strata_status check_batch(const strata_kv_cache* c, const strata_kv_batch* b, in
     return STRATA_ERR_SHAPE;
   if (b->n_seq == 0 || b->T == 0) return STRATA_OK;
   if (b->max_q < 1) return STRATA_ERR_SHAPE;
+  if ((b->max_kv / 32 + 1) * b->n_seq > 0x7FFFFFFF / c->n_kv_heads) return STRATA_ERR_SHAPE;
   if (b->table_stride < 0 || b->max_kv > b->table_stride * c->page_size) return STRATA_ERR_SHAPE;
   if (!b->q_start || !b->kv_len || (!b->page_table && b->max_kv > 0)) return STRATA_ERR_INVALID_ARG;
   if (!on(b->q_start, 4) || !on(b->kv_len, 4) || !on(b->page_table, 4)) return STRATA_ERR_INVALID_ARG;
@@ -86,7 +87,7 @@ struct AttnLayout {
 AttnLayout attn_layout(const AttnPlan& p) {
   AttnLayout L{};
   L.counters = sizeof(WsHeader);
-  L.part = round_up(L.counters + sizeof(uint32_t) * p.n_counters);
+  L.part = round_up(L.counters + 2 * sizeof(uint32_t) * p.n_slots);
   L.total = round_up(L.part + sizeof(float) * p.part_floats);
   return L;
 }
@@ -218,7 +219,7 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(workspace);
   if (!(flags & STRATA_WS_REUSE) &&
-      cudaMemsetAsync(base, 0, L.counters + sizeof(uint32_t) * p.n_counters, st) != cudaSuccess)
+      cudaMemsetAsync(base, 0, L.counters + 2 * sizeof(uint32_t) * p.n_slots, st) != cudaSuccess)
     return STRATA_ERR_CUDA;
   AttnArgs a{};
   a.c = *cache;
@@ -231,9 +232,8 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.group = n_heads / cache->n_kv_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
-  a.n_split = p.n_split;
-  a.split_tokens = p.split_tokens;
-  a.row_blocks = p.row_blocks;
+  a.pieces = p.pieces;
+  a.n_slots = p.n_slots;
   a.part = reinterpret_cast<float*>(base + L.part);
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);
   a.status = &reinterpret_cast<WsHeader*>(base)->status;

@@ -222,6 +222,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
 template <int kD>
 __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(KvAppendArgs a, int kv_blocks) {
   griddep_wait();
+  griddep_launch();
   if (blockIdx.x < static_cast<unsigned>(kv_blocks)) {
     const int head = blockIdx.x % a.c.n_kv_heads;
     const int lo = blockIdx.x / a.c.n_kv_heads * a.rows_per_block;  // rows_per_block <= kAppThreads

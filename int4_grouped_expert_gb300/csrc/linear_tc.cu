@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const __nv_bfloat16* _
                                                           int K, __half* __restrict__ xh, int* __restrict__ xexp) {
   __shared__ uint32_t s_mag[8];
   griddep_wait();
+  griddep_launch();
   const uint4* src = reinterpret_cast<const uint4*>(x + blockIdx.x * stride);
   uint4* dst = reinterpret_cast<uint4*>(xh + static_cast<int64_t>(blockIdx.x) * K);
   uint32_t m = 0;
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_a = tmem + kLtTok;
   griddep_wait();
+  griddep_launch();
 
   // tile = (token block, 128 weight rows), weight rows fastest
   const int mtiles = (a.N + kLtRows - 1) / kLtRows;
