@@ -21,7 +21,7 @@
 // run in one wave where the batch allows it, whatever the mix of lengths. (Blocks that start in a
 // later wave cost the time to find their work, fill their slots and join: about 8 us a wave measured.)
 // A block's warps join their results in shared memory; pieces leave reference, sum and fp32 rows in the
-// workspace, the last piece to arrive in a group of up to 16 (or the root of the count) joins the group's,
+// workspace, the last piece to arrive in a group of up to 8 (or the root of the count) joins the group's,
 // and the last group the groups'. All sums are in the order of the pieces.
 #include <algorithm>
 
@@ -83,6 +83,14 @@ struct Piece {
   int slot0;                 // workspace slot of the (sequence, head)'s piece 0, if of > 1
 };
 __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
+  if (a.b.n_seq == 1) {
+    const int steps = seq_steps(a, seq_view(a, 0, blockIdx.x == 0 && threadIdx.x == 0)).n, heads = a.c.n_kv_heads;
+    const int per = max(kAttMinSteps, (steps * heads + a.pieces - 1) / a.pieces), k = (steps + per - 1) / per;
+    if (static_cast<int>(blockIdx.x) >= k * heads) return false;
+    const int head = blockIdx.x / k;
+    p = {0, head, static_cast<int>(blockIdx.x) - head * k, k, head * k};
+    return true;
+  }
   // every warp scans for itself: a lane takes consecutive sequences
   const int lane = threadIdx.x & 31;
   const int per_lane = (a.b.n_seq + 31) / 32;
@@ -167,10 +175,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
   uint8_t* ring = att_smem + warp * (kAttSlots * 2 * KB);
   const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  float ks[kAttSlots][2], vs[kAttSlots][2];
-  int gone[kAttSlots];  // bit u: tile u of the step lies in a page that does not exist
-  auto issue = [&](int j0, float (&k_scale)[2], float (&v_scale)[2], int& lost, uint32_t slot) {
-    lost = 0;
+  // of each slot's two tiles: K scale, V scale (negative: the tile lies in a page that does not exist)
+  __shared__ float2 s_scale[kAttWarps][kAttSlots][2];
+  auto issue = [&](int j0, int i_slot) {
+    const uint32_t slot = ring_addr + i_slot * 2 * KB;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int j = j0 + 16 * u;
@@ -179,13 +187,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
         page = table[j >> pshift];
         if (page < 0 || page >= a.c.n_pages) {
           if (lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
-          page = -1;
-          lost |= 1 << u;
+          page = -2;
         }
       }
       const int64_t ph = page < 0 ? 0 : static_cast<int64_t>(page) * a.c.n_kv_heads + h;
-      k_scale[u] = page < 0 ? 0.f : a.c.k_scales[ph];
-      v_scale[u] = page < 0 ? 0.f : a.c.v_scales[ph];
+      const float2 scale = page < 0 ? make_float2(0.f, page == -2 ? -1.f : 0.f)
+                                    : make_float2(a.c.k_scales[ph], a.c.v_scales[ph]);
+      if (lane == 0) s_scale[warp][i_slot][u] = scale;
       const int64_t base = ((ph << pshift) + (j & pmask)) * kD + lane * 16;
       const int n = page < 0 ? 0 : hi - j;  // tokens of the tile from here on; past them: zeros
 #pragma unroll
@@ -199,11 +207,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     }
   };
   int j_next = lo + warp * kAttStep;
-#pragma unroll
-  for (int i = 0; i < kAttSlots; ++i) {
-    if (j_next < hi) issue(j_next, ks[i], vs[i], gone[i], ring_addr + i * 2 * KB);
+#pragma unroll 1
+  for (int i = 0; i < kAttSlots; ++i, j_next += kAttWarps * kAttStep) {
+    if (j_next < hi) issue(j_next, i);
     cp_async_commit();
-    j_next += kAttWarps * kAttStep;
   }
 
   // ---- the queries of column g of each tile as f16 B fragments, times 2^-e
@@ -269,7 +276,11 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     v_at[i] = KB + (kD == 128 ? slot_offset<kD>(r, g) : slot_offset<kD>(r, g >> 1) + (g & 1) * 8);
   }
 
-  auto step = [&](int j0, const float (&k_scale)[2], const float (&v_scale)[2], int lost, const uint8_t* slot) {
+  auto step = [&](int j0, int i_slot) {
+    const uint8_t* slot = ring + i_slot * 2 * KB;
+    const float2 sc0 = s_scale[warp][i_slot][0], sc1 = s_scale[warp][i_slot][1];
+    const float k_scale[2] = {sc0.x, sc1.x}, v_scale[2] = {fmaxf(sc0.y, 0.f), fmaxf(sc1.y, 0.f)};
+    const int lost = (sc0.y < 0.f ? 1 : 0) | (sc1.y < 0.f ? 2 : 0);
     // S^T: tokens tok_g, tok_g + 8 of each tile x columns 2t, 2t+1
     float sc[kNT][2][4];
 #pragma unroll
@@ -402,19 +413,16 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       }
     }
   };
-  for (int j0 = lo + warp * kAttStep; j0 < hi;) {
-#pragma unroll
-    for (int i = 0; i < kAttSlots; ++i) {
-      if (j0 >= hi) break;
-      cp_async_wait<kAttSlots - 1>();
-      __syncwarp();
-      step(j0, ks[i], vs[i], gone[i], ring + i * 2 * KB);
-      __syncwarp();  // every lane has read the slot
-      if (j_next < hi) issue(j_next, ks[i], vs[i], gone[i], ring_addr + i * 2 * KB);
-      cp_async_commit();
-      j_next += kAttWarps * kAttStep;
-      j0 += kAttWarps * kAttStep;
-    }
+  int i_slot = 0;
+#pragma unroll 1
+  for (int j0 = lo + warp * kAttStep; j0 < hi; j0 += kAttWarps * kAttStep, j_next += kAttWarps * kAttStep) {
+    cp_async_wait<kAttSlots - 1>();
+    __syncwarp();
+    step(j0, i_slot);
+    __syncwarp();  // every lane has read the slot
+    if (j_next < hi) issue(j_next, i_slot);
+    cp_async_commit();
+    i_slot = i_slot + 1 == kAttSlots ? 0 : i_slot + 1;
   }
 
   // ---- join the warps: every column to the largest reference, then the sums in the warps' order
@@ -497,66 +505,62 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     __syncthreads();
     return s_last != 0;
   };
-  // joins n slots, `step` apart from slot `from` on, into that slot, or into the output
-  float* s_w = s_o;  // [n][COLS]
+  // joins n slots, `step` apart from slot `from` on, into that slot, or into the output: each thread its
+  // elements, eight slots in flight
   auto join = [&](int from, int n, int step, bool final) {
     float* base = a.part + from * PART;
     const int64_t stride = step * PART;
-    constexpr int U = 16;  // loads in flight per thread
-    float4 v[U];
-    auto load = [&](int i, int k0) {
-      const float* src = base + i / (kD / 4) * kD + i % (kD / 4) * 4;
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        v[k] = k0 + k < n ? __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    if (threadIdx.x < rows * kD / 4) load(threadIdx.x, 0);
-    for (int i = threadIdx.x; i < n * COLS; i += kAttWarps * 32) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + i / COLS * stride + COLS * kD + 2 * (i % COLS)));
-      s_w[2 * i] = ml.x;
-      s_w[2 * i + 1] = ml.y;
-    }
-    __syncthreads();
-    for (int col = warp; col < rows; col += kAttWarps) {
-      float top = -INFINITY, l = 0.f;
-      for (int k = lane; k < n; k += 32) top = fmaxf(top, s_w[2 * (k * COLS + col)]);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      for (int k = lane; k < n; k += 32) {
-        const float f = top == -INFINITY ? 1.f : exp2_approx(s_w[2 * (k * COLS + col)] - top);
-        s_w[2 * (k * COLS + col)] = f;
-        l = fmaf(s_w[2 * (k * COLS + col) + 1], f, l);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      if (lane == 0) {
-        s_sum[0][col] = l;
-        s_ref[0][col] = top;
-      }
-    }
-    __syncthreads();
+#pragma unroll 1
     for (int i = threadIdx.x; i < rows * kD / 4; i += kAttWarps * 32) {
       const int col = i / (kD / 4), e = i % (kD / 4) * 4;
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k0 = 0; k0 < n; k0 += U) {
-        if (i != threadIdx.x || k0) load(i, k0);
+      const float* src = base + col * kD + e;
+      const float* stat = base + COLS * kD + 2 * col;
+      float top = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int k0 = 0; k0 < n; k0 += 8) {
+        float4 v[8];
+        float2 ml[8];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const float f = k0 + k < n ? s_w[2 * ((k0 + k) * COLS + col)] : 0.f;
-          y[0] = fmaf(v[k].x, f, y[0]); y[1] = fmaf(v[k].y, f, y[1]);
-          y[2] = fmaf(v[k].z, f, y[2]); y[3] = fmaf(v[k].w, f, y[3]);
+        for (int k = 0; k < 8; ++k) {
+          const bool in = k0 + k < n;
+          ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(stat + (k0 + k) * stride)) : make_float2(-INFINITY, 0.f);
+          v[k] = in ? __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) now = fmaxf(now, ml[k].x);
+        const float ref = now == -INFINITY ? 0.f : now;
+        const float f = now == -INFINITY ? 1.f : exp2_approx(top - ref);
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] *= f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          // (a slot that has seen nothing holds zeros; one that has seen nothing but nan, nan)
+          const float w = exp2_approx(ml[k].x - ref);
+          l = fmaf(ml[k].y, w, l);
+          y[0] = fmaf(v[k].x, w, y[0]); y[1] = fmaf(v[k].y, w, y[1]);
+          y[2] = fmaf(v[k].z, w, y[2]); y[3] = fmaf(v[k].w, w, y[3]);
+        }
+        top = now;
       }
       if (final) {
-        write(col, e, y, s_sum[0][col]);
-      } else {  // (this thread has read these elements of the slot)
+        write(col, e, y, l);
+      } else {  // (this thread alone reads these elements of the slot; its statistics are read by others)
         *reinterpret_cast<float4*>(base + col * kD + e) = make_float4(y[0], y[1], y[2], y[3]);
-        if (e == 0)
-          *reinterpret_cast<float2*>(base + COLS * kD + 2 * col) = make_float2(s_ref[0][col], s_sum[0][col]);
+        if (e == 0) {
+          s_ref[0][col] = top;
+          s_sum[0][col] = l;
+        }
       }
     }
+    if (!final) {
+      __syncthreads();  // all have read the statistics
+      if (threadIdx.x < rows)
+        *reinterpret_cast<float2*>(base + COLS * kD + 2 * threadIdx.x) = make_float2(s_ref[0][threadIdx.x], s_sum[0][threadIdx.x]);
+    }
   };
-  int gs = min(16, pc.of);
+  int gs = min(8, pc.of);
   while (gs * gs < pc.of) ++gs;
   const int groups = (pc.of + gs - 1) / gs, gi = pc.index / gs, g0 = gi * gs, gn = min(gs, pc.of - g0);
   if (!arrive_last(a.counters + pc.slot0 + g0, gn)) return;
