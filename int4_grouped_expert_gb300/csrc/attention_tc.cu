@@ -6,7 +6,7 @@
 //   S_i = Q_i K^T (f16, fp32 sums in TMEM) -> softmax weights P_i (f16, in TMEM over S_i) -> O_i += P_i V
 // with the two row tiles half a step apart, so that the tensor cores work on one while the softmax of
 // the other runs.
-//   warp 0         one thread issues the MMAs
+//   warp 0         an elected lane issues the MMAs
 //   warp 1         owns the TMEM allocation: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each)
 //   warps 4-11     softmax, one thread per row: running maximum and sum in fp32. O is rescaled only when
 //                  a maximum has grown by more than 2^8 over the one in use (weights up to 2^8 are as
@@ -174,56 +174,56 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t id_s = tc::idesc_f16(128, kAtTok), id_o = tc::idesc_f16(128, kD);
-      bool ok = true;
-      auto tile_at = [&](int t) { return tc::smem_u32(ring + (t % kAtRing) * C::TILE); };
-      auto full = [&](int t) {
-        return tc::mbar_wait(kv_full + t % kAtRing, (t / kAtRing) & 1, abort_flag, a.status);
-      };
-      auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
-        const uint32_t q = tc::smem_u32(smem + i * C::TILE), k = tile_at(2 * j);
+    const uint32_t id_s = tc::idesc_f16(128, kAtTok), id_o = tc::idesc_f16(128, kD);
+    auto tile_at = [&](int t) { return tc::smem_u32(ring + (t % kAtRing) * C::TILE); };
+    auto full = [&](int t) {
+      return tc::warp_wait(kv_full + t % kAtRing, (t / kAtRing) & 1, abort_flag, a.status);
+    };
+    auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
+      const uint64_t q = tc::sw128_desc(tc::smem_u32(smem + i * C::TILE)), k = tc::sw128_desc(tile_at(2 * j));
+      if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk)
-          tc::mma_f16_ss(tmem + i * 128, tc::sw128_desc(q + (kk >> 2) * (128 * 128)) + 2 * (kk & 3),
-                         tc::sw128_desc(k + (kk >> 2) * (128 * 128)) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
+        for (int kk = 0; kk < kD / 16; ++kk)  // (64-wide pieces are 16 KB apart, steps 32 bytes)
+          tc::mma_f16_ss(tmem + i * 128, q + (kk >> 2) * 1024 + 2 * (kk & 3), k + (kk >> 2) * 1024 + 2 * (kk & 3),
+                         id_s, kk ? 1u : 0u);
         tc::mma_commit(s_full + i);
         if (i == n_rt - 1) tc::mma_commit(kv_empty + (2 * j) % kAtRing);
-      };
-      ok = full(0);
-      if (ok) {
-        tc::tc_fence_after();
-        for (int i = 0; i < n_rt; ++i) scores(i, 0);
       }
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        for (int i = 0; i < n_rt; ++i) {
-          if (!tc::mbar_wait(p_full + i, j & 1, abort_flag, a.status) || (i == 0 && !full(2 * j + 1))) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t v = tile_at(2 * j + 1);
+      __syncwarp();
+    };
+    bool ok = full(0);
+    if (ok) {
+      tc::tc_fence_after();
+      for (int i = 0; i < n_rt; ++i) scores(i, 0);
+    }
+    for (int j = 0; ok && j < n_tiles; ++j) {
+      for (int i = 0; i < n_rt; ++i) {
+        ok = tc::warp_wait(p_full + i, j & 1, abort_flag, a.status) && (i > 0 || full(2 * j + 1));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t v = tc::sw128_desc(tile_at(2 * j + 1));
+        if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kAtTok / 16; ++kk)
-            tc::mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * kk,
-                           tc::sw128_desc(v + (kk >> 2) * (kD * 128)) + 2 * (kk & 3), id_o, (j | kk) ? 1u : 0u);
+          for (int kk = 0; kk < kAtTok / 16; ++kk)  // (64-token halves are kD * 128 bytes apart)
+            tc::mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * kk, v + (kk >> 2) * (kD * 8) + 2 * (kk & 3), id_o,
+                           (j | kk) ? 1u : 0u);
           tc::mma_commit(pv_done + i);
           if (i == n_rt - 1) tc::mma_commit(kv_empty + (2 * j + 1) % kAtRing);
-          if (j + 1 < n_tiles) {
-            // the next scores overwrite the weights: only once the product that reads them is done
-            if ((i == 0 && !full(2 * j + 2)) || !tc::mbar_wait(pv_done + i, j & 1, abort_flag, a.status)) {
-              ok = false;
-              break;
-            }
-            tc::tc_fence_after();
-            scores(i, j + 1);
-          }
+        }
+        __syncwarp();
+        if (j + 1 < n_tiles) {
+          // the next scores overwrite the weights: only once the product that reads them is done
+          ok = (i > 0 || full(2 * j + 2)) && tc::warp_wait(pv_done + i, j & 1, abort_flag, a.status);
+          if (!ok) break;
+          tc::tc_fence_after();
+          scores(i, j + 1);
         }
       }
-      if (!ok) {  // drain every MMA issued so far before TMEM is released
-        tc::mma_commit(drain);
-        tc::mbar_wait_drain(drain, 0);
-      }
+    }
+    if (!ok) {  // drain every MMA issued so far before TMEM is released
+      if (tc::elect_one()) tc::mma_commit(drain);
+      __syncwarp();
+      tc::mbar_wait_drain(drain, 0);
     }
     __syncwarp();
   } else if (softmax_warp && tile < n_rt) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(s_full + tile, j & 1, abort_flag, a.status));
+      ok = tc::warp_wait(s_full + tile, j & 1, abort_flag, a.status);
       if (!ok) break;
       tc::tc_fence_after();
       const int j0 = (j_lo + j) * kAtTok;
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       if (lane == 0) tc::mbar_arrive(p_full + tile);
     }
     if (ok) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_done + tile, (n_tiles - 1) & 1, abort_flag, a.status));
+      ok = tc::warp_wait(pv_done + tile, (n_tiles - 1) & 1, abort_flag, a.status);
       tc::tc_fence_after();
     }
     if (ok) {
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     bool ok = true;
     for (int t = 0; ok && t < 2 * n_tiles; ++t) {
       const int j = t >> 1;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(kv_empty + t % kAtRing, ((t / kAtRing) & 1) ^ 1, abort_flag, a.status));
+      ok = tc::warp_wait(kv_empty + t % kAtRing, ((t / kAtRing) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       uint8_t* dst = ring + (t % kAtRing) * C::TILE;
       if (t & 1) {

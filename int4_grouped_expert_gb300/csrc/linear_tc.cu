@@ -6,8 +6,8 @@
 // dequantizes 64 codes of its row and stores them to its own TMEM lane, so shared memory carries only
 // the activations. (Both operands in shared memory would move 96 KB a stage, 188 bytes a clock at the
 // MMA's pace, and 128 is what shared memory has; this way it is 64 KB.)
-//   warp 0       TMA: the stage's tokens (f16, 128-byte swizzle) -> a ring in shared memory
-//   warp 1       one thread issues tcgen05.mma (f16, M = 128, N = tokens, K = 16)
+//   warp 0       TMA (one elected lane): the stage's tokens (f16, 128-byte swizzle) -> a ring in shared memory
+//   warp 1       an elected lane issues tcgen05.mma (f16, M = 128, N = tokens, K = 16)
 //   warp 2       owns the TMEM allocation: 256 columns of sums, 8 stages x 32 columns of weights
 //   warps 4-11   dequantize: two warps per 32 lanes, one for the even and one for the odd stages
 //   warps 12-15  epilogue: TMEM -> registers -> bias, residual -> bf16
@@ -155,56 +155,58 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
-        const int nbox = (tokens(item) + kLtBox - 1) / kLtBox;
-        const int t0 = item / mtiles * kLtTok;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kLtBStages;
-          if (!tc::mbar_wait(empty_b + s, ((it / kLtBStages) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
+    int it = 0;
+    bool ok = true;
+    for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
+      const int nbox = (tokens(item) + kLtBox - 1) / kLtBox;
+      const int t0 = item / mtiles * kLtTok;
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const int s = it % kLtBStages;
+        ok = tc::warp_wait(empty_b + s, ((it / kLtBStages) & 1) ^ 1, abort_flag, a.status);
+        if (!ok) break;
+        if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(full_b + s, nbox * kLtBox * kLtBK * 2);
           for (int bx = 0; bx < nbox; ++bx)
             tc::tma_load_2d(smem + s * kLtBBytes + bx * kLtBox * kLtBK * 2, &tmap_x, (kb0 + kb) * kLtBK,
                             t0 + bx * kLtBox, full_b + s);
         }
+        __syncwarp();
       }
-      if (!ok)  // drain the copies that may still be in flight
-        for (int j = (it > kLtBStages ? it - kLtBStages : 0); j < it; ++j)
-          tc::mbar_wait_drain(full_b + (j % kLtBStages), (j / kLtBStages) & 1);
     }
+    if (!ok)  // drain the copies that may still be in flight
+      for (int j = (it > kLtBStages ? it - kLtBStages : 0); j < it; ++j)
+        tc::mbar_wait_drain(full_b + (j % kLtBStages), (j / kLtBStages) & 1);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      int it = 0, tcount = 0;
-      bool ok = true;
-      for (int item = blockIdx.x / ks; ok && item < n_items; item += step, ++tcount) {
-        const uint32_t idesc = tc::idesc_f16(kLtRows, (tokens(item) + 15) & ~15);
-        if (tcount > 0 && !tc::mbar_wait(acc_empty, (tcount - 1) & 1, abort_flag, a.status)) { ok = false; break; }
+    int it = 0, tcount = 0;
+    bool ok = true;
+    for (int item = blockIdx.x / ks; ok && item < n_items; item += step, ++tcount) {
+      const uint32_t idesc = tc::idesc_f16(kLtRows, (tokens(item) + 15) & ~15);
+      ok = tcount == 0 || tc::warp_wait(acc_empty, (tcount - 1) & 1, abort_flag, a.status);
+      if (!ok) break;
+      tc::tc_fence_after();
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const int sa = it % kLtAStages, sb = it % kLtBStages;
+        ok = tc::warp_wait(full_b + sb, (it / kLtBStages) & 1, abort_flag, a.status) &&
+             tc::warp_wait(full_a + sa, (it / kLtAStages) & 1, abort_flag, a.status);
+        if (!ok) break;
         tc::tc_fence_after();
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int sa = it % kLtAStages, sb = it % kLtBStages;
-          if (!tc::mbar_wait(full_b + sb, (it / kLtBStages) & 1, abort_flag, a.status) ||
-              !tc::mbar_wait(full_a + sa, (it / kLtAStages) & 1, abort_flag, a.status)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint64_t db = tc::sw128_desc(tc::smem_u32(smem + sb * kLtBBytes));
+        const uint64_t db = tc::sw128_desc(tc::smem_u32(smem + sb * kLtBBytes));
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kLtBK / 16; ++kk)
             tc::mma_f16_ts(tmem, tmem_a + sa * 32 + 8 * kk, db + 2 * kk, idesc, (kb | kk) ? 1u : 0u);
           tc::mma_commit(empty_a + sa);
           tc::mma_commit(empty_b + sb);
+          if (kb == nk - 1) tc::mma_commit(acc_full);
         }
-        if (!ok) break;
-        tc::mma_commit(acc_full);
+        __syncwarp();
       }
-      if (!ok) {  // drain every MMA issued so far before TMEM is released
-        tc::mma_commit(drain);
-        tc::mbar_wait_drain(drain, 0);
-      }
+    }
+    if (!ok) {  // drain every MMA issued so far before TMEM is released
+      if (tc::elect_one()) tc::mma_commit(drain);
+      __syncwarp();
+      tc::mbar_wait_drain(drain, 0);
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           }
           load(m + PD, u);
           // (the whole warp goes on or leaves: the TMEM instructions are warp-wide)
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(empty_a + s, ((it / kLtAStages) & 1) ^ 1, abort_flag, a.status));
+          ok = tc::warp_wait(empty_a + s, ((it / kLtAStages) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
           tc::tc_fence_after();
           tc::tmem_st32(lane_addr + s * 32, w);
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     int tcount = 0;
     for (int item = blockIdx.x / ks; item < n_items; item += step, ++tcount) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(acc_full, tcount & 1, abort_flag, a.status))) break;
+      if (!tc::warp_wait(acc_full, tcount & 1, abort_flag, a.status)) break;
       tc::tc_fence_after();
       const int n = item % mtiles * kLtRows + q4 * 32 + lane;
       const int64_t t0 = static_cast<int64_t>(item / mtiles) * kLtTok;

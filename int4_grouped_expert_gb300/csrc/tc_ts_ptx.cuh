@@ -6,6 +6,20 @@
 namespace strata {
 namespace tc {
 
+// One lane of a converged warp, always the same one. A warp that runs its loop whole and issues its
+// tcgen05 and TMA instructions under this predicate keeps their operands in uniform registers; a
+// branch on lane 0 around the loop costs about 100 clocks per MMA instead.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// mbar_wait by a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T: A holds one row per lane, two 16-bit elements per 32-bit column.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                            uint32_t idesc, uint32_t accumulate) {
