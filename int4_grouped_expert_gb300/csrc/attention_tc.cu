@@ -45,6 +45,33 @@ __device__ __forceinline__ uint32_t scaled_codes(uint32_t two, __half2 s) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Two fp32 values as one operand of the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int kD>
 __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a) {
   using C = AtCfg<kD>;
@@ -172,7 +199,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   if (k_ref == 0.f) k_ref = 1.f;
   if (v_ref == 0.f) v_ref = 1.f;
 
-  if (warp == 0) {
+  // registers: 5 warpgroups are launched with 96 a thread (61440 in all) and go on with
+  // 48 + 2 * 136 + 2 * 80 (the same)
+  if (warp < 4) {
+    tc::reg_dec<48>();
+    if (warp == 0) {
     // ------------------------------------------------------------------ MMA issuer
     const uint32_t id_s = tc::idesc_f16(128, kAtTok), id_o = tc::idesc_f16(128, kD);
     auto tile_at = [&](int t) { return tc::smem_u32(ring + (t % kAtRing) * C::TILE); };
@@ -205,7 +236,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kAtTok / 16; ++kk)  // (64-token halves are kD * 128 bytes apart)
-            tc::mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * kk, v + (kk >> 2) * (kD * 8) + 2 * (kk & 3), id_o,
+            tc::mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + 64 + 8 * kk, v + (kk >> 2) * (kD * 8) + 2 * (kk & 3), id_o,
                            (j | kk) ? 1u : 0u);
           tc::mma_commit(pv_done + i);
           if (i == n_rt - 1) tc::mma_commit(kv_empty + (2 * j + 1) % kAtRing);
@@ -225,13 +256,16 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       __syncwarp();
       tc::mbar_wait_drain(drain, 0);
     }
+    }
     __syncwarp();
-  } else if (softmax_warp && tile < n_rt) {
+  } else if (warp < 12) {
+    tc::reg_inc<136>();
+    if (tile < n_rt) {
     // ------------------------------------------------------------------ softmax
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
     const int pos = sv.len - sv.n + row / G;
-    cmul *= k_ref;
+    cmul = fmaxf(cmul * k_ref, 1.17549435e-38f);  // (never 0: a masked score, -inf, stays -inf under it)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
@@ -243,25 +277,32 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       const int hi = min(pos, sv.len - 1) - j0, lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
       const unsigned long long gone = bad[j % kAtBad];
       const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && lo <= 0) && gone == 0;
+      auto seen = [&](int c) { return c <= hi && c >= lo && !((gone >> (c / 16 * 8)) & 1); };
+      // Scores are read 32 columns at a time, the next ones on their way, up for the maximum and down
+      // again for the weights: the last columns are read once. The weights (16 columns of f16 pairs per
+      // 32 scores) go to the upper half of the scores' columns, always over scores that have been read.
+      uint32_t r[2][32];
+      auto mask = [&](uint32_t (&x)[32], int q) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = seen(32 * q + i) ? x[i] : 0xFF800000u;  // -inf
+      };
       float top = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < kAtTok; c += 32) {
-        uint32_t r[32];
-        tc::tmem_ld32(ts + c, r);
+      tc::tmem_ld32(ts, r[0]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
         tc::tmem_ld_wait();
-        if (whole) {
+        if (q < 3) tc::tmem_ld32(ts + 32 * (q + 1), r[(q + 1) & 1]);
+        uint32_t (&x)[32] = r[q & 1];
+        if (!whole) mask(x, q);
+        float t0 = top, t1 = __uint_as_float(x[31]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(r[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const bool seen = c + i <= hi && c + i >= lo && !((gone >> ((c + i) / 16 * 8)) & 1);
-            top = fmaxf(top, seen ? __uint_as_float(r[i]) : -INFINITY);
-          }
+        for (int i = 0; i < 30; i += 4) {
+          t0 = max3(t0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          t1 = max3(t1, __uint_as_float(x[i + 2]), __uint_as_float(x[min(i + 3, 30)]));
         }
+        top = fmaxf(t0, t1);
       }
       top *= cmul;
-      if (__isnanf(top)) top = -INFINITY;  // -inf * 0: nothing seen under a zero scale
       if (__any_sync(0xffffffffu, top > m + 8.f)) {
         const float now = fmaxf(m, top);
         const float f = now == -INFINITY ? 1.f : exp2_approx(m - now);
@@ -269,42 +310,39 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         l *= f;
         if (j > 0) {  // (the product that adds to O is done: the scores of this tile came after it)
 #pragma unroll 1
-          for (int c = 0; c < kD; c += 32) {
-            uint32_t r[32];
-            tc::tmem_ld32(to + c, r);
+          for (int c = 0; c < kD; c += 16) {
+            uint32_t x[16];
+            tc::tmem_ld16(to + c, x);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-            tc::tmem_st32(to + c, r);
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+            tc::tmem_st16(to + c, x);
           }
         }
       }
       const float ref = m == -INFINITY ? 0.f : m;
-      float add0 = 0.f, add1 = 0.f;
-#pragma unroll 1
-      for (int c = 0; c < kAtTok; c += 32) {
-        uint32_t r[32], p[16];
-        tc::tmem_ld32(ts + c, r);
-        tc::tmem_ld_wait();
+      const uint64_t cc = pack_f32x2(cmul, cmul), mm = pack_f32x2(-ref, -ref);
+      uint64_t sum0 = 0, sum1 = 0;  // (two zeros)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(r[i]), cmul, -ref)));
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const bool seen = c + i <= hi && c + i >= lo && !((gone >> ((c + i) / 16 * 8)) & 1);
-            if (!seen) r[i] = 0u;
-          }
-        }
+      for (int q = 3; q >= 0; --q) {
+        if (q < 3) tc::tmem_ld_wait();
+        if (q > 0) tc::tmem_ld32(ts + 32 * (q - 1), r[(q - 1) & 1]);
+        uint32_t (&x)[32] = r[q & 1];
+        if (!whole && q < 3) mask(x, q);
+        uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float x = __uint_as_float(r[2 * i]), y = __uint_as_float(r[2 * i + 1]);
-          add0 += x;
-          add1 += y;
-          p[i] = pack_f16x2(x, y);
+          float2 e = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, mm));
+          e.x = exp2_approx(e.x);
+          e.y = exp2_approx(e.y);
+          if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(e.x, e.y));
+          else sum0 = add_f32x2(sum0, pack_f32x2(e.x, e.y));
+          p[i] = pack_f16x2(e.x, e.y);
         }
-        tc::tmem_st16(ts + c / 2, p);  // over scores that this thread has read
+        tc::tmem_st16(ts + 64 + 16 * q, p);
       }
-      l += add0 + add1;
+      const float2 sums = unpack_f32x2(add_f32x2(sum0, sum1));
+      l += sums.x + sums.y;
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -336,7 +374,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         }
       }
     }
-  } else if (warp >= 12) {
+    }
+  } else {
+    tc::reg_dec<80>();
     // ------------------------------------------------------------------ codes -> f16 tiles
     const int w = warp - 12;
     // K: this warp's 16 tokens of the tile (one page); a lane takes 16 bytes of rows lane % 8 and + 8
@@ -346,49 +386,56 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     const int tg = lane & 3, dg = ((lane >> 2) & 1) | (lane >> 3) << 1;
     uint4 kr[2][KC];
     uint32_t vr[VP][8];
-    __half2 ks2, vs2[VP];
+    float k_scale, v_scale[VP];
+    const int pshift = 31 - __clz(P);
+    const float k_inv = 1.0f / k_ref, v_inv = 1.0f / v_ref;
     uint32_t k_gone = 0;
-    auto page_of = [&](int tok, bool flag) -> int64_t {
-      if (tok >= tok_hi) return -1;
-      const int64_t page = table[tok / P];
-      if (page >= 0 && page < a.c.n_pages) return page;
-      if (flag) set_status(a.status, STRATA_DEV_BAD_SLOT);
-      return -2;
-    };
+    // page of a token, -1 for one that no row sees; looked up a tile ahead
+    auto page_of = [&](int tok) { return tok < tok_hi ? table[tok >> pshift] : -1; };
+    auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
+    const int k_tok = j_lo * kAtTok + w * 16;
+    int v_tok[VP], k_page = page_of(k_tok), v_page[VP];
+#pragma unroll
+    for (int p = 0; p < VP; ++p) {
+      // piece: tokens (u % 4) * 32, elements (u / 4) * 32
+      v_tok[p] = j_lo * kAtTok + ((w * VP + p) & 3) * 32 + tg * 8;
+      v_page[p] = page_of(v_tok[p]);
+    }
     auto load_k = [&](int j) {
-      const int tok = (j_lo + j) * kAtTok + w * 16;
-      const int64_t page = page_of(tok, lane == 0);
-      k_gone = page == -2;
-      const int64_t ph = page < 0 ? 0 : page * a.c.n_kv_heads + h;
-      const float r = page < 0 ? 0.f : a.c.k_scales[ph] / k_ref;
-      ks2 = __floats2half2_rn(r, r);
-      const uint8_t* src = a.c.k_codes + (ph * P + tok % P) * kD + (lane >> 3) * 16;
+      const int tok = k_tok + j * kAtTok;
+      const bool on = good(k_page);
+      k_gone = !on && tok < tok_hi;
+      if (k_gone && lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
+      const int64_t ph = on ? static_cast<int64_t>(k_page) * a.c.n_kv_heads + h : 0;
+      k_scale = on ? a.c.k_scales[ph] : 0.f;
+      const uint8_t* src = a.c.k_codes + ((ph << pshift) + (tok & (P - 1)) + (lane & 7)) * kD + (lane >> 3) * 16;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-          const int t = (lane & 7) + 8 * i;
           kr[i][c] = make_uint4(0u, 0u, 0u, 0u);
-          if (page >= 0 && tok + t < tok_hi)
-            kr[i][c] = __ldcg(reinterpret_cast<const uint4*>(src + t * kD + c * 64));
+          if (on && tok + (lane & 7) + 8 * i < tok_hi)
+            kr[i][c] = __ldcg(reinterpret_cast<const uint4*>(src + 8 * i * kD + c * 64));
         }
+      k_page = page_of(tok + kAtTok);
     };
     auto load_v = [&](int j) {
 #pragma unroll
       for (int p = 0; p < VP; ++p) {
-        const int u = w * VP + p;                  // piece: tokens (u % 4) * 32, elements (u / 4) * 32
-        const int tok = (j_lo + j) * kAtTok + (u & 3) * 32 + tg * 8;
-        const int64_t page = page_of(tok, false);
-        const int64_t ph = page < 0 ? 0 : page * a.c.n_kv_heads + h;
-        const float r = page < 0 ? 0.f : a.c.v_scales[ph] / v_ref;
-        vs2[p] = __floats2half2_rn(r, r);
-        const uint8_t* src = a.c.v_codes + (ph * P + tok % P) * kD + (u >> 2) * 32 + dg * 4;
+        const int u = w * VP + p, tok = v_tok[p] + j * kAtTok;
+        const bool on = good(v_page[p]);
+        const int64_t ph = on ? static_cast<int64_t>(v_page[p]) * a.c.n_kv_heads + h : 0;
+        v_scale[p] = on ? a.c.v_scales[ph] : 0.f;
+        const uint8_t* src = a.c.v_codes + ((ph << pshift) + (tok & (P - 1))) * kD + (u >> 2) * 32 + dg * 4;
+        const int n = on ? tok_hi - tok : 0;
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-          vr[p][t] = page >= 0 && tok + t < tok_hi ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
+        for (int t = 0; t < 8; ++t) vr[p][t] = t < n ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
+        v_page[p] = page_of(tok + kAtTok);
       }
     };
     auto store_k = [&](uint8_t* dst) {
+      const float r = k_scale * k_inv;
+      const __half2 ks2 = __floats2half2_rn(r, r);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -408,6 +455,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 #pragma unroll
       for (int p = 0; p < VP; ++p) {
         const int u = w * VP + p;
+        const float r = v_scale[p] * v_inv;
+        const __half2 vs2 = __floats2half2_rn(r, r);
         const int ch = (u & 1) * 4 + tg;           // 8-token column within a 64-token half
         uint8_t* base = dst + ((u & 3) >> 1) * (kD * 128);
         uint32_t o[4][4];                          // [element][token pair]
@@ -415,10 +464,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         for (int t = 0; t < 4; ++t) {
           const uint32_t x = prmt(vr[p][2 * t], vr[p][2 * t + 1], 0x5140);
           const uint32_t y = prmt(vr[p][2 * t], vr[p][2 * t + 1], 0x7362);
-          o[0][t] = scaled_codes(x, vs2[p]);
-          o[1][t] = scaled_codes(x >> 16, vs2[p]);
-          o[2][t] = scaled_codes(y, vs2[p]);
-          o[3][t] = scaled_codes(y >> 16, vs2[p]);
+          o[0][t] = scaled_codes(x, vs2);
+          o[1][t] = scaled_codes(x >> 16, vs2);
+          o[2][t] = scaled_codes(y, vs2);
+          o[3][t] = scaled_codes(y >> 16, vs2);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
