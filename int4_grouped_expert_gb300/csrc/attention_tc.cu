@@ -2,25 +2,27 @@
 // the cache are those of attention.cu).
 //
 // A block owns 256 query rows of one sequence and K/V head (query rows x the heads that share it): two
-// tiles of 128 rows, a TMEM lane each. It walks the cache in tiles of 128 tokens:
+// tiles of 128 rows, a TMEM lane each. It walks the cache in tiles of 64 tokens:
 //   S_i = Q_i K^T (f16, fp32 sums in TMEM) -> softmax weights P_i (f16, in TMEM over S_i) -> O_i += P_i V
-// with the two row tiles half a step apart, so that the tensor cores work on one while the softmax of
-// the other runs.
+// Each row tile has two score buffers, so that its next scores are ready when a softmax ends, and the
+// two row tiles are half a step apart. (With 128-token tiles and one score buffer the chain scores ->
+// softmax -> product was the whole time: 5200 clocks per 128 tokens, of which the tensor cores
+// needed 2048.)
 //   warp 0         an elected lane issues the MMAs
-//   warp 1         owns the TMEM allocation: S_0, S_1 (128 columns each), O_0, O_1 (head_dim each)
-//   warps 4-11     softmax, one thread per row: running maximum and sum in fp32. O is rescaled only when
-//                  a maximum has grown by more than 2^8 over the one in use (weights up to 2^8 are as
-//                  exact in f16 and the sums fp32), which after the first tiles is rare
+//   warp 1         owns the TMEM allocation: the score buffers (4 x 64 columns), O_0, O_1 (head_dim each)
+//   warps 4-11     softmax, one thread per row: running reference and sum in fp32. O is rescaled only when
+//                  a score has grown by more than 2^8 over the reference (weights up to 2^8 are as exact
+//                  in f16 and the sums fp32), which after the first tiles is rare
 //   warps 12-19    codes -> f16 tiles in shared memory, K as it lies and V transposed (bytes of two
-//                  tokens paired with PRMT), a ring of 4 tiles in the order K, V, K, V, ...
+//                  tokens paired with PRMT), a ring of 8 tiles in the order K0, K1, V0, K2, V1, ...
 // A page's scale relative to the largest of the block's pages multiplies its codes on the way: exact for
 // powers of two down to 2^-15, absolute error below 2^-25 of the largest scale beyond.
 // Queries become f16 with a power of two per row; a token that no row sees or in a page that does not
 // exist becomes zeros and a masked score, so what lies there does not matter.
 //
-// Bound by the MMAs (1024 clocks per row tile and 128 tokens at 128-wide heads) and the softmax's
-// instructions, which overlap. Every mbarrier wait is bounded in time; on time-out the kernel sets
-// STRATA_DEV_TIMEOUT, every role leaves its loop, MMAs in flight are drained (bounded) and TMEM is freed.
+// Bound by the softmax's instructions and by shared memory (scores of 64 tokens read 6 KB per 32 clocks
+// of MMA). Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every
+// role leaves its loop, MMAs in flight are drained (bounded) and TMEM is freed.
 #include "attention.cuh"
 #include "tc_ts_ptx.cuh"
 
@@ -28,15 +30,16 @@ namespace strata {
 
 namespace {
 
-constexpr int kAtTok = 128;     // tokens per tile
-constexpr int kAtRing = 4;      // tiles of codes converted to f16
+constexpr int kAtTok = 64;      // tokens per tile
+constexpr int kAtRing = 8;      // tiles of codes converted to f16
 constexpr int kAtThreads = 640;
 constexpr int kAtBad = 8;       // ring of per-tile masks of tokens in pages that do not exist
 
 template <int kD>
 struct AtCfg {
-  static constexpr int TILE = 128 * kD * 2;  // bytes of a Q, K or V tile in f16
-  static constexpr size_t SMEM = static_cast<size_t>(2 + kAtRing) * TILE + 1024 + 512;
+  static constexpr int QTILE = 128 * kD * 2;   // bytes of a row tile of Q in f16
+  static constexpr int TILE = kAtTok * kD * 2; // of a tile of K or V
+  static constexpr size_t SMEM = 2 * QTILE + static_cast<size_t>(kAtRing) * TILE + 1024 + 512;
 };
 
 __device__ __forceinline__ uint32_t scaled_codes(uint32_t two, __half2 s) {
@@ -79,15 +82,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   extern __shared__ uint8_t at_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* ring = smem + 2 * C::TILE;
+  uint8_t* ring = smem + 2 * C::QTILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kAtRing * C::TILE);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + kAtRing;
-  uint64_t* s_full = kv_empty + kAtRing;  // [2]
-  uint64_t* p_full = s_full + 2;          // [2]
-  uint64_t* pv_done = p_full + 2;         // [2]
-  uint64_t* drain = pv_done + 2;
-  uint64_t* bad = drain + 1;              // [kAtBad], a byte per 16 tokens
+  uint64_t* s_full = kv_empty + kAtRing;  // [row tile][buffer]
+  uint64_t* p_full = s_full + 4;          // [row tile][buffer]
+  uint64_t* pv_done = p_full + 4;         // [row tile][buffer]
+  uint64_t* drain = pv_done + 4;
+  uint64_t* bad = drain + 1;              // [kAtBad], a byte per 8 tokens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bad + kAtBad);
   __shared__ int abort_flag_s;
   __shared__ float s_ref[2][8];
@@ -131,9 +134,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       tc::mbar_init(kv_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(s_full + i, 1);
-      tc::mbar_init(p_full + i, 4);
-      tc::mbar_init(pv_done + i, 1);
+      tc::mbar_init(s_full + 2 * i, 1);
+      tc::mbar_init(s_full + 2 * i + 1, 1);
+      tc::mbar_init(p_full + 2 * i, 4);
+      tc::mbar_init(p_full + 2 * i + 1, 4);
+      tc::mbar_init(pv_done + 2 * i, 1);
+      tc::mbar_init(pv_done + 2 * i + 1, 1);
     }
     tc::mbar_init(drain, 1);
     tc::fence_barrier_init();
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     // a negative softmax scale goes into the queries, so that the largest product has the largest weight
     const float f = a.scale_log2 < 0.f ? -exp2i(-e) : exp2i(-e);
     cmul = fabsf(a.scale_log2) * exp2i(e);
-    uint8_t* dst = smem + tile * C::TILE + (row & 127) * 128;
+    uint8_t* dst = smem + tile * C::QTILE + (row & 127) * 128;
 #pragma unroll
     for (int i = 0; i < kD / 8; ++i) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -201,56 +207,60 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 
   // registers: 5 warpgroups are launched with 96 a thread (61440 in all) and go on with
   // 48 + 2 * 136 + 2 * 80 (the same)
+  // places of K_j and V_j in the order of the ring
+  auto t_k = [](int j) { return j < 2 ? j : 2 * j - 1; };
+  auto t_v = [](int j) { return 2 * j + 2; };
+  // O_i += P_i(j) V_j is done. Barriers of step j are per buffer (j & 1): whoever waits for one knows that
+  // the step before it on the same buffer is over, and that no later one has begun.
+  auto done = [&](int i, int j) {
+    return tc::warp_wait(pv_done + 2 * i + (j & 1), (j >> 1) & 1, abort_flag, a.status);
+  };
   if (warp < 4) {
     tc::reg_dec<48>();
     if (warp == 0) {
     // ------------------------------------------------------------------ MMA issuer
     const uint32_t id_s = tc::idesc_f16(128, kAtTok), id_o = tc::idesc_f16(128, kD);
-    auto tile_at = [&](int t) { return tc::smem_u32(ring + (t % kAtRing) * C::TILE); };
+    auto tile_at = [&](int t) { return tc::sw128_desc(tc::smem_u32(ring + (t % kAtRing) * C::TILE)); };
     auto full = [&](int t) {
       return tc::warp_wait(kv_full + t % kAtRing, (t / kAtRing) & 1, abort_flag, a.status);
     };
-    auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
-      const uint64_t q = tc::sw128_desc(tc::smem_u32(smem + i * C::TILE)), k = tc::sw128_desc(tile_at(2 * j));
+    // S_i(j) = Q_i K_j^T into buffer j & 1, which held P_i(j - 2): once the product that read it is done
+    auto scores = [&](int i, int j) {
+      if (j >= n_tiles || i >= n_rt) return true;
+      if (!full(t_k(j)) || (j >= 2 && !done(i, j - 2))) return false;
+      tc::tc_fence_after();
+      const uint64_t q = tc::sw128_desc(tc::smem_u32(smem + i * C::QTILE)), k = tile_at(t_k(j));
       if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk)  // (64-wide pieces are 16 KB apart, steps 32 bytes)
-          tc::mma_f16_ss(tmem + i * 128, q + (kk >> 2) * 1024 + 2 * (kk & 3), k + (kk >> 2) * 1024 + 2 * (kk & 3),
-                         id_s, kk ? 1u : 0u);
-        tc::mma_commit(s_full + i);
-        if (i == n_rt - 1) tc::mma_commit(kv_empty + (2 * j) % kAtRing);
+        for (int kk = 0; kk < kD / 16; ++kk)  // (64-wide pieces of Q are 16 KB apart, of K 8 KB, steps 32 bytes)
+          tc::mma_f16_ss(tmem + i * 128 + (j & 1) * 64, q + (kk >> 2) * 1024 + 2 * (kk & 3),
+                         k + (kk >> 2) * (kAtTok * 8) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
+        tc::mma_commit(s_full + 2 * i + (j & 1));
+        if (i == n_rt - 1) tc::mma_commit(kv_empty + t_k(j) % kAtRing);
       }
       __syncwarp();
+      return true;
     };
-    bool ok = full(0);
-    if (ok) {
+    // O_i += P_i(j) V_j
+    auto product = [&](int i, int j) {
+      if (i >= n_rt) return true;
+      if (!tc::warp_wait(p_full + 2 * i + (j & 1), (j >> 1) & 1, abort_flag, a.status) || !full(t_v(j))) return false;
       tc::tc_fence_after();
-      for (int i = 0; i < n_rt; ++i) scores(i, 0);
-    }
-    for (int j = 0; ok && j < n_tiles; ++j) {
-      for (int i = 0; i < n_rt; ++i) {
-        ok = tc::warp_wait(p_full + i, j & 1, abort_flag, a.status) && (i > 0 || full(2 * j + 1));
-        if (!ok) break;
-        tc::tc_fence_after();
-        const uint64_t v = tc::sw128_desc(tile_at(2 * j + 1));
-        if (tc::elect_one()) {
+      const uint64_t v = tile_at(t_v(j));
+      if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kAtTok / 16; ++kk)  // (64-token halves are kD * 128 bytes apart)
-            tc::mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + 64 + 8 * kk, v + (kk >> 2) * (kD * 8) + 2 * (kk & 3), id_o,
-                           (j | kk) ? 1u : 0u);
-          tc::mma_commit(pv_done + i);
-          if (i == n_rt - 1) tc::mma_commit(kv_empty + (2 * j + 1) % kAtRing);
-        }
-        __syncwarp();
-        if (j + 1 < n_tiles) {
-          // the next scores overwrite the weights: only once the product that reads them is done
-          ok = (i > 0 || full(2 * j + 2)) && tc::warp_wait(pv_done + i, j & 1, abort_flag, a.status);
-          if (!ok) break;
-          tc::tc_fence_after();
-          scores(i, j + 1);
-        }
+        for (int kk = 0; kk < kAtTok / 16; ++kk)
+          tc::mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + (j & 1) * 64 + 32 + 8 * kk, v + 2 * kk, id_o,
+                         (j | kk) ? 1u : 0u);
+        tc::mma_commit(pv_done + 2 * i + (j & 1));
+        if (i == n_rt - 1) tc::mma_commit(kv_empty + t_v(j) % kAtRing);
       }
-    }
+      __syncwarp();
+      return true;
+    };
+    bool ok = scores(0, 0) && scores(1, 0) && scores(0, 1);
+    for (int j = 0; ok && j < n_tiles; ++j)
+      ok = product(0, j) && scores(1, j + 1) && product(1, j) && scores(0, j + 2);
     if (!ok) {  // drain every MMA issued so far before TMEM is released
       if (tc::elect_one()) tc::mma_commit(drain);
       __syncwarp();
@@ -263,13 +273,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     if (tile < n_rt) {
     // ------------------------------------------------------------------ softmax
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
+    const uint32_t to = tmem + 256 + tile * 128 + lanes;
     const int pos = sv.len - sv.n + row / G;
     cmul = fmaxf(cmul * k_ref, 1.17549435e-38f);  // (never 0: a masked score, -inf, stays -inf under it)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
-      ok = tc::warp_wait(s_full + tile, j & 1, abort_flag, a.status);
+      const uint32_t ts = tmem + tile * 128 + (j & 1) * 64 + lanes;
+      ok = tc::warp_wait(s_full + 2 * tile + (j & 1), (j >> 1) & 1, abort_flag, a.status);
       if (!ok) break;
       tc::tc_fence_after();
       const int j0 = (j_lo + j) * kAtTok;
@@ -277,38 +288,35 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       const int hi = min(pos, sv.len - 1) - j0, lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
       const unsigned long long gone = bad[j % kAtBad];
       const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && lo <= 0) && gone == 0;
-      auto seen = [&](int c) { return c <= hi && c >= lo && !((gone >> (c / 16 * 8)) & 1); };
-      // Scores are read 32 columns at a time, the next ones on their way, up for the maximum and down
-      // again for the weights: the last columns are read once. The weights (16 columns of f16 pairs per
-      // 32 scores) go to the upper half of the scores' columns, always over scores that have been read.
       uint32_t r[2][32];
-      auto mask = [&](uint32_t (&x)[32], int q) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = seen(32 * q + i) ? x[i] : 0xFF800000u;  // -inf
-      };
-      float top = -INFINITY;
       tc::tmem_ld32(ts, r[0]);
+      tc::tmem_ld32(ts + 32, r[1]);
+      tc::tmem_ld_wait();
+      if (!whole) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tc::tmem_ld_wait();
-        if (q < 3) tc::tmem_ld32(ts + 32 * (q + 1), r[(q + 1) & 1]);
-        uint32_t (&x)[32] = r[q & 1];
-        if (!whole) mask(x, q);
-        float t0 = top, t1 = __uint_as_float(x[31]);
-#pragma unroll
-        for (int i = 0; i < 30; i += 4) {
-          t0 = max3(t0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          t1 = max3(t1, __uint_as_float(x[i + 2]), __uint_as_float(x[min(i + 3, 30)]));
+        for (int i = 0; i < kAtTok; ++i) {
+          const bool seen = i <= hi && i >= lo && !((gone >> (i / 8 * 8)) & 1);
+          r[i / 32][i % 32] = seen ? r[i / 32][i % 32] : 0xFF800000u;  // -inf
         }
-        top = fmaxf(t0, t1);
       }
-      top *= cmul;
+      float t0 = __uint_as_float(r[0][0]), t1 = __uint_as_float(r[1][0]);
+#pragma unroll
+      for (int i = 1; i < 31; i += 2) {
+        t0 = max3(t0, __uint_as_float(r[0][i]), __uint_as_float(r[0][i + 1]));
+        t1 = max3(t1, __uint_as_float(r[1][i]), __uint_as_float(r[1][i + 1]));
+      }
+      t0 = max3(t0, t1, __uint_as_float(r[0][31]));
+      const float top = fmaxf(t0, __uint_as_float(r[1][31])) * cmul;
       if (__any_sync(0xffffffffu, top > m + 8.f)) {
         const float now = fmaxf(m, top);
         const float f = now == -INFINITY ? 1.f : exp2_approx(m - now);
         m = now;
         l *= f;
-        if (j > 0) {  // (the product that adds to O is done: the scores of this tile came after it)
+        if (j > 0) {
+          // the last product has to have added to O (the scores of this tile were issued before it)
+          ok = done(tile, j - 1);
+          if (!ok) break;
+          tc::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < kD; c += 16) {
             uint32_t x[16];
@@ -324,32 +332,28 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       const uint64_t cc = pack_f32x2(cmul, cmul), mm = pack_f32x2(-ref, -ref);
       uint64_t sum0 = 0, sum1 = 0;  // (two zeros)
 #pragma unroll
-      for (int q = 3; q >= 0; --q) {
-        if (q < 3) tc::tmem_ld_wait();
-        if (q > 0) tc::tmem_ld32(ts + 32 * (q - 1), r[(q - 1) & 1]);
-        uint32_t (&x)[32] = r[q & 1];
-        if (!whole && q < 3) mask(x, q);
+      for (int q = 0; q < 2; ++q) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          float2 e = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, mm));
+          float2 e = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(r[q][2 * i]), __uint_as_float(r[q][2 * i + 1])), cc, mm));
           e.x = exp2_approx(e.x);
           e.y = exp2_approx(e.y);
           if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(e.x, e.y));
           else sum0 = add_f32x2(sum0, pack_f32x2(e.x, e.y));
           p[i] = pack_f16x2(e.x, e.y);
         }
-        tc::tmem_st16(ts + 64 + 16 * q, p);
+        tc::tmem_st16(ts + 32 + 16 * q, p);  // f16 pairs, over scores that this thread has read
       }
       const float2 sums = unpack_f32x2(add_f32x2(sum0, sum1));
       l += sums.x + sums.y;
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(p_full + tile);
+      if (lane == 0) tc::mbar_arrive(p_full + 2 * tile + (j & 1));
     }
     if (ok) {
-      ok = tc::warp_wait(pv_done + tile, (n_tiles - 1) & 1, abort_flag, a.status);
+      ok = done(tile, n_tiles - 1);
       tc::tc_fence_after();
     }
     if (ok) {
@@ -379,123 +383,120 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     tc::reg_dec<80>();
     // ------------------------------------------------------------------ codes -> f16 tiles
     const int w = warp - 12;
-    // K: this warp's 16 tokens of the tile (one page); a lane takes 16 bytes of rows lane % 8 and + 8
-    // V: 32 x 32 pieces (tokens x elements); a lane takes 4 elements of 8 tokens, chosen so that eight
+    // K: this warp's 8 tokens of the tile (one page); a lane takes 16 bytes of row lane % 8 per 64-wide piece
+    // V: a 32 x 32 piece (tokens x elements); a lane takes 4 elements of 8 tokens, chosen so that eight
     // lanes store to eight different 16-byte columns of the swizzled rows
-    constexpr int VP = 2 * KC / 2;                 // V pieces per warp: 1 or 2
+    const bool v_on = w < 2 * kD / 32;               // (64-wide heads have 4 pieces)
     const int tg = lane & 3, dg = ((lane >> 2) & 1) | (lane >> 3) << 1;
+    // codes and scales of the tiles j (even) and j (odd), on their way two tiles ahead
     uint4 kr[2][KC];
-    uint32_t vr[VP][8];
-    float k_scale, v_scale[VP];
+    uint32_t vr[2][8];
+    float k_scale[2], v_scale[2];
+    uint32_t k_gone[2];
     const int pshift = 31 - __clz(P);
     const float k_inv = 1.0f / k_ref, v_inv = 1.0f / v_ref;
-    uint32_t k_gone = 0;
-    // page of a token, -1 for one that no row sees; looked up a tile ahead
+    // page of a token, -1 for one that no row sees; looked up one more tile ahead
     auto page_of = [&](int tok) { return tok < tok_hi ? table[tok >> pshift] : -1; };
     auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-    const int k_tok = j_lo * kAtTok + w * 16;
-    int v_tok[VP], k_page = page_of(k_tok), v_page[VP];
-#pragma unroll
-    for (int p = 0; p < VP; ++p) {
-      // piece: tokens (u % 4) * 32, elements (u / 4) * 32
-      v_tok[p] = j_lo * kAtTok + ((w * VP + p) & 3) * 32 + tg * 8;
-      v_page[p] = page_of(v_tok[p]);
-    }
-    auto load_k = [&](int j) {
+    const int k_tok = j_lo * kAtTok + w * 8, v_tok = j_lo * kAtTok + (w & 1) * 32 + tg * 8;
+    int k_page = page_of(k_tok), v_page = page_of(v_tok);
+    auto load_k = [&](int j, uint4 (&x)[KC], float& scale, uint32_t& gone) {
       const int tok = k_tok + j * kAtTok;
       const bool on = good(k_page);
-      k_gone = !on && tok < tok_hi;
-      if (k_gone && lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
+      gone = !on && tok < tok_hi;
+      if (gone && lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
       const int64_t ph = on ? static_cast<int64_t>(k_page) * a.c.n_kv_heads + h : 0;
-      k_scale = on ? a.c.k_scales[ph] : 0.f;
+      scale = on ? a.c.k_scales[ph] : 0.f;
       const uint8_t* src = a.c.k_codes + ((ph << pshift) + (tok & (P - 1)) + (lane & 7)) * kD + (lane >> 3) * 16;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          kr[i][c] = make_uint4(0u, 0u, 0u, 0u);
-          if (on && tok + (lane & 7) + 8 * i < tok_hi)
-            kr[i][c] = __ldcg(reinterpret_cast<const uint4*>(src + 8 * i * kD + c * 64));
-        }
+      for (int c = 0; c < KC; ++c)
+        x[c] = on && tok + (lane & 7) < tok_hi ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
       k_page = page_of(tok + kAtTok);
     };
-    auto load_v = [&](int j) {
+    auto load_v = [&](int j, uint32_t (&x)[8], float& scale) {
+      const int tok = v_tok + j * kAtTok;
+      const bool on = good(v_page) && v_on;
+      const int64_t ph = on ? static_cast<int64_t>(v_page) * a.c.n_kv_heads + h : 0;
+      scale = on ? a.c.v_scales[ph] : 0.f;
+      const uint8_t* src = a.c.v_codes + ((ph << pshift) + (tok & (P - 1))) * kD + (w >> 1) * 32 + dg * 4;
+      const int n = on ? tok_hi - tok : 0;
 #pragma unroll
-      for (int p = 0; p < VP; ++p) {
-        const int u = w * VP + p, tok = v_tok[p] + j * kAtTok;
-        const bool on = good(v_page[p]);
-        const int64_t ph = on ? static_cast<int64_t>(v_page[p]) * a.c.n_kv_heads + h : 0;
-        v_scale[p] = on ? a.c.v_scales[ph] : 0.f;
-        const uint8_t* src = a.c.v_codes + ((ph << pshift) + (tok & (P - 1))) * kD + (u >> 2) * 32 + dg * 4;
-        const int n = on ? tok_hi - tok : 0;
+      for (int t = 0; t < 8; ++t) x[t] = t < n ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
+      v_page = page_of(tok + kAtTok);
+    };
+    auto store_k = [&](uint8_t* dst, const uint4 (&x)[KC], float scale) {
+      const float r = scale * k_inv;
+      const __half2 s2 = __floats2half2_rn(r, r);
+      uint8_t* rowp = dst + (w * 8 + (lane & 7)) * 128;
+      const int ch = 2 * (lane >> 3);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) vr[p][t] = t < n ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
-        v_page[p] = page_of(tok + kAtTok);
+      for (int c = 0; c < KC; ++c) {
+        const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          *reinterpret_cast<uint4*>(rowp + c * (kAtTok * 128) + (((ch + b) ^ (lane & 7)) << 4)) =
+              make_uint4(scaled_codes(y[2 * b], s2), scaled_codes(y[2 * b] >> 16, s2), scaled_codes(y[2 * b + 1], s2),
+                         scaled_codes(y[2 * b + 1] >> 16, s2));
       }
     };
-    auto store_k = [&](uint8_t* dst) {
-      const float r = k_scale * k_inv;
-      const __half2 ks2 = __floats2half2_rn(r, r);
+    auto store_v = [&](uint8_t* dst, const uint32_t (&x)[8], float scale) {
+      if (!v_on) return;
+      const float r = scale * v_inv;
+      const __half2 s2 = __floats2half2_rn(r, r);
+      const int ch = (w & 1) * 4 + tg;  // 8-token column
+      uint32_t o[4][4];                 // [element][token pair]
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t y = prmt(x[2 * t], x[2 * t + 1], 0x5140), z = prmt(x[2 * t], x[2 * t + 1], 0x7362);
+        o[0][t] = scaled_codes(y, s2);
+        o[1][t] = scaled_codes(y >> 16, s2);
+        o[2][t] = scaled_codes(z, s2);
+        o[3][t] = scaled_codes(z >> 16, s2);
+      }
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const int t = w * 16 + (lane & 7) + 8 * i;
-          const uint32_t x[4] = {kr[i][c].x, kr[i][c].y, kr[i][c].z, kr[i][c].w};
-          uint8_t* rowp = dst + c * (128 * 128) + t * 128;
-          const int ch = 2 * (lane >> 3);
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            *reinterpret_cast<uint4*>(rowp + (((ch + b) ^ (t & 7)) << 4)) =
-                make_uint4(scaled_codes(x[2 * b], ks2), scaled_codes(x[2 * b] >> 16, ks2),
-                           scaled_codes(x[2 * b + 1], ks2), scaled_codes(x[2 * b + 1] >> 16, ks2));
-        }
-    };
-    auto store_v = [&](uint8_t* dst) {
-#pragma unroll
-      for (int p = 0; p < VP; ++p) {
-        const int u = w * VP + p;
-        const float r = v_scale[p] * v_inv;
-        const __half2 vs2 = __floats2half2_rn(r, r);
-        const int ch = (u & 1) * 4 + tg;           // 8-token column within a 64-token half
-        uint8_t* base = dst + ((u & 3) >> 1) * (kD * 128);
-        uint32_t o[4][4];                          // [element][token pair]
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t x = prmt(vr[p][2 * t], vr[p][2 * t + 1], 0x5140);
-          const uint32_t y = prmt(vr[p][2 * t], vr[p][2 * t + 1], 0x7362);
-          o[0][t] = scaled_codes(x, vs2);
-          o[1][t] = scaled_codes(x >> 16, vs2);
-          o[2][t] = scaled_codes(y, vs2);
-          o[3][t] = scaled_codes(y >> 16, vs2);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int d = (u >> 2) * 32 + dg * 4 + k;
-          *reinterpret_cast<uint4*>(base + d * 128 + ((ch ^ (d & 7)) << 4)) =
-              make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int d = (w >> 1) * 32 + dg * 4 + k;
+        *reinterpret_cast<uint4*>(dst + d * 128 + ((ch ^ (d & 7)) << 4)) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
       }
     };
-    load_k(0);
-    load_v(0);
     bool ok = true;
-    for (int t = 0; ok && t < 2 * n_tiles; ++t) {
-      const int j = t >> 1;
+    auto begin = [&](int t) {
       ok = tc::warp_wait(kv_empty + t % kAtRing, ((t / kAtRing) & 1) ^ 1, abort_flag, a.status);
-      if (!ok) break;
-      uint8_t* dst = ring + (t % kAtRing) * C::TILE;
-      if (t & 1) {
-        store_v(dst);
-        if (j + 1 < n_tiles) load_v(j + 1);
-      } else {
-        if (lane == 0) reinterpret_cast<volatile uint8_t*>(bad + j % kAtBad)[w] = static_cast<uint8_t>(k_gone);
-        store_k(dst);
-        if (j + 1 < n_tiles) load_k(j + 1);
-      }
+      return ring + (t % kAtRing) * C::TILE;
+    };
+    auto end = [&](int t) {
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(kv_full + t % kAtRing);
+    };
+    auto put_k = [&](int j, uint4 (&x)[KC], float& scale, uint32_t& gone) {
+      if (j >= n_tiles || !ok) return;
+      uint8_t* dst = begin(t_k(j));
+      if (!ok) return;
+      if (lane == 0) reinterpret_cast<volatile uint8_t*>(bad + j % kAtBad)[w] = static_cast<uint8_t>(gone);
+      store_k(dst, x, scale);
+      end(t_k(j));
+      if (j + 2 < n_tiles) load_k(j + 2, x, scale, gone);
+    };
+    auto put_v = [&](int j, uint32_t (&x)[8], float& scale) {
+      if (j >= n_tiles || !ok) return;
+      uint8_t* dst = begin(t_v(j));
+      if (!ok) return;
+      store_v(dst, x, scale);
+      end(t_v(j));
+      if (j + 2 < n_tiles) load_v(j + 2, x, scale);
+    };
+    load_k(0, kr[0], k_scale[0], k_gone[0]);
+    load_v(0, vr[0], v_scale[0]);
+    load_k(1, kr[1], k_scale[1], k_gone[1]);
+    load_v(1, vr[1], v_scale[1]);
+    put_k(0, kr[0], k_scale[0], k_gone[0]);
+    put_k(1, kr[1], k_scale[1], k_gone[1]);
+    for (int j = 0; ok && j < n_tiles; j += 2) {
+      put_v(j, vr[0], v_scale[0]);
+      put_k(j + 2, kr[0], k_scale[0], k_gone[0]);
+      put_v(j + 1, vr[1], v_scale[1]);
+      put_k(j + 3, kr[1], k_scale[1], k_gone[1]);
     }
   }
   __syncwarp();
