@@ -8,8 +8,8 @@
 // two row tiles are half a step apart. (With 128-token tiles and one score buffer the chain scores ->
 // softmax -> product was the whole time: 5200 clocks per 128 tokens, of which the tensor cores
 // needed 2048.)
-//   warp 0         an elected lane issues the MMAs
-//   warp 1         owns the TMEM allocation: the score buffers (4 x 64 columns), O_0, O_1 (head_dim each)
+//   warps 0, 1     an elected lane issues the MMAs of row tile 0, 1
+//   warp 2         owns the TMEM allocation: the score buffers (4 x 64 columns), O_0, O_1 (head_dim each)
 //   warps 4-11     softmax, one thread per row: running reference and sum in fp32. O is rescaled only when
 //                  a score has grown by more than 2^8 over the reference (weights up to 2^8 are as exact
 //                  in f16 and the sums fp32), which after the first tiles is rare
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   uint64_t* p_full = s_full + 4;          // [row tile][buffer]
   uint64_t* pv_done = p_full + 4;         // [row tile][buffer]
   uint64_t* drain = pv_done + 4;
-  uint64_t* bad = drain + 1;              // [kAtBad], a byte per 8 tokens
+  uint64_t* bad = drain + 2;              // [kAtBad], a byte per 8 tokens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bad + kAtBad);
   __shared__ int abort_flag_s;
   __shared__ float s_ref[2][8];
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kAtRing; ++i) {
       tc::mbar_init(kv_full + i, 8);
-      tc::mbar_init(kv_empty + i, 1);
+      tc::mbar_init(kv_empty + i, n_rt);  // each row tile's MMAs
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(s_full + 2 * i, 1);
@@ -140,12 +140,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       tc::mbar_init(p_full + 2 * i + 1, 4);
       tc::mbar_init(pv_done + 2 * i, 1);
       tc::mbar_init(pv_done + 2 * i + 1, 1);
+      tc::mbar_init(drain + i, 1);
     }
-    tc::mbar_init(drain, 1);
     tc::fence_barrier_init();
     abort_flag_s = 0;
   }
-  if (warp == 1) {
+  if (warp == 2) {
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
@@ -217,55 +217,54 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   };
   if (warp < 4) {
     tc::reg_dec<48>();
-    if (warp == 0) {
-    // ------------------------------------------------------------------ MMA issuer
-    const uint32_t id_s = tc::idesc_f16(128, kAtTok), id_o = tc::idesc_f16(128, kD);
-    auto tile_at = [&](int t) { return tc::sw128_desc(tc::smem_u32(ring + (t % kAtRing) * C::TILE)); };
-    auto full = [&](int t) {
-      return tc::warp_wait(kv_full + t % kAtRing, (t / kAtRing) & 1, abort_flag, a.status);
-    };
-    // S_i(j) = Q_i K_j^T into buffer j & 1, which held P_i(j - 2): once the product that read it is done
-    auto scores = [&](int i, int j) {
-      if (j >= n_tiles || i >= n_rt) return true;
-      if (!full(t_k(j)) || (j >= 2 && !done(i, j - 2))) return false;
-      tc::tc_fence_after();
-      const uint64_t q = tc::sw128_desc(tc::smem_u32(smem + i * C::QTILE)), k = tile_at(t_k(j));
-      if (tc::elect_one()) {
+    if (warp < n_rt) {
+      // ---------------------------------------------------------------- MMA issuer of row tile i
+      const int i = warp;
+      const uint32_t id_s = tc::idesc_f16(128, kAtTok), id_o = tc::idesc_f16(128, kD);
+      const uint32_t ts = tmem + i * 128, to = tmem + 256 + i * 128;
+      const uint64_t q = tc::sw128_desc(tc::smem_u32(smem + i * C::QTILE));
+      auto tile_at = [&](int t) { return tc::sw128_desc(tc::smem_u32(ring + (t % kAtRing) * C::TILE)); };
+      auto full = [&](int t) {
+        return tc::warp_wait(kv_full + t % kAtRing, (t / kAtRing) & 1, abort_flag, a.status);
+      };
+      // S(j) = Q K_j^T into buffer j & 1, which held P(j - 2): once the product that read it is done
+      auto scores = [&](int j) {
+        if (!full(t_k(j)) || (j >= 2 && !done(i, j - 2))) return false;
+        tc::tc_fence_after();
+        const uint64_t k = tile_at(t_k(j));
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk)  // (64-wide pieces of Q are 16 KB apart, of K 8 KB, steps 32 bytes)
-          tc::mma_f16_ss(tmem + i * 128 + (j & 1) * 64, q + (kk >> 2) * 1024 + 2 * (kk & 3),
-                         k + (kk >> 2) * (kAtTok * 8) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
-        tc::mma_commit(s_full + 2 * i + (j & 1));
-        if (i == n_rt - 1) tc::mma_commit(kv_empty + t_k(j) % kAtRing);
-      }
-      __syncwarp();
-      return true;
-    };
-    // O_i += P_i(j) V_j
-    auto product = [&](int i, int j) {
-      if (i >= n_rt) return true;
-      if (!tc::warp_wait(p_full + 2 * i + (j & 1), (j >> 1) & 1, abort_flag, a.status) || !full(t_v(j))) return false;
-      tc::tc_fence_after();
-      const uint64_t v = tile_at(t_v(j));
-      if (tc::elect_one()) {
+          for (int kk = 0; kk < kD / 16; ++kk)  // (64-wide pieces of Q are 16 KB apart, of K 8 KB, steps 32 bytes)
+            tc::mma_f16_ss(ts + (j & 1) * 64, q + (kk >> 2) * 1024 + 2 * (kk & 3),
+                           k + (kk >> 2) * (kAtTok * 8) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
+          tc::mma_commit(s_full + 2 * i + (j & 1));
+          tc::mma_commit(kv_empty + t_k(j) % kAtRing);
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = scores(0) && (n_tiles < 2 || scores(1));
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        // O += P(j) V_j
+        ok = full(t_v(j)) && tc::warp_wait(p_full + 2 * i + (j & 1), (j >> 1) & 1, abort_flag, a.status);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t v = tile_at(t_v(j));
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kAtTok / 16; ++kk)
-          tc::mma_f16_ts(tmem + 256 + i * 128, tmem + i * 128 + (j & 1) * 64 + 32 + 8 * kk, v + 2 * kk, id_o,
-                         (j | kk) ? 1u : 0u);
-        tc::mma_commit(pv_done + 2 * i + (j & 1));
-        if (i == n_rt - 1) tc::mma_commit(kv_empty + t_v(j) % kAtRing);
+          for (int kk = 0; kk < kAtTok / 16; ++kk)
+            tc::mma_f16_ts(to, ts + (j & 1) * 64 + 32 + 8 * kk, v + 2 * kk, id_o, (j | kk) ? 1u : 0u);
+          tc::mma_commit(pv_done + 2 * i + (j & 1));
+          tc::mma_commit(kv_empty + t_v(j) % kAtRing);
+        }
+        __syncwarp();
+        if (j + 2 < n_tiles) ok = scores(j + 2);
       }
-      __syncwarp();
-      return true;
-    };
-    bool ok = scores(0, 0) && scores(1, 0) && scores(0, 1);
-    for (int j = 0; ok && j < n_tiles; ++j)
-      ok = product(0, j) && scores(1, j + 1) && product(1, j) && scores(0, j + 2);
-    if (!ok) {  // drain every MMA issued so far before TMEM is released
-      if (tc::elect_one()) tc::mma_commit(drain);
-      __syncwarp();
-      tc::mbar_wait_drain(drain, 0);
-    }
+      if (!ok) {  // drain every MMA issued so far before TMEM is released
+        if (tc::elect_one()) tc::mma_commit(drain + i);
+        __syncwarp();
+        tc::mbar_wait_drain(drain + i, 0);
+      }
     }
     __syncwarp();
   } else if (warp < 12) {
@@ -502,7 +501,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 2) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
