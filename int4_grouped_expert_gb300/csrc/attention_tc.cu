@@ -14,7 +14,7 @@
 //                  a score has grown by more than 2^8 over the reference (weights up to 2^8 are as exact
 //                  in f16 and the sums fp32), which after the first tiles is rare
 //   warps 12-19    codes -> f16 tiles in shared memory, K as it lies and V transposed (bytes of two
-//                  tokens paired with PRMT), a ring of 8 tiles in the order K0, K1, V0, K2, V1, ...
+//                  tokens paired with PRMT), a ring of 4 stages: (K0, K1), (V0, K2), (V1, K3), ...
 // A page's scale relative to the largest of the block's pages multiplies its codes on the way: exact for
 // powers of two down to 2^-15, absolute error below 2^-25 of the largest scale beyond.
 // Queries become f16 with a power of two per row; a token that no row sees or in a page that does not
@@ -31,7 +31,7 @@ namespace strata {
 namespace {
 
 constexpr int kAtTok = 64;      // tokens per tile
-constexpr int kAtRing = 8;      // tiles of codes converted to f16
+constexpr int kAtRing = 4;      // stages of two tiles of codes converted to f16
 constexpr int kAtThreads = 640;
 constexpr int kAtBad = 8;       // ring of per-tile masks of tokens in pages that do not exist
 
@@ -39,7 +39,7 @@ template <int kD>
 struct AtCfg {
   static constexpr int QTILE = 128 * kD * 2;   // bytes of a row tile of Q in f16
   static constexpr int TILE = kAtTok * kD * 2; // of a tile of K or V
-  static constexpr size_t SMEM = 2 * QTILE + static_cast<size_t>(kAtRing) * TILE + 1024 + 512;
+  static constexpr size_t SMEM = 2 * QTILE + static_cast<size_t>(kAtRing) * 2 * TILE + 1024 + 512;
 };
 
 __device__ __forceinline__ uint32_t scaled_codes(uint32_t two, __half2 s) {
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem + 2 * C::QTILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kAtRing * C::TILE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kAtRing * 2 * C::TILE);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + kAtRing;
   uint64_t* s_full = kv_empty + kAtRing;  // [row tile][buffer]
@@ -207,9 +207,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 
   // registers: 5 warpgroups are launched with 96 a thread (61440 in all) and go on with
   // 48 + 2 * 136 + 2 * 80 (the same)
-  // places of K_j and V_j in the order of the ring
-  auto t_k = [](int j) { return j < 2 ? j : 2 * j - 1; };
-  auto t_v = [](int j) { return 2 * j + 2; };
+  // stage 0 holds K_0 and K_1, stage j + 1 V_j and K_(j+2): what the product of step j and the scores after
+  // it read
   // O_i += P_i(j) V_j is done. Barriers of step j are per buffer (j & 1): whoever waits for one knows that
   // the step before it on the same buffer is over, and that no later one has begun.
   auto done = [&](int i, int j) {
@@ -223,42 +222,53 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       const uint32_t id_s = tc::idesc_f16(128, kAtTok), id_o = tc::idesc_f16(128, kD);
       const uint32_t ts = tmem + i * 128, to = tmem + 256 + i * 128;
       const uint64_t q = tc::sw128_desc(tc::smem_u32(smem + i * C::QTILE));
-      auto tile_at = [&](int t) { return tc::sw128_desc(tc::smem_u32(ring + (t % kAtRing) * C::TILE)); };
+      auto stage_at = [&](int t) { return tc::sw128_desc(tc::smem_u32(ring + (t % kAtRing) * 2 * C::TILE)); };
       auto full = [&](int t) {
         return tc::warp_wait(kv_full + t % kAtRing, (t / kAtRing) & 1, abort_flag, a.status);
       };
-      // S(j) = Q K_j^T into buffer j & 1, which held P(j - 2): once the product that read it is done
-      auto scores = [&](int j) {
-        if (!full(t_k(j)) || (j >= 2 && !done(i, j - 2))) return false;
-        tc::tc_fence_after();
-        const uint64_t k = tile_at(t_k(j));
-        if (tc::elect_one()) {
+      // S(j) = Q K_j^T into buffer j & 1 (one lane)
+      auto scores = [&](int j, uint64_t k) {
 #pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk)  // (64-wide pieces of Q are 16 KB apart, of K 8 KB, steps 32 bytes)
-            tc::mma_f16_ss(ts + (j & 1) * 64, q + (kk >> 2) * 1024 + 2 * (kk & 3),
-                           k + (kk >> 2) * (kAtTok * 8) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
-          tc::mma_commit(s_full + 2 * i + (j & 1));
-          tc::mma_commit(kv_empty + t_k(j) % kAtRing);
+        for (int kk = 0; kk < kD / 16; ++kk)  // (64-wide pieces of Q are 16 KB apart, of K 8 KB, steps 32 bytes)
+          tc::mma_f16_ss(ts + (j & 1) * 64, q + (kk >> 2) * 1024 + 2 * (kk & 3),
+                         k + (kk >> 2) * (kAtTok * 8) + 2 * (kk & 3), id_s, kk ? 1u : 0u);
+        tc::mma_commit(s_full + 2 * i + (j & 1));
+      };
+      constexpr uint64_t kSecond = C::TILE >> 4;  // descriptor distance of a stage's second tile
+      bool ok = full(0);
+      if (ok) {
+        tc::tc_fence_after();
+        const uint64_t k = stage_at(0);
+        if (tc::elect_one()) {
+          scores(0, k);
+          if (n_tiles > 1) scores(1, k + kSecond);
+          tc::mma_commit(kv_empty);
         }
         __syncwarp();
-        return true;
-      };
-      bool ok = scores(0) && (n_tiles < 2 || scores(1));
+      }
       for (int j = 0; ok && j < n_tiles; ++j) {
         // O += P(j) V_j
-        ok = full(t_v(j)) && tc::warp_wait(p_full + 2 * i + (j & 1), (j >> 1) & 1, abort_flag, a.status);
+        ok = full(j + 1) && tc::warp_wait(p_full + 2 * i + (j & 1), (j >> 1) & 1, abort_flag, a.status);
         if (!ok) break;
         tc::tc_fence_after();
-        const uint64_t v = tile_at(t_v(j));
+        const uint64_t v = stage_at(j + 1);
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kAtTok / 16; ++kk)
             tc::mma_f16_ts(to, ts + (j & 1) * 64 + 32 + 8 * kk, v + 2 * kk, id_o, (j | kk) ? 1u : 0u);
           tc::mma_commit(pv_done + 2 * i + (j & 1));
-          tc::mma_commit(kv_empty + t_v(j) % kAtRing);
         }
         __syncwarp();
-        if (j + 2 < n_tiles) ok = scores(j + 2);
+        if (j + 2 >= n_tiles) continue;  // (the last stages are not filled again)
+        // the next scores go where these weights are: once the product that reads them is done
+        ok = done(i, j);
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+          scores(j + 2, v + kSecond);
+          tc::mma_commit(kv_empty + (j + 1) % kAtRing);
+        }
+        __syncwarp();
       }
       if (!ok) {  // drain every MMA issued so far before TMEM is released
         if (tc::elect_one()) tc::mma_commit(drain + i);
@@ -461,41 +471,43 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     bool ok = true;
     auto begin = [&](int t) {
       ok = tc::warp_wait(kv_empty + t % kAtRing, ((t / kAtRing) & 1) ^ 1, abort_flag, a.status);
-      return ring + (t % kAtRing) * C::TILE;
+      return ring + (t % kAtRing) * 2 * C::TILE;
     };
     auto end = [&](int t) {
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(kv_full + t % kAtRing);
     };
-    auto put_k = [&](int j, uint4 (&x)[KC], float& scale, uint32_t& gone) {
-      if (j >= n_tiles || !ok) return;
-      uint8_t* dst = begin(t_k(j));
-      if (!ok) return;
+    auto put_k = [&](int j, uint8_t* dst, const uint4 (&x)[KC], float scale, uint32_t gone) {
       if (lane == 0) reinterpret_cast<volatile uint8_t*>(bad + j % kAtBad)[w] = static_cast<uint8_t>(gone);
       store_k(dst, x, scale);
-      end(t_k(j));
-      if (j + 2 < n_tiles) load_k(j + 2, x, scale, gone);
     };
-    auto put_v = [&](int j, uint32_t (&x)[8], float& scale) {
+    // stage j + 1: V_j and K_(j+2); then the codes of V_(j+2) and K_(j+4) start
+    auto put = [&](int j, uint32_t (&xv)[8], float& sv_, uint4 (&xk)[KC], float& sk, uint32_t& gone) {
       if (j >= n_tiles || !ok) return;
-      uint8_t* dst = begin(t_v(j));
+      uint8_t* dst = begin(j + 1);
       if (!ok) return;
-      store_v(dst, x, scale);
-      end(t_v(j));
-      if (j + 2 < n_tiles) load_v(j + 2, x, scale);
+      store_v(dst, xv, sv_);
+      if (j + 2 < n_tiles) put_k(j + 2, dst + C::TILE, xk, sk, gone);
+      end(j + 1);
+      if (j + 2 < n_tiles) load_v(j + 2, xv, sv_);
+      if (j + 4 < n_tiles) load_k(j + 4, xk, sk, gone);
     };
     load_k(0, kr[0], k_scale[0], k_gone[0]);
-    load_v(0, vr[0], v_scale[0]);
     load_k(1, kr[1], k_scale[1], k_gone[1]);
+    load_v(0, vr[0], v_scale[0]);
     load_v(1, vr[1], v_scale[1]);
-    put_k(0, kr[0], k_scale[0], k_gone[0]);
-    put_k(1, kr[1], k_scale[1], k_gone[1]);
+    uint8_t* dst = begin(0);
+    if (ok) {
+      put_k(0, dst, kr[0], k_scale[0], k_gone[0]);
+      put_k(1, dst + C::TILE, kr[1], k_scale[1], k_gone[1]);
+      end(0);
+      load_k(2, kr[0], k_scale[0], k_gone[0]);
+      load_k(3, kr[1], k_scale[1], k_gone[1]);
+    }
     for (int j = 0; ok && j < n_tiles; j += 2) {
-      put_v(j, vr[0], v_scale[0]);
-      put_k(j + 2, kr[0], k_scale[0], k_gone[0]);
-      put_v(j + 1, vr[1], v_scale[1]);
-      put_k(j + 3, kr[1], k_scale[1], k_gone[1]);
+      put(j, vr[0], v_scale[0], kr[0], k_scale[0], k_gone[0]);
+      put(j + 1, vr[1], v_scale[1], kr[1], k_scale[1], k_gone[1]);
     }
   }
   __syncwarp();
