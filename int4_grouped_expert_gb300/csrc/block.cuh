@@ -7,7 +7,10 @@
 namespace strata {
 
 // Up to this many tokens a projection streams its codes through registers (linear.cu).
-constexpr int kLinearStreamT = STRATA_LINEAR_STREAM_T;
+constexpr int kLinearStreamT = 8;
+// Beyond that and up to this many, the tensor cores multiply x with weights in two bf16 parts
+// (linear_tc.cu); more tokens take f16 operands.
+constexpr int kLinearMidT = STRATA_LINEAR_EXACT_T;
 
 // The power of two that a row of f16 operands is divided by, for its largest bf16 magnitude (key as
 // bf16x8_mag): it brings the row's largest entry to [8, 16), so that rows of any size keep their

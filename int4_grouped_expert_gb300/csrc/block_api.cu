@@ -40,7 +40,7 @@ struct LinearLayout {
 LinearLayout linear_layout(const strata_linear* w, int64_t T) {
   LinearLayout L{};
   L.xexp = sizeof(WsHeader);
-  const int64_t rows = T > kLinearStreamT ? T : 0;
+  const int64_t rows = T > kLinearMidT ? T : 0;
   L.xh = round_up(L.xexp + sizeof(int) * rows);
   L.total = round_up(L.xh + sizeof(uint16_t) * rows * w->K);
   return L;
@@ -140,7 +140,6 @@ strata_status strata_linear_forward(const strata_linear* w, const void* x_bf16, 
   a.xh = reinterpret_cast<__half*>(base + L.xh);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (T <= kLinearStreamT) return of(launch_linear_stream(a, st));
-  if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st) != cudaSuccess) return STRATA_ERR_CUDA;
   int sms = 0;
   if (!sm_count(&sms)) return STRATA_ERR_CUDA;
   return of(launch_linear_tc(a, sms, st));

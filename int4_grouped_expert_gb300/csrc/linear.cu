@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kLinWarps * 32) linear_stream_kernel(LinearArg
   __shared__ float red[kLinWarps][16][COLS + 1];
   griddep_wait();
   griddep_launch();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * 16;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * COLS;

@@ -1,23 +1,28 @@
-// Projections with group-quantized weights for many tokens, on tcgen05: out[t][n] = sum_c x[t][c] w[n][c]
-// with w = f16(q * s) ("Strata" MoE tuning notes, lpnh.cn/news/2730718, §2.1: G codes share one scale).
+// Projections with group-quantized weights on tcgen05: out[t][n] = sum_c x[t][c] w[n][c], w = q * s ("Strata"
+// MoE tuning notes, lpnh.cn/news/2730718, §2.1: G codes share one scale).
 //
 // Tile: 128 weight rows (the MMA's M, one TMEM lane each) x up to 256 tokens, contraction in 64-wide
 // stages. The weights are the A operand and go to tensor memory, not shared memory: a thread
 // dequantizes 64 codes of its row and stores them to its own TMEM lane, so shared memory carries only
 // the activations. (Both operands in shared memory would move 96 KB a stage, 188 bytes a clock at the
 // MMA's pace, and 128 is what shared memory has; this way it is 64 KB.)
-//   warp 0       TMA (one elected lane): the stage's tokens (f16, 128-byte swizzle) -> a ring in shared memory
-//   warp 1       an elected lane issues tcgen05.mma (f16, M = 128, N = tokens, K = 16)
-//   warp 2       owns the TMEM allocation: 256 columns of sums, 8 stages x 32 columns of weights
+//   warp 0       TMA (one elected lane): the stage's tokens (16-bit, 128-byte swizzle) -> a ring in
+//                shared memory
+//   warp 1       an elected lane issues tcgen05.mma (M = 128, N = tokens, K = 16)
+//   warp 2       owns the TMEM allocation: the sums, then a ring of weight stages
 //   warps 4-11   dequantize: two warps per 32 lanes, one for the even and one for the odd stages
 //   warps 12-15  epilogue: TMEM -> registers -> bias, residual -> bf16
 // Blocks are persistent over the tiles. Where the tiles are too few to fill the GPU, a cluster of 2 to
 // 8 blocks shares a tile along the contraction; the sums meet in shared memory over the cluster, in
 // the order of the ranks.
 //
-// Operands are f16: the weight is the exact code times the fp16 scale, rounded once (2^-11 relative; bf16
-// would leave 2^-8), and a pass before this kernel copies x to f16, each row times a power of two that
-// keeps its range; the epilogue multiplies it back.
+// Two operand forms:
+//   up to 128 tokens (kMid)  streaming the codes is what bounds it, so x stays as it is (bf16, no pass
+//       before) and the weight is two bf16 numbers, hi + lo = q * s to 2^-16 of it: with s = s1 + s2 in bf16
+//       (exact), hi = q * s1 rounded, lo = (q * s1 - hi) + q * s2 (the first term exact); two MMAs.
+//   more tokens              the MMAs bound it: f16 operands, w = q * s rounded once (2^-11; bf16 would
+//       leave 2^-8), and a pass before copies x to f16, each row times a power of two that keeps its
+//       range; the epilogue multiplies it back.
 //
 // Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every role
 // leaves its loop, in-flight copies and MMAs are drained (bounded) and TMEM is freed.
@@ -32,15 +37,40 @@ namespace strata {
 
 namespace {
 
-constexpr int kLtRows = 128;              // weight rows per tile
-constexpr int kLtTok = 256;               // tokens per tile
-constexpr int kLtBK = 64;                 // contraction per stage
-constexpr int kLtAStages = 8;             // weight stages in TMEM, 32 columns each
-constexpr int kLtBStages = 6;             // activation stages in shared memory
-constexpr int kLtBBytes = kLtTok * kLtBK * 2;
-constexpr int kLtBox = 64;                // token rows per TMA box
+constexpr int kLtRows = 128;  // weight rows per tile
+constexpr int kLtBK = 64;     // contraction per stage
 constexpr int kLtThreads = 512;
-constexpr size_t kLtSmem = static_cast<size_t>(kLtBStages) * kLtBBytes + 1024 + 512;
+template <bool kMid>
+struct LtCfg {
+  static constexpr int TOK = kMid ? 128 : 256;       // tokens per tile
+  static constexpr int A_COLS = kMid ? 64 : 32;      // TMEM columns of a weight stage
+  static constexpr int STAGES = 6;                   // weights in TMEM (at most 384 columns), tokens in smem
+  static constexpr int B_BYTES = TOK * kLtBK * 2;
+  static constexpr int BOX = kMid ? 16 : 64;         // token rows per TMA box
+  static constexpr size_t SMEM = static_cast<size_t>(STAGES) * B_BYTES + 1024 + 512;
+};
+
+// bf16x2 of two codes, exact. 4 bits: codes 2 byte, 2 byte + 1 of an 8-code word; w4 is the word >> 4.
+__device__ __forceinline__ __nv_bfloat162 lt_pair4_bf16(uint32_t w, uint32_t w4, int byte) {
+  const uint32_t v = prmt(w, w4, byte | (byte + 4) << 8);  // low nibbles of bytes 0 and 2: the codes
+  uint32_t d;  // (v & 0x000F000F) ^ 0x43084308: 136 + q
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(v), "n"(0x000F000F), "n"(0x43084308));
+  return __hsub2(*reinterpret_cast<__nv_bfloat162*>(&d), __floats2bfloat162_rn(136.f, 136.f));
+}
+// 8 bits: 128 + (low 7 bits) minus 128, or 256 where the sign bit is set.
+__device__ __forceinline__ __nv_bfloat162 lt_pair8_bf16(uint32_t w, int pair) {
+  const uint32_t v = prmt(w, 0u, pair ? 0x4342 : 0x4140);
+  const uint32_t m = (v & 0x007F007Fu) | 0x43004300u, b = (v & 0x00800080u) | 0x43004300u;
+  return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&b));
+}
+// q * (s1 + s2) as hi + lo
+__device__ __forceinline__ void lt_split(__nv_bfloat162 q, __nv_bfloat162 s1, __nv_bfloat162 s2, uint32_t& hi,
+                                         uint32_t& lo) {
+  const __nv_bfloat162 h = __hmul2(q, s1);
+  const __nv_bfloat162 l = __hfma2(q, s2, __hfma2(q, s1, __hneg2(h)));
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
 
 // f16x2 of two codes, exact. 4 bits: codes 2 byte, 2 byte + 1 of an 8-code word; w4 is the word >> 4.
 __device__ __forceinline__ __half2 lt_pair4(uint32_t w, uint32_t w4, int byte) {
@@ -61,10 +91,12 @@ __device__ __forceinline__ uint32_t lt_scaled(__half2 q, __half2 s) {
 
 // f16 copy of the rows of x, each times 2^-e (its largest entry in [8, 16)), and e.
 __global__ void __launch_bounds__(256) linear_rows_kernel(const __nv_bfloat16* __restrict__ x, int64_t stride,
-                                                          int K, __half* __restrict__ xh, int* __restrict__ xexp) {
+                                                          int K, __half* __restrict__ xh, int* __restrict__ xexp,
+                                                          uint32_t* status) {
   __shared__ uint32_t s_mag[8];
   griddep_wait();
   griddep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   const uint4* src = reinterpret_cast<const uint4*>(x + blockIdx.x * stride);
   uint4* dst = reinterpret_cast<uint4*>(xh + static_cast<int64_t>(blockIdx.x) * K);
   uint32_t m = 0;
@@ -96,18 +128,17 @@ __device__ __forceinline__ float lt_epilogue(const LinearArgs& a, float y, float
   return y;
 }
 
-template <int kBits>
+template <int kBits, bool kMid>
 __global__ void __launch_bounds__(kLtThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, LinearArgs a, int ks) {
+  using C = LtCfg<kMid>;
   extern __shared__ uint8_t lt_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lt_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kLtBStages * kLtBBytes);
-  uint64_t* full_a = bars;
-  uint64_t* empty_a = full_a + kLtAStages;
-  uint64_t* full_b = empty_a + kLtAStages;
-  uint64_t* empty_b = full_b + kLtBStages;
-  uint64_t* acc_full = empty_b + kLtBStages;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::B_BYTES);
+  uint64_t* full = bars;                  // a stage's weights and tokens are in place
+  uint64_t* empty = full + C::STAGES;     // its MMAs are done
+  uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* drain = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -116,13 +147,9 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kLtAStages; ++s) {
-      tc::mbar_init(full_a + s, 4);   // one warp per lane quarter
-      tc::mbar_init(empty_a + s, 1);
-    }
-    for (int s = 0; s < kLtBStages; ++s) {
-      tc::mbar_init(full_b + s, 1);
-      tc::mbar_init(empty_b + s, 1);
+    for (int s = 0; s < C::STAGES; ++s) {
+      tc::mbar_init(full + s, 5);   // four dequant warps (one per lane quarter) and the TMA
+      tc::mbar_init(empty + s, 1);
     }
     tc::mbar_init(acc_full, 1);
     tc::mbar_init(acc_empty, 4);      // the epilogue warps
@@ -139,68 +166,85 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tmem_a = tmem + kLtTok;
+  const uint32_t tmem_a = tmem + C::TOK;
   griddep_wait();
   griddep_launch();
+  if (kMid && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;  // (else the pass before has cleared it)
 
   // tile = (token block, 128 weight rows), weight rows fastest
   const int mtiles = (a.N + kLtRows - 1) / kLtRows;
-  const int ttiles = static_cast<int>((a.T + kLtTok - 1) / kLtTok);
+  const int ttiles = static_cast<int>((a.T + C::TOK - 1) / C::TOK);
   const int n_items = mtiles * ttiles;
   const int rank = blockIdx.x % ks, step = gridDim.x / ks;
   const int nk_all = a.K / kLtBK;
   const int kb0 = nk_all * rank / ks, nk = nk_all * (rank + 1) / ks - kb0;  // this rank's stages
   auto tokens = [&](int item) {
-    return static_cast<int>(min(static_cast<int64_t>(kLtTok), a.T - static_cast<int64_t>(item / mtiles) * kLtTok));
+    return static_cast<int>(min(static_cast<int64_t>(C::TOK), a.T - static_cast<int64_t>(item / mtiles) * C::TOK));
   };
 
   if (warp == 0) {
     int it = 0;
     bool ok = true;
     for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
-      const int nbox = (tokens(item) + kLtBox - 1) / kLtBox;
-      const int t0 = item / mtiles * kLtTok;
+      const int nbox = (tokens(item) + C::BOX - 1) / C::BOX;
+      const int t0 = item / mtiles * C::TOK;
       for (int kb = 0; kb < nk; ++kb, ++it) {
-        const int s = it % kLtBStages;
-        ok = tc::warp_wait(empty_b + s, ((it / kLtBStages) & 1) ^ 1, abort_flag, a.status);
+        const int s = it % C::STAGES;
+        ok = tc::warp_wait(empty + s, ((it / C::STAGES) & 1) ^ 1, abort_flag, a.status);
         if (!ok) break;
         if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(full_b + s, nbox * kLtBox * kLtBK * 2);
+          tc::mbar_arrive_expect_tx(full + s, nbox * C::BOX * kLtBK * 2);
           for (int bx = 0; bx < nbox; ++bx)
-            tc::tma_load_2d(smem + s * kLtBBytes + bx * kLtBox * kLtBK * 2, &tmap_x, (kb0 + kb) * kLtBK,
-                            t0 + bx * kLtBox, full_b + s);
+            tc::tma_load_2d(smem + s * C::B_BYTES + bx * C::BOX * kLtBK * 2, &tmap_x, (kb0 + kb) * kLtBK,
+                            t0 + bx * C::BOX, full + s);
         }
         __syncwarp();
       }
     }
-    if (!ok)  // drain the copies that may still be in flight
-      for (int j = (it > kLtBStages ? it - kLtBStages : 0); j < it; ++j)
-        tc::mbar_wait_drain(full_b + (j % kLtBStages), (j / kLtBStages) & 1);
+    if (!ok) {
+      // drain the copies that may still be in flight (a stage that its dequant warps have left does not
+      // complete: the wait is bounded, and so is the copies' time)
+      for (int j = (it > C::STAGES ? it - C::STAGES : 0); j < it; ++j)
+        tc::mbar_wait_drain(full + (j % C::STAGES), (j / C::STAGES) & 1);
+    }
     __syncwarp();
   } else if (warp == 1) {
-    int it = 0, tcount = 0;
-    bool ok = true;
+    // The loop looks at the next stage's barrier while this stage's MMAs are issued: a wait costs about 100
+    // clocks even when there is nothing to wait for.
+    int s = 0, tcount = 0;
+    uint32_t ph = 0;
+    bool ok = true, ready = false;
+    const uint64_t db0 = tc::sw128_desc(tc::smem_u32(smem));
     for (int item = blockIdx.x / ks; ok && item < n_items; item += step, ++tcount) {
-      const uint32_t idesc = tc::idesc_f16(kLtRows, (tokens(item) + 15) & ~15);
+      const int n_mma = (tokens(item) + 15) & ~15;
+      const uint32_t idesc = kMid ? tc::idesc_bf16(kLtRows, n_mma) : tc::idesc_f16(kLtRows, n_mma);
       ok = tcount == 0 || tc::warp_wait(acc_empty, (tcount - 1) & 1, abort_flag, a.status);
       if (!ok) break;
       tc::tc_fence_after();
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        const int sa = it % kLtAStages, sb = it % kLtBStages;
-        ok = tc::warp_wait(full_b + sb, (it / kLtBStages) & 1, abort_flag, a.status) &&
-             tc::warp_wait(full_a + sa, (it / kLtAStages) & 1, abort_flag, a.status);
-        if (!ok) break;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!ready) {
+          ok = tc::warp_wait(full + s, ph, abort_flag, a.status);
+          if (!ok) break;
+        }
         tc::tc_fence_after();
-        const uint64_t db = tc::sw128_desc(tc::smem_u32(smem + sb * kLtBBytes));
+        const int s1 = s + 1 == C::STAGES ? 0 : s + 1;
+        const uint32_t ph1 = s + 1 == C::STAGES ? ph ^ 1 : ph;
+        const bool next = tc::mbar_test(full + s1, ph1);
         if (tc::elect_one()) {
+          const uint64_t db = db0 + s * (C::B_BYTES >> 4);
+          const uint32_t da = tmem_a + s * C::A_COLS;
 #pragma unroll
-          for (int kk = 0; kk < kLtBK / 16; ++kk)
-            tc::mma_f16_ts(tmem, tmem_a + sa * 32 + 8 * kk, db + 2 * kk, idesc, (kb | kk) ? 1u : 0u);
-          tc::mma_commit(empty_a + sa);
-          tc::mma_commit(empty_b + sb);
+          for (int kk = 0; kk < kLtBK / 16; ++kk) {
+            tc::mma_f16_ts(tmem, da + 8 * kk, db + 2 * kk, idesc, (kb | kk) ? 1u : 0u);
+            if (kMid) tc::mma_f16_ts(tmem, da + 32 + 8 * kk, db + 2 * kk, idesc, 1u);
+          }
+          tc::mma_commit(empty + s);
           if (kb == nk - 1) tc::mma_commit(acc_full);
         }
         __syncwarp();
+        ready = __all_sync(0xffffffffu, next);
+        s = s1;
+        ph = ph1;
       }
     }
     if (!ok) {  // drain every MMA issued so far before TMEM is released
@@ -242,28 +286,32 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         for (int u = 0; u < PD; ++u) {
           const int m = m0 + u;
           if (m >= mine) break;
-          const int it = it0 + first + 2 * m, s = it % kLtAStages;
+          const int it = it0 + first + 2 * m, s = it % C::STAGES;
           const __half sh = __ushort_as_half(sw[u]);
           const __half2 s2 = __halves2half2(sh, sh);
-          uint32_t w[32];
+          const float sf = __half2float(sh);
+          const __nv_bfloat16 sb1 = __float2bfloat16_rn(sf), sb2 = __float2bfloat16_rn(sf - __bfloat162float(sb1));
+          const __nv_bfloat162 b1 = __halves2bfloat162(sb1, sb1), b2 = __halves2bfloat162(sb2, sb2);
+          uint32_t w[32], wl[kMid ? 32 : 1];
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
             const uint32_t c[4] = {cw[u][v].x, cw[u][v].y, cw[u][v].z, cw[u][v].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              if (kBits == 4) {
-                const uint32_t c4 = c[j] >> 4;
+              const uint32_t other = kBits == 4 ? c[j] >> 4 : c[j] ^ 0x80808080u;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) w[(16 * v + 4 * j + b) & 31] = lt_scaled(lt_pair4(c[j], c4, b), s2);
-              } else {
-                const uint32_t cu = c[j] ^ 0x80808080u;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) w[(8 * v + 2 * j + b) & 31] = lt_scaled(lt_pair8(cu, b), s2);
+              for (int b = 0; b < 16 / kBits; ++b) {
+                const int at = (16 / kBits * (4 * v + j) + b) & 31;
+                if (kMid)
+                  lt_split(kBits == 4 ? lt_pair4_bf16(c[j], other, b) : lt_pair8_bf16(c[j], b), b1, b2, w[at],
+                           wl[kMid ? at : 0]);
+                else
+                  w[at] = lt_scaled(kBits == 4 ? lt_pair4(c[j], other, b) : lt_pair8(other, b), s2);
               }
             }
           }
           // weights of the largest fp16 magnitudes may round to inf: they stay finite (nan stays nan)
-          if (__half2float(sh) > 65504.f / (kBits == 4 ? 8 : 128)) {
+          if (!kMid && sf > 65504.f / (kBits == 4 ? 8 : 128)) {
             const __half2 top = __floats2half2_rn(65504.f, 65504.f);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -273,14 +321,15 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           }
           load(m + PD, u);
           // (the whole warp goes on or leaves: the TMEM instructions are warp-wide)
-          ok = tc::warp_wait(empty_a + s, ((it / kLtAStages) & 1) ^ 1, abort_flag, a.status);
+          ok = tc::warp_wait(empty + s, ((it / C::STAGES) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
           tc::tc_fence_after();
-          tc::tmem_st32(lane_addr + s * 32, w);
+          tc::tmem_st32(lane_addr + s * C::A_COLS, w);
+          if constexpr (kMid) tc::tmem_st32(lane_addr + s * C::A_COLS + 32, wl);
           tc::tmem_st_wait();
           tc::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(full_a + s);
+          if (lane == 0) tc::mbar_arrive(full + s);
         }
       }
     }
@@ -293,18 +342,20 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       if (!tc::warp_wait(acc_full, tcount & 1, abort_flag, a.status)) break;
       tc::tc_fence_after();
       const int n = item % mtiles * kLtRows + q4 * 32 + lane;
-      const int64_t t0 = static_cast<int64_t>(item / mtiles) * kLtTok;
+      const int64_t t0 = static_cast<int64_t>(item / mtiles) * C::TOK;
       const int nt = tokens(item);
       const float bias = a.bias && n < a.N ? a.bias[n] : 0.f;
       float* sums = reinterpret_cast<float*>(smem);  // ks > 1: [token][row], in place of the stages
       for (int c = 0; c < nt; c += 32) {
         uint32_t r[32];
         tc::tmem_ld32(lane_addr + c, r);
-        const float my_up = c + lane < nt ? exp2i(a.xexp[t0 + c + lane]) : 0.f;
+        const float my_up = !kMid && c + lane < nt ? exp2i(a.xexp[t0 + c + lane]) : 0.f;
         tc::tmem_ld_wait();
+        if (!kMid) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(0xffffffffu, my_up, j));
+          for (int j = 0; j < 32; ++j)
+            r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(0xffffffffu, my_up, j));
+        }
         if (ks > 1) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -329,7 +380,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     const int item = blockIdx.x / ks;
     const int nt = tokens(item), r = threadIdx.x & (kLtRows - 1);
     const int n = item % mtiles * kLtRows + r;
-    const int64_t t0 = static_cast<int64_t>(item / mtiles) * kLtTok;
+    const int64_t t0 = static_cast<int64_t>(item / mtiles) * C::TOK;
     if (n < a.N && !abort_flag_s) {
       const float bias = a.bias ? a.bias[n] : 0.f;
       const uint32_t base = tc::smem_u32(smem) + r * 4;
@@ -363,15 +414,46 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-template <int kBits>
-cudaError_t launch_tc_t(const CUtensorMap& map, const LinearArgs& a, int ks, unsigned grid, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<kBits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kLtSmem));
+template <int kBits, bool kMid>
+cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
+  using C = LtCfg<kMid>;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return cudaErrorInvalidValue;
+  if (!kMid) {
+    const cudaError_t e = launch_kernel(linear_rows_kernel, dim3(static_cast<unsigned>(a.T)), dim3(256), 0, stream,
+                                        true, a.x, a.x_stride, a.K, a.xh, a.xexp, a.status);
+    if (e != cudaSuccess) return e;
+  }
+  // the tokens (x itself, or its f16 copy) as a 2-d tensor: boxes of BOX tokens x 64 columns (128 bytes),
+  // zero fill past the last token
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kMid ? a.x_stride : a.K) * 2};
+  const cuuint32_t box[2] = {kLtBK, C::BOX}, estr[2] = {1, 1};
+  if (enc(&map, kMid ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+          kMid ? const_cast<void*>(static_cast<const void*>(a.x)) : static_cast<void*>(a.xh), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const int64_t items = static_cast<int64_t>((a.N + kLtRows - 1) / kLtRows) * ((a.T + C::TOK - 1) / C::TOK);
+  const int nk = a.K / kLtBK;
+  // contraction splits: stages of a share + about 8 stages' worth of start, drain and join, only while a
+  // tile per cluster fits the GPU at once. Clusters of k blocks of this size that 152 SMs hold (the
+  // GPU processing clusters leave some SMs over): 76, 46, 36, 28, 23, 15, 15 for k = 2 .. 8.
+  constexpr int kHeld[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+  int ks = 1;
+  int64_t best = (items + num_sms - 1) / num_sms * (nk + 8);
+  for (int k = 2; k <= 8 && nk >= 4 * k; ++k) {
+    const int64_t cost = (nk + k - 1) / k + 8 + k;
+    if (items * 152 <= static_cast<int64_t>(kHeld[k]) * num_sms && cost < best) best = cost, ks = k;
+  }
+  const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<kBits, kMid>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(static_cast<unsigned>(ks > 1 ? items * ks : std::min<int64_t>(items, num_sms)));
   cfg.blockDim = dim3(kLtThreads);
-  cfg.dynamicSmemBytes = kLtSmem;
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -382,38 +464,15 @@ cudaError_t launch_tc_t(const CUtensorMap& map, const LinearArgs& a, int ks, uns
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<kBits>, map, a, ks);
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<kBits, kMid>, map, a, ks);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
-  if (!enc) return cudaErrorInvalidValue;
-  cudaError_t e = launch_kernel(linear_rows_kernel, dim3(static_cast<unsigned>(a.T)), dim3(256), 0, stream, true,
-                                a.x, a.x_stride, a.K, a.xh, a.xexp);
-  if (e != cudaSuccess) return e;
-  // the f16 rows as a 2-d tensor: boxes of 64 tokens x 64 columns (128 bytes), zero fill past the last token
-  CUtensorMap map;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.K) * 2};
-  const cuuint32_t box[2] = {kLtBK, kLtBox}, estr[2] = {1, 1};
-  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.xh, dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  const int64_t items = static_cast<int64_t>((a.N + kLtRows - 1) / kLtRows) * ((a.T + kLtTok - 1) / kLtTok);
-  const int nk = a.K / kLtBK;
-  // contraction splits: rounds of blocks x (stages of a share + about 8 stages' worth of start, drain
-  // and join), only while a tile per cluster fits the GPU at once
-  int ks = 1;
-  int64_t best = (items + num_sms - 1) / num_sms * (nk + 8);
-  for (int k = 2; k <= 8 && items * k <= num_sms && nk >= 4 * k; k *= 2) {
-    const int64_t cost = (nk + k - 1) / k + 8 + k;
-    if (cost < best) best = cost, ks = k;
-  }
-  const unsigned grid = static_cast<unsigned>(ks > 1 ? items * ks : std::min<int64_t>(items, num_sms));
-  return a.bits == 4 ? launch_tc_t<4>(map, a, ks, grid, stream) : launch_tc_t<8>(map, a, ks, grid, stream);
+  if (a.T <= kLinearMidT)
+    return a.bits == 4 ? launch_tc_t<4, true>(a, num_sms, stream) : launch_tc_t<8, true>(a, num_sms, stream);
+  return a.bits == 4 ? launch_tc_t<4, false>(a, num_sms, stream) : launch_tc_t<8, false>(a, num_sms, stream);
 }
 
 }  // namespace strata

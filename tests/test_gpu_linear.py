@@ -61,7 +61,7 @@ def check(T, N, K, bits, group, with_bias=False, with_res=False, **kw):
     got = run(x, codes, scales, bits, group, bias, res, **kw)
     want, bound = ref.linear(ref.bf16_bits_to_f64(x), codes, scales, bits, group, bias,
                              None if res is None else ref.bf16_bits_to_f64(res),
-                             rounded_weights=T > st.LINEAR_STREAM_T)
+                             rounded_weights=T > st.LINEAR_EXACT_T)
     worst = (np.abs(got - want) / bound).max()
     print(f"T {T} N {N} K {K} w{bits} g{group}: worst error / bound {worst:.3f}")
     assert worst <= 1
