@@ -7,7 +7,7 @@
 namespace strata {
 
 // Up to this many tokens a projection streams its codes through registers (linear.cu).
-constexpr int kLinearStreamT = 8;
+constexpr int kLinearStreamT = 32;
 // Beyond that and up to this many, the tensor cores multiply x with weights in two bf16 parts
 // (linear_tc.cu); more tokens take f16 operands.
 constexpr int kLinearMidT = STRATA_LINEAR_EXACT_T;

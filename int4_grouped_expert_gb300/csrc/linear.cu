@@ -1,19 +1,18 @@
 // Projections with group-quantized weights for few tokens: y[t,n] = sum_g s[n,g] sum_{c in g} x[t,c] q[n,c],
 // the format of "Strata" MoE tuning notes (lpnh.cn/news/2730718, §2.1: G codes share one fp16 scale).
 //
-// The weights are read once, so the kernel is bound by streaming their codes. A block owns 16 weight
-// rows and its 8 warps take alternate pieces of the contraction; every lane loads its codes straight
-// into registers and multiplies them on the tensor cores (mma.sync m16n8k16, the 16 rows as A, 8
-// tokens as B). The order of a contraction is free, so lane t of a quad takes 16 or 32 consecutive
-// codes of a row instead of the pairs the instruction names, and the matching activations.
+// The weights are read once. A block owns 16 to 64 weight rows and its 8 warps take alternate pieces of the
+// contraction; every lane loads its codes straight into registers and multiplies them on the tensor
+// cores (mma.sync m16n8k16, 16 rows as A, 8 tokens as B). The order of a contraction is free, so lane t
+// of a quad takes 16 or 32 consecutive codes of a row instead of the pairs the instruction names, and
+// the matching activations. What bounds it: at one token and 4 bits the ALU pipe (70% busy: shifts and
+// LOP3 that unpack the codes), with more tokens the reads of x from L2.
 //
 // The codes are exact in bf16 (|q| <= 128), the activations are bf16, their products are exact in
 // fp32, and the group's scale multiplies the fp32 sum: nothing is rounded before the output.
 #include "block.cuh"
 
 namespace strata {
-
-constexpr int kLinWarps = 8;
 
 // bf16x2 {q_0, q_1} and {q_2, q_3} of four int8 codes: 128 + (low 7 bits) minus 128 or, where the
 // sign bit is set, 256. Both are exact bf16 values, and so is the difference.
@@ -29,133 +28,183 @@ __device__ __forceinline__ void codes8_bf16(uint32_t w, uint32_t& lo, uint32_t& 
   hi = *reinterpret_cast<uint32_t*>(&r1);
 }
 
+// D += A * B, m16n8k16, bf16 inputs, fp32 sums. (Not volatile: the compiler may interleave independent chains.)
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // kUnit: columns of one step, 128 (32 consecutive codes a lane), or 64 for 64-wide groups (16 a
-// lane), so that a step's products share one scale per row.
-template <int kBits, int kNT, int kUnit>
-__global__ void __launch_bounds__(kLinWarps * 32) linear_stream_kernel(LinearArgs a) {
+// lane), so that a step's products share one scale per row. kMT: 16-row tiles of a block, which share the
+// activations that a lane reads; kPF: steps whose codes are on their way.
+template <int kBits, int kUnit, int kNT, int kMT, int kPF, int kLinWarps, int kBlocks>
+__global__ void __launch_bounds__(kLinWarps * 32, kBlocks) linear_stream_kernel(LinearArgs a) {
   constexpr int CPL = kUnit / 4;            // codes a lane takes of a row
   constexpr int WPL = CPL * kBits / 32;     // words of them: 2, 4 or 8
-  constexpr int COLS = 8 * kNT;
-  __shared__ float red[kLinWarps][16][COLS + 1];
+  constexpr int COLS = 8 * kNT, ROWS = 16 * kMT;
+  __shared__ float red[kLinWarps][ROWS][COLS + 1];
   griddep_wait();
   griddep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * ROWS;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * COLS;
   const int64_t row_bytes = static_cast<int64_t>(a.K) * kBits / 8;
-  // rows past the end repeat the last one; their sums are not written
-  const int64_t r0 = min(n0 + g, a.N - 1), r1 = min(n0 + g + 8, a.N - 1);
-  const uint8_t* c0 = a.codes + r0 * row_bytes + t * (CPL * kBits / 8);
-  const uint8_t* c1 = a.codes + r1 * row_bytes + t * (CPL * kBits / 8);
   const int ng = a.K / a.group, ushift = a.group == 256 ? 1 : 0;
-  const __half* s0 = a.scales + r0 * ng;
-  const __half* s1 = a.scales + r1 * ng;
-  float acc[kNT][4];
+  // rows g and g + 8 of each tile; rows past the end repeat the last one, and their sums are not written
+  const uint8_t* cp[2 * kMT];
+  const __half* sp[2 * kMT];
 #pragma unroll
-  for (int n = 0; n < kNT; ++n)
+  for (int r = 0; r < 2 * kMT; ++r) {
+    const int64_t row = min(n0 + 8 * r + g, a.N - 1);
+    cp[r] = a.codes + row * row_bytes + t * (CPL * kBits / 8);
+    sp[r] = a.scales + row * ng;
+  }
+  const __nv_bfloat16* xp[kNT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-
-  auto load_codes = [&](const uint8_t* p, uint32_t (&w)[WPL]) {
-    if (WPL == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = v.x; w[1] = v.y;
-    } else {
+  for (int n = 0; n < kNT; ++n) {
+    const int64_t tok = t0 + n * 8 + g;
+    xp[n] = tok < a.T ? a.x + tok * a.x_stride + t * CPL : nullptr;
+  }
+  float acc[kMT][kNT][4];
 #pragma unroll
-      for (int i = 0; i < WPL / 4; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-      }
-    }
-  };
-
-  const int units = a.K / kUnit;
-  for (int u = warp; u < units; u += kLinWarps) {
-    uint32_t w0[WPL], w1[WPL];
-    load_codes(c0 + static_cast<int64_t>(u) * (kUnit * kBits / 8), w0);
-    load_codes(c1 + static_cast<int64_t>(u) * (kUnit * kBits / 8), w1);
-    const float f0 = __half2float(__ldg(s0 + (u >> ushift)));
-    const float f1 = __half2float(__ldg(s1 + (u >> ushift)));
-    float part[kNT][4];
+  for (int m = 0; m < kMT; ++m)
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
-    // 8 columns at a time: two MMA steps of 4 columns per lane
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+
+  uint32_t w[kPF][2 * kMT][WPL];
+  __half sc[kPF][2 * kMT];
+  const int units = a.K / kUnit;
+  auto load = [&](int u, int slot) {
+    if (u >= units) return;
 #pragma unroll
-    for (int j = 0; j < CPL / 8; ++j) {
-      uint32_t A[2][4];
-      if (kBits == 4) {
-        // pairs (0,4) (1,5) and (2,6) (3,7) of the 8 codes
-        const uint32_t u0 = w0[j] ^ 0x88888888u, u1 = w1[j] ^ 0x88888888u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          A[h][0] = int4pair_to_bf16x2(u0, 2 * h);
-          A[h][1] = int4pair_to_bf16x2(u1, 2 * h);
-          A[h][2] = int4pair_to_bf16x2(u0, 2 * h + 1);
-          A[h][3] = int4pair_to_bf16x2(u1, 2 * h + 1);
-        }
+    for (int r = 0; r < 2 * kMT; ++r) {
+      const uint8_t* p = cp[r] + static_cast<int64_t>(u) * (kUnit * kBits / 8);
+      if (WPL == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        w[slot][r][0] = v.x; w[slot][r][1] = v.y;
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          codes8_bf16(w0[(2 * j + h) % WPL], A[h][0], A[h][2]);
-          codes8_bf16(w1[(2 * j + h) % WPL], A[h][1], A[h][3]);
+        for (int i = 0; i < WPL / 4; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          w[slot][r][4 * i] = v.x; w[slot][r][4 * i + 1] = v.y; w[slot][r][4 * i + 2] = v.z; w[slot][r][4 * i + 3] = v.w;
+        }
+      }
+      sc[slot][r] = __ldg(sp[r] + (u >> ushift));
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < kPF; ++p) load(warp + p * kLinWarps, p);
+  for (int u0 = warp; u0 < units; u0 += kPF * kLinWarps) {
+#pragma unroll
+    for (int p = 0; p < kPF; ++p) {
+      const int u = u0 + p * kLinWarps;
+      if (u >= units) break;
+      float part[kMT][kNT][4];
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[m][n][i] = 0.f;
+      // 8 columns at a time: two MMA steps of 4 columns per lane
+#pragma unroll
+      for (int j = 0; j < CPL / 8; ++j) {
+        uint4 xv[kNT];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+          xv[n] = xp[n] ? *(reinterpret_cast<const uint4*>(xp[n] + u * kUnit) + j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+          const uint32_t* w0 = w[p][2 * m];
+          const uint32_t* w1 = w[p][2 * m + 1];
+          uint32_t A[2][4];
+          if (kBits == 4) {
+            // pairs (0,4) (1,5) and (2,6) (3,7) of the 8 codes
+            const uint32_t u0_ = w0[j] ^ 0x88888888u, u1_ = w1[j] ^ 0x88888888u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              A[h][0] = int4pair_to_bf16x2(u0_, 2 * h);
+              A[h][1] = int4pair_to_bf16x2(u1_, 2 * h);
+              A[h][2] = int4pair_to_bf16x2(u0_, 2 * h + 1);
+              A[h][3] = int4pair_to_bf16x2(u1_, 2 * h + 1);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              codes8_bf16(w0[(2 * j + h) % WPL], A[h][0], A[h][2]);
+              codes8_bf16(w1[(2 * j + h) % WPL], A[h][1], A[h][3]);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            if (kBits == 4) {
+              mma_bf16(part[m][n], A[0], prmt(xv[n].x, xv[n].z, 0x5410), prmt(xv[n].x, xv[n].z, 0x7632));
+              mma_bf16(part[m][n], A[1], prmt(xv[n].y, xv[n].w, 0x5410), prmt(xv[n].y, xv[n].w, 0x7632));
+            } else {
+              mma_bf16(part[m][n], A[0], xv[n].x, xv[n].y);
+              mma_bf16(part[m][n], A[1], xv[n].z, xv[n].w);
+            }
+          }
         }
       }
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        const int64_t tok = t0 + n * 8 + g;
-        uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-        if (tok < a.T)
-          xv = *(reinterpret_cast<const uint4*>(a.x + tok * a.x_stride + u * kUnit + t * CPL) + j);
-        if (kBits == 4) {
-          mma_bf16_16816(part[n], A[0], prmt(xv.x, xv.z, 0x5410), prmt(xv.x, xv.z, 0x7632), part[n]);
-          mma_bf16_16816(part[n], A[1], prmt(xv.y, xv.w, 0x5410), prmt(xv.y, xv.w, 0x7632), part[n]);
-        } else {
-          mma_bf16_16816(part[n], A[0], xv.x, xv.y, part[n]);
-          mma_bf16_16816(part[n], A[1], xv.z, xv.w, part[n]);
+      for (int m = 0; m < kMT; ++m) {
+        const float f0 = __half2float(sc[p][2 * m]), f1 = __half2float(sc[p][2 * m + 1]);
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          acc[m][n][0] = fmaf(f0, part[m][n][0], acc[m][n][0]);
+          acc[m][n][1] = fmaf(f0, part[m][n][1], acc[m][n][1]);
+          acc[m][n][2] = fmaf(f1, part[m][n][2], acc[m][n][2]);
+          acc[m][n][3] = fmaf(f1, part[m][n][3], acc[m][n][3]);
         }
       }
-    }
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      acc[n][0] = fmaf(f0, part[n][0], acc[n][0]);
-      acc[n][1] = fmaf(f0, part[n][1], acc[n][1]);
-      acc[n][2] = fmaf(f1, part[n][2], acc[n][2]);
-      acc[n][3] = fmaf(f1, part[n][3], acc[n][3]);
+      load(u + kPF * kLinWarps, p);
     }
   }
 #pragma unroll
-  for (int n = 0; n < kNT; ++n) {
-    red[warp][g][n * 8 + 2 * t] = acc[n][0];
-    red[warp][g][n * 8 + 2 * t + 1] = acc[n][1];
-    red[warp][g + 8][n * 8 + 2 * t] = acc[n][2];
-    red[warp][g + 8][n * 8 + 2 * t + 1] = acc[n][3];
-  }
+  for (int m = 0; m < kMT; ++m)
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[warp][16 * m + g + 8 * (i >> 1)][n * 8 + 2 * t + (i & 1)] = acc[m][n][i];
   __syncthreads();
   // the warps' sums in a fixed order, consecutive threads along the weight rows (output columns)
-  for (int i = threadIdx.x; i < 16 * COLS; i += kLinWarps * 32) {
-    const int r = i & 15, c = i >> 4;
+  for (int i = threadIdx.x; i < ROWS * COLS; i += kLinWarps * 32) {
+    const int r = i % ROWS, c = i / ROWS;
     const int64_t tok = t0 + c;
     if (n0 + r >= a.N || tok >= a.T) continue;
     float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kLinWarps; ++w) y += red[w][r][c];
+    for (int k = 0; k < kLinWarps; ++k) y += red[k][r][c];
     if (a.bias) y += a.bias[n0 + r];
     if (a.residual) y += __bfloat162float(a.residual[tok * a.residual_stride + n0 + r]);
     a.out[tok * a.out_stride + n0 + r] = __float2bfloat16_rn(y);
   }
 }
 
+template <int kBits, int kUnit, int kNT, int kMT, int kPF, int kLinWarps, int kBlocks>
+static cudaError_t launch_stream_n(const LinearArgs& a, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((a.N + 16 * kMT - 1) / (16 * kMT)),
+                  static_cast<unsigned>((a.T + 8 * kNT - 1) / (8 * kNT)));
+  return launch_kernel(linear_stream_kernel<kBits, kUnit, kNT, kMT, kPF, kLinWarps, kBlocks>, grid, kLinWarps * 32, 0, stream, true, a);
+}
+// Up to 8 tokens the weights are all the traffic: 16 rows a block, the next step's codes on their way. With
+// more, every block reads all of x, and wider blocks (32 rows, 64 beyond 16 tokens) read it less
+// often; where 16-row blocks leave SMs idle, they are faster (us, wide / 16 rows: 16 tokens, 8 bits,
+// 7168 -> 9216 19.6 / 32.1, 4 bits, 1024 -> 1024 2.7 / 2.2; 32 tokens 30.4 / 67 and 5.6 / 3.2).
 template <int kBits, int kUnit>
 static cudaError_t launch_stream_t(const LinearArgs& a, cudaStream_t stream) {
-  const unsigned gx = static_cast<unsigned>((a.N + 15) / 16);
-  const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-  const dim3 grid(gx, static_cast<unsigned>((a.T + 8 * nt - 1) / (8 * nt)));
-  if (nt == 1) return launch_kernel(linear_stream_kernel<kBits, 1, kUnit>, grid, kLinWarps * 32, 0, stream, true, a);
-  if (nt == 2) return launch_kernel(linear_stream_kernel<kBits, 2, kUnit>, grid, kLinWarps * 32, 0, stream, true, a);
-  return launch_kernel(linear_stream_kernel<kBits, 4, kUnit>, grid, kLinWarps * 32, 0, stream, true, a);
+  const bool narrow = a.N <= 152 * 16;
+  if (a.T <= 8) return launch_stream_n<kBits, kUnit, 1, 1, 2, 8, 3>(a, stream);
+  if (a.T <= 16)
+    return narrow ? launch_stream_n<kBits, kUnit, 2, 1, 1, 8, 3>(a, stream)
+                  : launch_stream_n<kBits, kUnit, 2, 2, 1, 8, 2>(a, stream);
+  return narrow ? launch_stream_n<kBits, kUnit, 4, 1, 1, 8, 2>(a, stream)
+                : launch_stream_n<kBits, kUnit, 4, 4, 1, 8, 1>(a, stream);
 }
 
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t stream) {
