@@ -2,16 +2,22 @@
 // power-of-two scale per (page, head).
 //
 // A run is a stretch of rows with consecutive slots in one page; one block owns a run of one K/V head,
-// so the scale of a (page, head) has one writer and needs no atomics. The block finds the largest
-// magnitude of the run (pass 1), settles the new scale with the page's old one, rewrites the older
-// codes if the scale grew, and writes the codes (pass 2, from L1/L2). The rotation is elementwise
-// in fp32 with each product and sum rounded once, so both passes see the same values. The call moves
-// each byte of q, k and v once: it is bound by memory for prompts and by latency for single tokens.
+// so the scale of a (page, head) has one writer and needs no atomics. The block holds the run's rows in
+// registers as they came, finds the largest magnitude of the rotated rows, settles the new scale with
+// the page's old one, rewrites the older codes if the scale grew, rotates again and writes the codes:
+// the rotation is elementwise in fp32 with each product and sum rounded once, so both times give the
+// same values. The call moves each byte of q, k and v once and is bound by memory for prompts, by the
+// chain slot -> position -> table row -> codes for single tokens.
+//
+// A thread takes two chunks of 8 elements of a head's row that the rotation keeps to themselves: chunks c
+// and c + rot / 16 where halves are paired, neighbouring chunks elsewhere; with them it needs 8 cosines
+// and 8 sines, which serve all heads of a row that it takes.
 #include "block.cuh"
 
 namespace strata {
 
-constexpr int kAppThreads = 128;
+constexpr int kAppThreads = 256;
+constexpr int kAppHeads = 8;  // query heads that a block takes at a time
 
 // Two values as e4m3 codes (lo in the low byte), rounded to nearest-even. |x| <= 448 by the choice of
 // the scale; larger ones (a scale that an earlier writer chose) saturate.
@@ -36,59 +42,72 @@ __device__ __forceinline__ float append_scale(float absmax) {
   return exp2i(max(e, -100));
 }
 
-// Elements 8c .. 8c+7 of one head's row, rotated: fp32, every product and sum rounded once.
-__device__ __forceinline__ void rotated8(const __nv_bfloat16* row, int c, const float* cs, int rot,
-                                         int neighbours, float (&y)[8]) {
-  const uint4 w = *(reinterpret_cast<const uint4*>(row) + c);
-  float x[8] = {bf16_lo_f32(w.x), bf16_hi_f32(w.x), bf16_lo_f32(w.y), bf16_hi_f32(w.y),
-                bf16_lo_f32(w.z), bf16_hi_f32(w.z), bf16_lo_f32(w.w), bf16_hi_f32(w.w)};
-  const int i0 = 8 * c, h = rot >> 1;
-  if (i0 >= rot) {
+// Two chunks of a row: their places, and how they turn.
+struct Pair {
+  int a, b;    // chunk indices
+  int kind;    // 0: not rotated, 1: halves (a with b), 2: neighbours (within a, within b)
+  int at;      // first of their 8 cosines in the table row
+};
+__device__ __forceinline__ Pair pair_of(int p, int rot, int neighbours) {
+  const int turned = rot >> 4;  // pairs that are rotated
+  if (p >= turned) return {2 * p, 2 * p + 1, 0, 0};
+  if (neighbours) return {2 * p, 2 * p + 1, 2, 8 * p};
+  return {p, p + turned, 1, 8 * p};
+}
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ Turn turn_of(const KvAppendArgs& a, const Pair& p, int row) {
+  Turn t = {};
+  if (p.kind == 0) return t;
+  const float* cs = a.rope + static_cast<int64_t>(a.positions[row]) * a.rot_dim + p.at;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i];
-  } else if (neighbours) {
-    const float4 co = *reinterpret_cast<const float4*>(cs + i0 / 2);
-    const float4 si = *reinterpret_cast<const float4*>(cs + h + i0 / 2);
-    const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+  for (int q = 0; q < 2; ++q) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + 4 * q);
+    const float4 s = *reinterpret_cast<const float4*>(cs + (a.rot_dim >> 1) + 4 * q);
+    t.c[4 * q] = c.x; t.c[4 * q + 1] = c.y; t.c[4 * q + 2] = c.z; t.c[4 * q + 3] = c.w;
+    t.s[4 * q] = s.x; t.s[4 * q + 1] = s.y; t.s[4 * q + 2] = s.z; t.s[4 * q + 3] = s.w;
+  }
+  return t;
+}
+__device__ __forceinline__ void to_f32(const uint4& w, float* x) {
+  x[0] = bf16_lo_f32(w.x); x[1] = bf16_hi_f32(w.x); x[2] = bf16_lo_f32(w.y); x[3] = bf16_hi_f32(w.y);
+  x[4] = bf16_lo_f32(w.z); x[5] = bf16_hi_f32(w.z); x[6] = bf16_lo_f32(w.w); x[7] = bf16_hi_f32(w.w);
+}
+// The 16 elements of a pair of chunks, rotated: fp32, every product and sum rounded once.
+__device__ __forceinline__ void rotated(const uint4& wa, const uint4& wb, const Pair& p, const Turn& t, float (&y)[16]) {
+  to_f32(wa, y);
+  to_f32(wb, y + 8);
+  if (p.kind == 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], cc[i]), __fmul_rn(x[2 * i + 1], ss[i]));
-      y[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], cc[i]), __fmul_rn(x[2 * i], ss[i]));
+    for (int i = 0; i < 8; ++i) {
+      const float u = y[i], v = y[8 + i];
+      y[i] = __fsub_rn(__fmul_rn(u, t.c[i]), __fmul_rn(v, t.s[i]));
+      y[8 + i] = __fadd_rn(__fmul_rn(v, t.c[i]), __fmul_rn(u, t.s[i]));
     }
-  } else {
-    const bool first = i0 < h;  // rot % 16 == 0: a chunk lies in one half
-    const int f = first ? i0 : i0 - h;
-    const uint4 o = *(reinterpret_cast<const uint4*>(row) + (first ? i0 + h : f) / 8);
-    const float z[8] = {bf16_lo_f32(o.x), bf16_hi_f32(o.x), bf16_lo_f32(o.y), bf16_hi_f32(o.y),
-                        bf16_lo_f32(o.z), bf16_hi_f32(o.z), bf16_lo_f32(o.w), bf16_hi_f32(o.w)};
+  } else if (p.kind == 2) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float4 co = *reinterpret_cast<const float4*>(cs + f + 4 * q);
-      const float4 si = *reinterpret_cast<const float4*>(cs + h + f + 4 * q);
-      const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 4 * q + i;
-        const float own = __fmul_rn(x[k], cc[i]), other = __fmul_rn(z[k], ss[i]);
-        y[k] = first ? __fsub_rn(own, other) : __fadd_rn(own, other);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float u = y[2 * i], v = y[2 * i + 1];
+      y[2 * i] = __fsub_rn(__fmul_rn(u, t.c[i]), __fmul_rn(v, t.s[i]));
+      y[2 * i + 1] = __fadd_rn(__fmul_rn(v, t.c[i]), __fmul_rn(u, t.s[i]));
     }
   }
 }
 
-__device__ __forceinline__ bool finite8(const float (&y)[8]) {
+__device__ __forceinline__ bool finite16(const float (&y)[16]) {
   bool ok = true;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ok = ok && (__float_as_uint(y[i]) & 0x7F800000u) != 0x7F800000u;
+  for (int i = 0; i < 16; ++i) ok = ok && (__float_as_uint(y[i]) & 0x7F800000u) != 0x7F800000u;
   return ok;
 }
-__device__ __forceinline__ float max8(const float (&y)[8]) {
+__device__ __forceinline__ float max16(const float (&y)[16]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(y[i]));
   return m;
 }
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+__device__ __forceinline__ uint2 codes8(const float* y, float inv) {
   uint2 d;
   d.x = f32x2_to_e4m3x2(y[0] * inv, y[1] * inv) | f32x2_to_e4m3x2(y[2] * inv, y[3] * inv) << 16;
   d.y = f32x2_to_e4m3x2(y[4] * inv, y[5] * inv) | f32x2_to_e4m3x2(y[6] * inv, y[7] * inv) << 16;
@@ -129,16 +148,36 @@ __device__ __forceinline__ void rescale(uint8_t* codes, int bytes, float ratio) 
   }
 }
 
-template <int kD>
+// kIter: iterations that a page of rows takes.
+template <int kD, int kIter>
 __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int head) {
-  constexpr int TPR = kD / 8;               // threads per row
+  constexpr int TPR = kD / 16;              // threads per row
   constexpr int RPI = kAppThreads / TPR;    // rows per iteration
-  __shared__ int s_len[kAppThreads / 32];
-  __shared__ float s_max[2][kAppThreads / 32];
+  constexpr int WARPS = kAppThreads / 32;
+  __shared__ int s_len[WARPS];
+  __shared__ float s_max[2][WARPS];
   const int P = a.c.page_size;
   const int slot = a.slots[row0], off = slot % P;
   const int64_t page = slot / P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the rows that may be the run's, on their way while its length is found
+  const Pair kp = pair_of(threadIdx.x % TPR, a.rot_dim, a.neighbours);
+  const Pair vp = {kp.a, kp.b, 0, 0};
+  const int ri = threadIdx.x / TPR;
+  const Turn none = {};
+  uint4 kw[kIter][2], vw[kIter][2];
+#pragma unroll
+  for (int j = 0; j < kIter; ++j) {
+    const int64_t r = row0 + j * RPI + ri;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const bool on = off + j * RPI + ri < P && r < a.T;
+    const uint4* k = reinterpret_cast<const uint4*>(a.k + r * a.k_stride + head * kD);
+    const uint4* v = reinterpret_cast<const uint4*>(a.v + r * a.v_stride + head * kD);
+    kw[j][0] = on ? k[kp.a] : z;
+    kw[j][1] = on ? k[kp.b] : z;
+    vw[j][0] = on ? v[kp.a] : z;
+    vw[j][1] = on ? v[kp.b] : z;
+  }
   // the run's length: the first row that does not continue it (P <= kAppThreads)
   {
     const int i = threadIdx.x, r = row0 + i;
@@ -149,32 +188,30 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   __syncthreads();
   int n = kAppThreads;
 #pragma unroll
-  for (int w = 0; w < kAppThreads / 32; ++w) n = min(n, s_len[w]);
+  for (int w = 0; w < WARPS; ++w) n = min(n, s_len[w]);
 
-  const int c = threadIdx.x % TPR, ri = threadIdx.x / TPR;
-  const int rot = a.rot_dim;
-  auto load = [&](int i, float (&k)[8], float (&v)[8]) {
-    const int64_t r = row0 + i;
-    const float* cs = rot ? a.rope + static_cast<int64_t>(a.positions[r]) * rot : nullptr;
-    rotated8(a.k + r * a.k_stride + head * kD, c, cs, rot, a.neighbours, k);
-    rotated8(a.v + r * a.v_stride + head * kD, c, nullptr, 0, 0, v);
-  };
+#pragma unroll
+  for (int j = 0; j < kIter; ++j)
+    if (j * RPI + ri >= n) kw[j][0] = kw[j][1] = vw[j][0] = vw[j][1] = make_uint4(0u, 0u, 0u, 0u);
   // a row is good when all its threads hold finite values
-  auto good_row = [&](const float (&k)[8], const float (&v)[8]) {
-    const unsigned bad = __ballot_sync(0xffffffffu, !(finite8(k) && finite8(v)));
+  auto good_row = [&](const float (&k)[16], const float (&v)[16]) {
+    const unsigned bad = __ballot_sync(0xffffffffu, !(finite16(k) && finite16(v)));
     return ((bad >> (lane / TPR * TPR)) & ((1u << TPR) - 1u)) == 0;
   };
   float km = 0.f, vm = 0.f;
-  bool any_bad = false;
-  for (int i0 = 0; i0 < n; i0 += RPI) {
-    const int i = i0 + ri;
-    float k[8] = {}, v[8] = {};
-    if (i < n) load(i, k, v);
-    const bool ok = good_row(k, v);
-    any_bad |= !ok;
-    if (ok) {
-      km = fmaxf(km, max8(k));
-      vm = fmaxf(vm, max8(v));
+  unsigned bad_rows = 0;  // bit j: this thread's row of iteration j
+#pragma unroll
+  for (int j = 0; j < kIter; ++j) {
+    if (j * RPI >= n) break;
+    float k[16], v[16];
+    const int i = j * RPI + ri;
+    rotated(kw[j][0], kw[j][1], kp, i < n ? turn_of(a, kp, row0 + i) : none, k);
+    rotated(vw[j][0], vw[j][1], vp, none, v);
+    if (good_row(k, v)) {
+      km = fmaxf(km, max16(k));
+      vm = fmaxf(vm, max16(v));
+    } else {
+      bad_rows |= 1u << j;
     }
   }
   km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(km)));  // >= 0: bits order
@@ -185,7 +222,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppThreads / 32; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     km = fmaxf(km, s_max[0][w]);
     vm = fmaxf(vm, s_max[1][w]);
   }
@@ -199,80 +236,107 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     if (vs > v_old) rescale(vc, off * kD, __fdiv_rn(v_old, vs)); else vs = v_old;
   }
   const float ki = __fdiv_rn(1.0f, ks), vi = __fdiv_rn(1.0f, vs);
-  for (int i0 = 0; i0 < n; i0 += RPI) {
-    const int i = i0 + ri;
-    float k[8] = {}, v[8] = {};
-    if (i < n) load(i, k, v);
-    const bool ok = good_row(k, v);
-    if (i < n) {
-      const int64_t at = static_cast<int64_t>(off + i) * kD + 8 * c;
-      const uint32_t nan4 = 0x7F7F7F7Fu;
-      *reinterpret_cast<uint2*>(kc + at) = ok ? codes8(k, ki) : make_uint2(nan4, nan4);
-      *reinterpret_cast<uint2*>(vc + at) = ok ? codes8(v, vi) : make_uint2(0u, 0u);
-    }
+#pragma unroll
+  for (int j = 0; j < kIter; ++j) {
+    const int i = j * RPI + ri;
+    if (i >= n) break;
+    float k[16], v[16];
+    rotated(kw[j][0], kw[j][1], kp, turn_of(a, kp, row0 + i), k);
+    rotated(vw[j][0], vw[j][1], vp, none, v);
+    const bool ok = !(bad_rows >> j & 1u);
+    const uint2 nan8 = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), zero = make_uint2(0u, 0u);
+    uint2* kd = reinterpret_cast<uint2*>(kc + static_cast<int64_t>(off + i) * kD);
+    uint2* vd = reinterpret_cast<uint2*>(vc + static_cast<int64_t>(off + i) * kD);
+    kd[kp.a] = ok ? codes8(k, ki) : nan8;
+    kd[kp.b] = ok ? codes8(k + 8, ki) : nan8;
+    vd[kp.a] = ok ? codes8(v, vi) : zero;
+    vd[kp.b] = ok ? codes8(v + 8, vi) : zero;
   }
   __syncthreads();  // every thread has read the old scales (and the shared words, for the next run)
   if (threadIdx.x == 0) {
     a.c.k_scales[ph] = ks;
     a.c.v_scales[ph] = vs;
   }
-  if (__any_sync(0xffffffffu, any_bad) && lane == 0) set_status(a.status, STRATA_DEV_NONFINITE);
+  if (__any_sync(0xffffffffu, bad_rows != 0) && lane == 0) set_status(a.status, STRATA_DEV_NONFINITE);
 }
 
+// Queries: a block takes kAppThreads / (kD / 16 * kAppHeads) rows; a thread one pair of chunks of every
+// kAppHeads-th head of a row.
 template <int kD>
-__global__ void __launch_bounds__(kAppThreads) kv_append_kernel(KvAppendArgs a, int kv_blocks) {
+__device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block) {
+  constexpr int TPR = kD / 16, ROWS = kAppThreads / (TPR * kAppHeads);
+  const int r = block * ROWS + threadIdx.x / (TPR * kAppHeads);
+  if (r >= a.T || row_state(a, r) != 1) return;
+  const Pair p = pair_of(threadIdx.x % TPR, a.rot_dim, a.neighbours);
+  const Turn t = turn_of(a, p, r);
+  const __nv_bfloat16* src = a.q + r * a.q_stride;
+  __nv_bfloat16* dst = a.q_out + r * a.q_out_stride;
+  constexpr int U = 4;  // heads on their way
+  for (int h0 = threadIdx.x / TPR % kAppHeads; h0 < a.n_heads; h0 += U * kAppHeads) {
+    uint4 wa[U], wb[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * kAppHeads;
+      if (h >= a.n_heads) break;
+      wa[i] = reinterpret_cast<const uint4*>(src + h * kD)[p.a];
+      wb[i] = reinterpret_cast<const uint4*>(src + h * kD)[p.b];
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * kAppHeads;
+      if (h >= a.n_heads) break;
+      float y[16];
+      rotated(wa[i], wb[i], p, t, y);
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
+        o[k] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      // (q_out may be q: nobody else reads these chunks)
+      reinterpret_cast<uint4*>(dst + h * kD)[p.a] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4*>(dst + h * kD)[p.b] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+template <int kD, int kIter>
+__global__ void __launch_bounds__(kAppThreads, kIter > 2 ? 1 : 3) kv_append_kernel(KvAppendArgs a, int kv_blocks) {
   griddep_wait();
   griddep_launch();
-  if (blockIdx.x < static_cast<unsigned>(kv_blocks)) {
-    const int head = blockIdx.x % a.c.n_kv_heads;
-    const int lo = blockIdx.x / a.c.n_kv_heads * a.rows_per_block;  // rows_per_block <= kAppThreads
-    const int r = lo + threadIdx.x;
-    const int st = threadIdx.x < a.rows_per_block && r < a.T ? row_state(a, r) : 0;
-    if (st == 2) set_status(a.status, STRATA_DEV_BAD_SLOT);
-    __shared__ unsigned s_starts[kAppThreads / 32];
-    const unsigned starts = __ballot_sync(0xffffffffu, st == 1 && !continues(a, r));
-    if ((threadIdx.x & 31) == 0) s_starts[threadIdx.x >> 5] = starts;
-    __syncthreads();
-    for (int w = 0; w < kAppThreads / 32; ++w)
-      for (unsigned m = s_starts[w]; m; m &= m - 1) append_run<kD>(a, lo + 32 * w + __ffs(m) - 1, head);
+  if (blockIdx.x >= static_cast<unsigned>(kv_blocks)) {
+    rotate_queries<kD>(a, blockIdx.x - kv_blocks);
     return;
   }
-  // queries: one thread per 8 elements
-  const int64_t per_row = static_cast<int64_t>(a.n_heads) * (kD / 8);
-  const int64_t i = static_cast<int64_t>(blockIdx.x - kv_blocks) * kAppThreads + threadIdx.x;
-  const bool in = i < per_row * a.T;
-  const int r = in ? static_cast<int>(i / per_row) : 0, j = in ? static_cast<int>(i % per_row) : 0;
-  const bool on = in && row_state(a, r) == 1;
-  float y[8] = {};
-  if (on) {
-    const int head = j / (kD / 8), c = j % (kD / 8);
-    const float* cs = a.rot_dim ? a.rope + static_cast<int64_t>(a.positions[r]) * a.rot_dim : nullptr;
-    rotated8(a.q + r * a.q_stride + head * kD, c, cs, a.rot_dim, a.neighbours, y);
-  }
-  __syncwarp();  // q_out may be q: a head's chunks are in one warp, all read before any is written
-  if (on) {
-    uint4 o;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
-      w[k] = *reinterpret_cast<uint32_t*>(&b);
-    }
-    *(reinterpret_cast<uint4*>(a.q_out + r * a.q_out_stride) + j) = o;
-  }
+  const int head = blockIdx.x % a.c.n_kv_heads;
+  const int lo = blockIdx.x / a.c.n_kv_heads * a.rows_per_block;  // rows_per_block <= kAppThreads
+  const int r = lo + threadIdx.x;
+  const int st = threadIdx.x < a.rows_per_block && r < a.T ? row_state(a, r) : 0;
+  if (st == 2) set_status(a.status, STRATA_DEV_BAD_SLOT);
+  __shared__ unsigned s_starts[kAppThreads / 32];
+  const unsigned starts = __ballot_sync(0xffffffffu, st == 1 && !continues(a, r));
+  if ((threadIdx.x & 31) == 0) s_starts[threadIdx.x >> 5] = starts;
+  __syncthreads();
+  for (int w = 0; w < kAppThreads / 32; ++w)
+    for (unsigned m = s_starts[w]; m; m &= m - 1) append_run<kD, kIter>(a, lo + 32 * w + __ffs(m) - 1, head);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a0, int num_sms, cudaStream_t stream) {
   KvAppendArgs a = a0;
-  const int D = a.c.head_dim;
-  // one row per block while that leaves the GPU room, a page of rows per block beyond
-  a.rows_per_block = static_cast<int64_t>(a.T) * a.c.n_kv_heads <= 8 * num_sms ? 1 : a.c.page_size;
+  const int D = a.c.head_dim, P = a.c.page_size;
+  // Rows whose runs a block starts: single tokens are a run each, prompts one per page, so as few as keep the
+  // blocks at about four per SM, and at most a page.
+  const int64_t share = (static_cast<int64_t>(a.T) * a.c.n_kv_heads + 4 * num_sms - 1) / (4 * num_sms);
+  a.rows_per_block = static_cast<int>(share < P ? share : P);
   const int64_t kv_blocks = static_cast<int64_t>((a.T + a.rows_per_block - 1) / a.rows_per_block) * a.c.n_kv_heads;
-  const int64_t q_chunks = a.q ? static_cast<int64_t>(a.T) * a.n_heads * (D / 8) : 0;
-  const int64_t grid = kv_blocks + (q_chunks + kAppThreads - 1) / kAppThreads;
+  const int q_rows = kAppThreads / (D / 16 * kAppHeads);
+  const int64_t grid = kv_blocks + (a.q ? (a.T + q_rows - 1) / q_rows : 0);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch_kernel(D == 64 ? kv_append_kernel<64> : kv_append_kernel<128>,
-                       dim3(static_cast<unsigned>(grid)), dim3(kAppThreads), 0, stream, true, a,
+  auto kern = D == 64 ? (P <= 64 ? kv_append_kernel<64, 1> : kv_append_kernel<64, 2>)
+                      : (P <= 32   ? kv_append_kernel<128, 1>
+                         : P <= 64 ? kv_append_kernel<128, 2>
+                                   : kv_append_kernel<128, 4>);
+  return launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(kAppThreads), 0, stream, true, a,
                        static_cast<int>(kv_blocks));
 }
 
