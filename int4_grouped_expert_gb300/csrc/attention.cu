@@ -155,8 +155,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   constexpr int KB = kAttStep * kD; // bytes of a step's K (and V)
   constexpr float kLag = 8.0f;      // how far a score may exceed the reference (log2)
   extern __shared__ __align__(1024) uint8_t att_smem[];
-  griddep_wait();
+  // Beside the tensor-core kernel of the same call (launched first) this one starts at once: that kernel's
+  // blocks have all waited for what came before the call. It still ends after it, so that whoever
+  // waits for this kernel has waited for both.
+  if (!a.beside) griddep_wait();
   griddep_launch();
+  struct Last {
+    bool wait;
+    __device__ ~Last() { if (wait) griddep_wait(); }
+  } last_wait{a.beside};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   Piece pc;
   if (!find_piece(a, pc)) return;
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       const int j = j0 + 16 * u;
       int page = -1;
       if (j < hi) {
-        page = table[j >> pshift];
+        page = input(a, table + (j >> pshift));
         if (page < 0 || page >= a.c.n_pages) {
           if (lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
           page = -2;
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       }
       const int64_t ph = page < 0 ? 0 : static_cast<int64_t>(page) * a.c.n_kv_heads + h;
       const float2 scale = page < 0 ? make_float2(0.f, page == -2 ? -1.f : 0.f)
-                                    : make_float2(a.c.k_scales[ph], a.c.v_scales[ph]);
+                                    : make_float2(input(a, a.c.k_scales + ph), input(a, a.c.v_scales + ph));
       if (lane == 0) s_scale[warp][i_slot][u] = scale;
       const int64_t base = ((ph << pshift) + (j & pmask)) * kD + lane * 16;
       const int n = page < 0 ? 0 : hi - j;  // tokens of the tile from here on; past them: zeros
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       if (r < rows) {
         const __nv_bfloat16* q = a.q + static_cast<int64_t>(sv.q0 + r / G) * a.q_stride +
                                  (h * G + r % G) * kD + (i >> 1) * 64 + t * 16;
-        v[i] = *(reinterpret_cast<const uint4*>(q) + (i & 1));
+        v[i] = input(a, reinterpret_cast<const uint4*>(q) + (i & 1));
       }
       mag = max(mag, bf16x8_mag(v[i]));
     }

@@ -27,9 +27,15 @@ struct SeqView {
   int q0, n;  // first row, rows
   int len;    // tokens in the cache
 };
+// A load of the call's inputs. A kernel that runs beside another of its call has not waited for the kernels
+// before, whose results are in L2 by then: it does not look in L1.
+template <class T>
+__device__ __forceinline__ T input(const AttnArgs& a, const T* p) {
+  return a.beside ? __ldcg(p) : *p;
+}
 __device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s, bool flag) {
   SeqView v;
-  int q0 = a.b.q_start[s], q1 = a.b.q_start[s + 1], len = a.b.kv_len[s];
+  int q0 = input(a, a.b.q_start + s), q1 = input(a, a.b.q_start + s + 1), len = input(a, a.b.kv_len + s);
   const int T = static_cast<int>(a.b.T);
   bool bad = q0 < 0 || q1 < q0 || q1 > T || len < 0 || len > a.b.max_kv;
   q0 = min(max(q0, 0), T);

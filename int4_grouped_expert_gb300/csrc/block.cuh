@@ -63,6 +63,7 @@ struct AttnArgs {
   int rows_above;         // attention.cu takes the sequences with at most so many rows per K/V head,
   int rows_below;         // attention_tc.cu those with more
   // attention.cu
+  bool beside;            // launched after attention_tc.cu's kernel, to run beside it
   int pieces;             // blocks that an even share of the steps is meant for
   int n_slots;            // workspace slots
   float* part;            // partial results, a slot per piece of a cut (sequence, K/V head)

@@ -237,11 +237,12 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);
   a.status = &reinterpret_cast<WsHeader*>(base)->status;
   a.rows_above = a.rows_below = p.stream_rows;
-  if (p.stream_rows > 0) {
-    const cudaError_t e = launch_attention(a, p, st);
+  if (p.tc_blocks > 0) {
+    const cudaError_t e = launch_attention_tc(a, p.tc_blocks, st);
     if (e != cudaSuccess) return STRATA_ERR_CUDA;
   }
-  return p.tc_blocks > 0 ? of(launch_attention_tc(a, p.tc_blocks, st)) : STRATA_OK;
+  a.beside = p.tc_blocks > 0;
+  return p.stream_rows > 0 ? of(launch_attention(a, p, st)) : STRATA_OK;
 }
 
 }  // extern "C"

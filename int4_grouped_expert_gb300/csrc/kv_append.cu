@@ -57,10 +57,10 @@ __device__ __forceinline__ Pair pair_of(int p, int rot, int neighbours) {
 struct Turn {
   float c[8], s[8];
 };
-__device__ __forceinline__ Turn turn_of(const KvAppendArgs& a, const Pair& p, int row) {
+__device__ __forceinline__ Turn turn_at(const KvAppendArgs& a, const Pair& p, int64_t position) {
   Turn t = {};
   if (p.kind == 0) return t;
-  const float* cs = a.rope + static_cast<int64_t>(a.positions[row]) * a.rot_dim + p.at;
+  const float* cs = a.rope + position * a.rot_dim + p.at;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const float4 c = *reinterpret_cast<const float4*>(cs + 4 * q);
@@ -69,6 +69,9 @@ __device__ __forceinline__ Turn turn_of(const KvAppendArgs& a, const Pair& p, in
     t.s[4 * q] = s.x; t.s[4 * q + 1] = s.y; t.s[4 * q + 2] = s.z; t.s[4 * q + 3] = s.w;
   }
   return t;
+}
+__device__ __forceinline__ Turn turn_of(const KvAppendArgs& a, const Pair& p, int row) {
+  return turn_at(a, p, p.kind == 0 ? 0 : a.positions[row]);
 }
 __device__ __forceinline__ void to_f32(const uint4& w, float* x) {
   x[0] = bf16_lo_f32(w.x); x[1] = bf16_hi_f32(w.x); x[2] = bf16_lo_f32(w.y); x[3] = bf16_hi_f32(w.y);
@@ -178,6 +181,15 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     vw[j][0] = on ? v[kp.a] : z;
     vw[j][1] = on ? v[kp.b] : z;
   }
+  // its first row's cosines (a position out of range is no row of the run: any table row will do) and the
+  // page's scales as well
+  Turn t_first = none;
+  if (a.rot_dim > 0) {
+    const int r = min(row0 + ri, a.T - 1);
+    t_first = turn_at(a, kp, min(static_cast<int64_t>(max(a.positions[r], 0)), a.n_pos - 1));
+  }
+  const int64_t ph = page * a.c.n_kv_heads + head;
+  const float k_old = off ? a.c.k_scales[ph] : 0.f, v_old = off ? a.c.v_scales[ph] : 0.f;
   // the run's length: the first row that does not continue it (P <= kAppThreads)
   {
     const int i = threadIdx.x, r = row0 + i;
@@ -205,7 +217,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     if (j * RPI >= n) break;
     float k[16], v[16];
     const int i = j * RPI + ri;
-    rotated(kw[j][0], kw[j][1], kp, i < n ? turn_of(a, kp, row0 + i) : none, k);
+    rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : i < n ? turn_of(a, kp, row0 + i) : none, k);
     rotated(vw[j][0], vw[j][1], vp, none, v);
     if (good_row(k, v)) {
       km = fmaxf(km, max16(k));
@@ -226,12 +238,10 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     km = fmaxf(km, s_max[0][w]);
     vm = fmaxf(vm, s_max[1][w]);
   }
-  const int64_t ph = page * a.c.n_kv_heads + head;
   uint8_t* kc = a.c.k_codes + ph * P * kD;
   uint8_t* vc = a.c.v_codes + ph * P * kD;
   float ks = append_scale(km), vs = append_scale(vm);
   if (off) {
-    const float k_old = a.c.k_scales[ph], v_old = a.c.v_scales[ph];
     if (ks > k_old) rescale(kc, off * kD, __fdiv_rn(k_old, ks)); else ks = k_old;
     if (vs > v_old) rescale(vc, off * kD, __fdiv_rn(v_old, vs)); else vs = v_old;
   }
@@ -241,7 +251,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     const int i = j * RPI + ri;
     if (i >= n) break;
     float k[16], v[16];
-    rotated(kw[j][0], kw[j][1], kp, turn_of(a, kp, row0 + i), k);
+    rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : turn_of(a, kp, row0 + i), k);
     rotated(vw[j][0], vw[j][1], vp, none, v);
     const bool ok = !(bad_rows >> j & 1u);
     const uint2 nan8 = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), zero = make_uint2(0u, 0u);

@@ -10,8 +10,8 @@
 //                shared memory
 //   warp 1       an elected lane issues tcgen05.mma (M = 128, N = tokens, K = 16)
 //   warp 2       owns the TMEM allocation: the sums, then a ring of weight stages
-//   warps 4-11   dequantize: two warps per 32 lanes, one for the even and one for the odd stages
-//   warps 12-15  epilogue: TMEM -> registers -> bias, residual -> bf16
+//   warps 4 ..   dequantize (8 or 16 warps): per 32 lanes some for the even and some for the odd stages
+//   last 4 warps epilogue: TMEM -> registers -> bias, residual -> bf16
 // Blocks are persistent over the tiles. Where the tiles are too few to fill the GPU, a cluster of 2 to
 // 8 blocks shares a tile along the contraction; the sums meet in shared memory over the cluster, in
 // the order of the ranks.
@@ -39,7 +39,6 @@ namespace {
 
 constexpr int kLtRows = 128;  // weight rows per tile
 constexpr int kLtBK = 64;     // contraction per stage
-constexpr int kLtThreads = 512;
 template <bool kMid>
 struct LtCfg {
   static constexpr int TOK = kMid ? 128 : 256;       // tokens per tile
@@ -47,6 +46,11 @@ struct LtCfg {
   static constexpr int STAGES = 6;                   // weights in TMEM (at most 384 columns), tokens in smem
   static constexpr int B_BYTES = TOK * kLtBK * 2;
   static constexpr int BOX = kMid ? 16 : 64;         // token rows per TMA box
+  // Dequant warps: per 32 lanes, PARTS that share a stage's columns, for the even and for the odd stages. With two
+  // parts (and few tokens to multiply) a stage's chain load -> convert -> store is half as long.
+  static constexpr int PARTS = kMid ? 2 : 1;
+  static constexpr int DQW = 8 * PARTS;
+  static constexpr int THREADS = (4 + DQW + 4) * 32;
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * B_BYTES + 1024 + 512;
 };
 
@@ -129,7 +133,7 @@ __device__ __forceinline__ float lt_epilogue(const LinearArgs& a, float y, float
 }
 
 template <int kBits, bool kMid>
-__global__ void __launch_bounds__(kLtThreads, 1)
+__global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, LinearArgs a, int ks) {
   using C = LtCfg<kMid>;
   extern __shared__ uint8_t lt_raw[];
@@ -148,7 +152,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      tc::mbar_init(full + s, 5);   // four dequant warps (one per lane quarter) and the TMA
+      tc::mbar_init(full + s, 4 * C::PARTS + 1);  // the dequant warps of a stage and the TMA
       tc::mbar_init(empty + s, 1);
     }
     tc::mbar_init(acc_full, 1);
@@ -253,10 +257,12 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       tc::mbar_wait_drain(drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
-    const int q4 = warp & 3, par = (warp - 4) >> 2;
+  } else if (warp >= 4 && warp < 4 + C::DQW) {
+    const int q4 = warp & 3, part = ((warp - 4) >> 2) % C::PARTS, par = ((warp - 4) >> 2) / C::PARTS;
+    constexpr int CPT = kLtBK / C::PARTS;        // codes per thread and stage
+    constexpr int WR = CPT / 2;                  // 32-bit columns they fill
     const uint32_t lane_addr = tmem_a + (static_cast<uint32_t>(q4 * 32) << 16);
-    constexpr int NV = kBits * kLtBK / 128;      // 16-byte vectors of a row's stage: 2 or 4
+    constexpr int NV = kBits * CPT / 128;        // 16-byte vectors of them
     constexpr int PD = kBits == 4 ? 4 : 2;       // own stages in flight in registers
     const int gs = a.group == 64 ? 0 : a.group == 128 ? 1 : 2;
     const int64_t row_bytes = static_cast<int64_t>(a.K) * kBits / 8;
@@ -267,7 +273,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       // rows past the end repeat the last one; their sums are not written
       const int64_t row = min(item % mtiles * kLtRows + q4 * 32 + lane, a.N - 1);
       const int first = (par ^ it0) & 1;
-      const uint8_t* cp = a.codes + row * row_bytes + static_cast<int64_t>(kb0 + first) * (kLtBK * kBits / 8);
+      const uint8_t* cp = a.codes + row * row_bytes + static_cast<int64_t>(kb0 + first) * (kLtBK * kBits / 8) +
+                          part * (CPT * kBits / 8);
       const unsigned short* sp = reinterpret_cast<const unsigned short*>(a.scales) + row * ng;
       const int mine = nk > first ? (nk - first + 1) / 2 : 0;
       uint4 cw[PD][NV];
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           const float sf = __half2float(sh);
           const __nv_bfloat16 sb1 = __float2bfloat16_rn(sf), sb2 = __float2bfloat16_rn(sf - __bfloat162float(sb1));
           const __nv_bfloat162 b1 = __halves2bfloat162(sb1, sb1), b2 = __halves2bfloat162(sb2, sb2);
-          uint32_t w[32], wl[kMid ? 32 : 1];
+          uint32_t w[WR], wl[kMid ? WR : 1];
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
             const uint32_t c[4] = {cw[u][v].x, cw[u][v].y, cw[u][v].z, cw[u][v].w};
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
               const uint32_t other = kBits == 4 ? c[j] >> 4 : c[j] ^ 0x80808080u;
 #pragma unroll
               for (int b = 0; b < 16 / kBits; ++b) {
-                const int at = (16 / kBits * (4 * v + j) + b) & 31;
+                const int at = 16 / kBits * (4 * v + j) + b;
                 if (kMid)
                   lt_split(kBits == 4 ? lt_pair4_bf16(c[j], other, b) : lt_pair8_bf16(c[j], b), b1, b2, w[at],
                            wl[kMid ? at : 0]);
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           if (!kMid && sf > 65504.f / (kBits == 4 ? 8 : 128)) {
             const __half2 top = __floats2half2_rn(65504.f, 65504.f);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < WR; ++i) {
               const __half2 r = __hmin2_nan(__hmax2_nan(*reinterpret_cast<__half2*>(&w[i]), __hneg2(top)), top);
               w[i] = *reinterpret_cast<const uint32_t*>(&r);
             }
@@ -324,8 +331,12 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           ok = tc::warp_wait(empty + s, ((it / C::STAGES) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
           tc::tc_fence_after();
-          tc::tmem_st32(lane_addr + s * C::A_COLS, w);
-          if constexpr (kMid) tc::tmem_st32(lane_addr + s * C::A_COLS + 32, wl);
+          if constexpr (kMid) {
+            tc::tmem_st16(lane_addr + s * C::A_COLS + part * WR, w);
+            tc::tmem_st16(lane_addr + s * C::A_COLS + 32 + part * WR, wl);
+          } else {
+            tc::tmem_st32(lane_addr + s * C::A_COLS, w);
+          }
           tc::tmem_st_wait();
           tc::tc_fence_before();
           __syncwarp();
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + C::DQW) {
     const int q4 = warp & 3;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     int tcount = 0;
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     if (n < a.N && !abort_flag_s) {
       const float bias = a.bias ? a.bias[n] : 0.f;
       const uint32_t base = tc::smem_u32(smem) + r * 4;
-      for (int c = nt * rank / ks + (threadIdx.x >> 7); c < nt * (rank + 1) / ks; c += kLtThreads / kLtRows) {
+      for (int c = nt * rank / ks + (threadIdx.x >> 7); c < nt * (rank + 1) / ks; c += C::THREADS / kLtRows) {
         float y = 0.f;
         for (int k = 0; k < ks; ++k) y += tc::ld_cluster_f32(tc::cluster_map(base + c * kLtRows * 4, k));
         a.out[(t0 + c) * a.out_stride + n] = __float2bfloat16_rn(lt_epilogue(a, y, bias, t0 + c, n));
@@ -452,7 +463,7 @@ cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ks > 1 ? items * ks : std::min<int64_t>(items, num_sms)));
-  cfg.blockDim = dim3(kLtThreads);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
