@@ -81,6 +81,7 @@ class strata_kv_batch(ctypes.Structure):
 
 
 _lib = None
+_byref = ctypes.byref
 _P = ctypes.c_void_p
 _F32 = ctypes.c_float
 _I64 = ctypes.c_int64
@@ -149,11 +150,12 @@ def lib() -> ctypes.CDLL:
 
 def ptr(t) -> int | None:
     """Device pointer of a torch tensor (or pass through an int / None)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
 
 
 _raw_stream = None      # (device index) -> handle of torch's current stream, once CUDA is in use
@@ -170,8 +172,8 @@ def stream_handle(stream) -> int | None:
             if torch.cuda.is_available():
                 h = torch.cuda.current_stream().cuda_stream
                 # the same lookup without building a Stream object: 0.3 us against 7 us a call
-                if hasattr(torch._C, "_cuda_getCurrentRawStream"):
-                    _current_device = torch.cuda.current_device
+                if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+                    _current_device = torch._C._cuda_getDevice
                     _raw_stream = torch._C._cuda_getCurrentRawStream
                 return h
         except Exception:  # pragma: no cover
@@ -308,9 +310,9 @@ def strata_linear_workspace_size(lin: strata_linear, T_max: int) -> int:
 def strata_linear_forward(lin: strata_linear, x, T, out, workspace, ws_bytes, x_stride=None,
                           residual=None, residual_stride=None, out_stride=None, stream=None):
     """Strides in elements; None: rows follow one another."""
-    return lib().strata_linear_forward(
-        ctypes.byref(lin), ptr(x), lin.K if x_stride is None else x_stride, T, ptr(residual),
-        lin.N if residual_stride is None else residual_stride, ptr(out),
+    return (_lib or lib()).strata_linear_forward(
+        _byref(lin), ptr(x), lin.K if x_stride is None else x_stride, T,
+        None if residual is None else ptr(residual), lin.N if residual_stride is None else residual_stride, ptr(out),
         lin.N if out_stride is None else out_stride, ptr(workspace), ws_bytes, stream_handle(stream))
 
 
@@ -318,13 +320,18 @@ def strata_kv_append(cache: strata_kv_cache, k, v, T, slots, positions=None, rop
                      rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
                      q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
     """Strides in elements; None: rows follow one another."""
-    kv = cache.n_kv_heads * cache.head_dim
-    qd = n_heads * cache.head_dim
-    return lib().strata_kv_append(
-        ctypes.byref(cache), ptr(q), qd if q_stride is None else q_stride, n_heads, ptr(k),
-        kv if k_stride is None else k_stride, ptr(v), kv if v_stride is None else v_stride, T,
-        ptr(slots), ptr(positions), ptr(rope), n_pos, rot_dim, flags, ptr(q_out),
-        qd if q_out_stride is None else q_out_stride, ptr(dev_status), stream_handle(stream))
+    if k_stride is None or v_stride is None:
+        kv = cache.n_kv_heads * cache.head_dim
+        k_stride = kv if k_stride is None else k_stride
+        v_stride = kv if v_stride is None else v_stride
+    if q_stride is None or q_out_stride is None:
+        qd = n_heads * cache.head_dim
+        q_stride = qd if q_stride is None else q_stride
+        q_out_stride = qd if q_out_stride is None else q_out_stride
+    return (_lib or lib()).strata_kv_append(
+        _byref(cache), None if q is None else ptr(q), q_stride, n_heads, ptr(k), k_stride, ptr(v), v_stride, T,
+        ptr(slots), ptr(positions), ptr(rope), n_pos, rot_dim, flags, None if q_out is None else ptr(q_out),
+        q_out_stride, None if dev_status is None else ptr(dev_status), stream_handle(stream))
 
 
 def strata_attention_workspace_size(cache: strata_kv_cache, batch: strata_kv_batch, n_heads) -> int:
@@ -335,10 +342,12 @@ def strata_attention_forward(cache: strata_kv_cache, batch: strata_kv_batch, q, 
                              workspace, ws_bytes, window=0, flags=0, q_stride=None, out_stride=None,
                              stream=None):
     """Strides in elements; None: rows follow one another."""
-    qd = n_heads * cache.head_dim
-    return lib().strata_attention_forward(
-        ctypes.byref(cache), ctypes.byref(batch), ptr(q), qd if q_stride is None else q_stride,
-        n_heads, scale, window, flags, ptr(out), qd if out_stride is None else out_stride,
+    if q_stride is None or out_stride is None:
+        qd = n_heads * cache.head_dim
+        q_stride = qd if q_stride is None else q_stride
+        out_stride = qd if out_stride is None else out_stride
+    return (_lib or lib()).strata_attention_forward(
+        _byref(cache), _byref(batch), ptr(q), q_stride, n_heads, scale, window, flags, ptr(out), out_stride,
         ptr(workspace), ws_bytes, stream_handle(stream))
 
 

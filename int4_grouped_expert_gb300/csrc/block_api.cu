@@ -2,6 +2,7 @@
 // layout and launches. Every check runs before the first CUDA call of an entry point; nothing here
 // allocates, throws or keeps state.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "block.cuh"
@@ -15,10 +16,19 @@ constexpr size_t kWsAlign = 256;
 size_t round_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 strata_status of(cudaError_t e) { return e == cudaSuccess ? STRATA_OK : STRATA_ERR_CUDA; }
+// SMs of the current device, looked up once per device (a property that does not change).
 bool sm_count(int* out) {
+  static std::atomic<int> known[64];
   int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const bool keep = dev >= 0 && dev < 64;
+  int n = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+    if (keep) known[dev].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return true;
 }
 
 strata_status check_linear(const strata_linear* w) {

@@ -45,7 +45,6 @@ struct LtCfg {
   static constexpr int A_COLS = kMid ? 64 : 32;      // TMEM columns of a weight stage
   static constexpr int STAGES = 6;                   // weights in TMEM (at most 384 columns), tokens in smem
   static constexpr int B_BYTES = TOK * kLtBK * 2;
-  static constexpr int BOX = kMid ? 16 : 64;         // token rows per TMA box
   // Dequant warps: per 32 lanes, PARTS that share a stage's columns, for the even and for the odd stages. With two
   // parts (and few tokens to multiply) a stage's chain load -> convert -> store is half as long.
   static constexpr int PARTS = kMid ? 2 : 1;
@@ -134,7 +133,7 @@ __device__ __forceinline__ float lt_epilogue(const LinearArgs& a, float y, float
 
 template <int kBits, bool kMid>
 __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
-    linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, LinearArgs a, int ks) {
+    linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, LinearArgs a, int ks, int box_rows) {
   using C = LtCfg<kMid>;
   extern __shared__ uint8_t lt_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lt_raw) + 1023) &
@@ -190,17 +189,15 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
     int it = 0;
     bool ok = true;
     for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
-      const int nbox = (tokens(item) + C::BOX - 1) / C::BOX;
       const int t0 = item / mtiles * C::TOK;
       for (int kb = 0; kb < nk; ++kb, ++it) {
         const int s = it % C::STAGES;
         ok = tc::warp_wait(empty + s, ((it / C::STAGES) & 1) ^ 1, abort_flag, a.status);
         if (!ok) break;
         if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(full + s, nbox * C::BOX * kLtBK * 2);
-          for (int bx = 0; bx < nbox; ++bx)
-            tc::tma_load_2d(smem + s * C::B_BYTES + bx * C::BOX * kLtBK * 2, &tmap_x, (kb0 + kb) * kLtBK,
-                            t0 + bx * C::BOX, full + s);
+          // (one box: each costs the issuing warp about 130 clocks)
+          tc::mbar_arrive_expect_tx(full + s, box_rows * kLtBK * 2);
+          tc::tma_load_2d(smem + s * C::B_BYTES, &tmap_x, (kb0 + kb) * kLtBK, t0, full + s);
         }
         __syncwarp();
       }
@@ -350,7 +347,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     int tcount = 0;
     for (int item = blockIdx.x / ks; item < n_items; item += step, ++tcount) {
-      if (!tc::warp_wait(acc_full, tcount & 1, abort_flag, a.status)) break;
+      if (!tc::warp_wait_long(acc_full, tcount & 1, abort_flag, a.status)) break;
       tc::tc_fence_after();
       const int n = item % mtiles * kLtRows + q4 * 32 + lane;
       const int64_t t0 = static_cast<int64_t>(item / mtiles) * C::TOK;
@@ -435,12 +432,13 @@ cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
                                         true, a.x, a.x_stride, a.K, a.xh, a.xexp, a.status);
     if (e != cudaSuccess) return e;
   }
-  // the tokens (x itself, or its f16 copy) as a 2-d tensor: boxes of BOX tokens x 64 columns (128 bytes),
+  // the tokens (x itself, or its f16 copy) as a 2-d tensor: boxes of a tile's tokens x 64 columns (128 bytes),
   // zero fill past the last token
+  const int box_rows = static_cast<int>(std::min<int64_t>(C::TOK, (a.T + 15) / 16 * 16));
   CUtensorMap map;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kMid ? a.x_stride : a.K) * 2};
-  const cuuint32_t box[2] = {kLtBK, C::BOX}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {kLtBK, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
   if (enc(&map, kMid ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
           kMid ? const_cast<void*>(static_cast<const void*>(a.x)) : static_cast<void*>(a.xh), dims, strides, box, estr,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -475,7 +473,7 @@ cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<kBits, kMid>, map, a, ks);
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<kBits, kMid>, map, a, ks, box_rows);
 }
 
 }  // namespace

@@ -20,6 +20,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
+// The same for a wait that is known to be long: it sleeps between its looks, and leaves the issue slots to
+// the warps that work.
+__device__ __forceinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               uint32_t* status) {
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) {
+      set_status(status, STRATA_DEV_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+    __nanosleep(100);
+  }
+  return true;
+}
+
 // Whether the phase with `parity` has completed, without waiting (try_wait may sleep in the barrier).
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
