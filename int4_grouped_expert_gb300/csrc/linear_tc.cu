@@ -386,16 +386,41 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
     // one tile per cluster: every rank sums its share of the tokens over the ranks, in their order
     tc::cluster_sync();
     const int item = blockIdx.x / ks;
-    const int nt = tokens(item), r = threadIdx.x & (kLtRows - 1);
-    const int n = item % mtiles * kLtRows + r;
+    const int nt = tokens(item), n0 = item % mtiles * kLtRows;
     const int64_t t0 = static_cast<int64_t>(item / mtiles) * C::TOK;
-    if (n < a.N && !abort_flag_s) {
-      const float bias = a.bias ? a.bias[n] : 0.f;
-      const uint32_t base = tc::smem_u32(smem) + r * 4;
-      for (int c = nt * rank / ks + (threadIdx.x >> 7); c < nt * (rank + 1) / ks; c += C::THREADS / kLtRows) {
-        float y = 0.f;
-        for (int k = 0; k < ks; ++k) y += tc::ld_cluster_f32(tc::cluster_map(base + c * kLtRows * 4, k));
-        a.out[(t0 + c) * a.out_stride + n] = __float2bfloat16_rn(lt_epilogue(a, y, bias, t0 + c, n));
+    const int c0 = nt * rank / ks, items = (nt * (rank + 1) / ks - c0) * (kLtRows / 4);  // (token, four rows)
+    const uint32_t base = tc::smem_u32(smem);
+    constexpr int U = 4;  // items on their way per thread
+    for (int i0 = threadIdx.x; i0 < items && !abort_flag_s; i0 += U * C::THREADS) {
+      float4 y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < ks; ++k) {
+        const uint32_t at = tc::cluster_map(base, k);
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = min(i0 + u * C::THREADS, items - 1);
+          v[u] = tc::ld_cluster_f32x4(at + (c0 * (kLtRows / 4) + i) * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          y[u].x += v[u].x; y[u].y += v[u].y; y[u].z += v[u].z; y[u].w += v[u].w;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * C::THREADS;
+        if (i >= items) break;
+        const int64_t tok = t0 + c0 + i / (kLtRows / 4);
+        const float f[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = n0 + i % (kLtRows / 4) * 4 + j;
+          if (n < a.N)
+            a.out[tok * a.out_stride + n] =
+                __float2bfloat16_rn(lt_epilogue(a, f[j], a.bias ? a.bias[n] : 0.f, tok, n));
+        }
       }
     }
     tc::cluster_sync();  // no block leaves while another reads its sums
