@@ -369,13 +369,13 @@ typedef struct {
  * row; *_stride: elements from one row to the next (>= the row's length; x: a multiple of 8, and x
  * 16-byte aligned). out may be the residual itself (same address and stride); otherwise out
  * overlaps no input. T == 0 is a no-op.
- * Up to STRATA_LINEAR_EXACT_T tokens the products take the weight exactly or to 2^-16 of it; longer
- * batches multiply weights rounded once to f16 (2^-11 relative), with f16 copies of the rows of
+ * Up to STRATA_LINEAR_EXACT_T tokens the codes are multiplied as exact integers and the sums scaled in fp32;
+ * longer batches multiply weights rounded once to f16 (2^-11 relative), with f16 copies of the rows of
  * x in the workspace, each times a power of two that keeps its range.
  * workspace >= strata_linear_workspace_size(w, T) bytes (0: the projection or T is invalid),
  * 256-byte aligned, device; it needs no initialisation. strata_workspace_status reads its status.
  */
-#define STRATA_LINEAR_EXACT_T 128
+#define STRATA_LINEAR_EXACT_T 64
 size_t strata_linear_workspace_size(const strata_linear* w, int64_t T_max);
 strata_status strata_linear_forward(const strata_linear* w, const void* x_bf16, int64_t x_stride,
                                     int64_t T, const void* residual_bf16, int64_t residual_stride,

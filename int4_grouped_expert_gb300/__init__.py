@@ -34,7 +34,7 @@ STRATA_ERR_DEVICE_STATUS = 6
 STRATA_ERR_TIMEOUT = 7
 GROUP_WORKSPACE_BYTES = 256
 GROUP = 128
-LINEAR_EXACT_T = 128  # STRATA_LINEAR_EXACT_T
+LINEAR_EXACT_T = 64  # STRATA_LINEAR_EXACT_T
 
 
 class StrataError(RuntimeError):

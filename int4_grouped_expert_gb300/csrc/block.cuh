@@ -8,8 +8,8 @@ namespace strata {
 
 // Up to this many tokens a projection streams its codes through registers (linear.cu).
 constexpr int kLinearStreamT = 32;
-// Beyond that and up to this many, the tensor cores multiply x with weights in two bf16 parts
-// (linear_tc.cu); more tokens take f16 operands.
+// Beyond that and up to this many, tcgen05 multiplies x with the integer codes (linear_tc.cu); more tokens
+// take f16 operands.
 constexpr int kLinearMidT = STRATA_LINEAR_EXACT_T;
 
 // The power of two that a row of f16 operands is divided by, for its largest bf16 magnitude (key as

@@ -10,19 +10,19 @@
 //                shared memory
 //   warp 1       an elected lane issues tcgen05.mma (M = 128, N = tokens, K = 16)
 //   warp 2       owns the TMEM allocation: the sums, then a ring of weight stages
-//   warps 4 ..   dequantize (8 or 16 warps): per 32 lanes some for the even and some for the odd stages
-//   last 4 warps epilogue: TMEM -> registers -> bias, residual -> bf16
+//   warps 4-11   dequantize: two warps per 32 lanes, one for the even and one for the odd stages
+//   warps 12-15  epilogue: TMEM -> registers -> bias, residual -> bf16
 // Blocks are persistent over the tiles. Where the tiles are too few to fill the GPU, a cluster of 2 to
 // 8 blocks shares a tile along the contraction; the sums meet in shared memory over the cluster, in
 // the order of the ranks.
 //
 // Two operand forms:
-//   up to 128 tokens (kMid)  streaming the codes is what bounds it, so x stays as it is (bf16, no pass
-//       before) and the weight is two bf16 numbers, hi + lo = q * s to 2^-16 of it: with s = s1 + s2 in bf16
-//       (exact), hi = q * s1 rounded, lo = (q * s1 - hi) + q * s2 (the first term exact); two MMAs.
-//   more tokens              the MMAs bound it: f16 operands, w = q * s rounded once (2^-11; bf16 would
-//       leave 2^-8), and a pass before copies x to f16, each row times a power of two that keeps its
-//       range; the epilogue multiplies it back.
+//   up to 64 tokens (kMid)  unpacking the codes is what bounds it, so they are multiplied as exact
+//       bf16 integers with x as it is (bf16, no pass before), group by group into one of four sums in
+//       TMEM, which the epilogue warps multiply by the group's scale and add up in fp32 registers.
+//   more tokens   the MMAs bound it: f16 operands, w = q * s rounded once (2^-11; bf16 would leave 2^-8), and
+//       a pass before copies x to f16, each row times a power of two that keeps its range; the epilogue
+//       multiplies it back.
 //
 // Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every role
 // leaves its loop, in-flight copies and MMAs are drained (bounded) and TMEM is freed.
@@ -39,17 +39,13 @@ namespace {
 
 constexpr int kLtRows = 128;  // weight rows per tile
 constexpr int kLtBK = 64;     // contraction per stage
+constexpr int kLtThreads = 512;
 template <bool kMid>
 struct LtCfg {
-  static constexpr int TOK = kMid ? 128 : 256;       // tokens per tile
-  static constexpr int A_COLS = kMid ? 64 : 32;      // TMEM columns of a weight stage
-  static constexpr int STAGES = 6;                   // weights in TMEM (at most 384 columns), tokens in smem
+  static constexpr int TOK = kMid ? 64 : 256;        // tokens per tile
+  static constexpr int BUFS = kMid ? 4 : 1;          // sums in TMEM (256 columns), then the weight stages
+  static constexpr int STAGES = kMid ? 8 : 6;        // weights in TMEM (32 columns), tokens in shared memory
   static constexpr int B_BYTES = TOK * kLtBK * 2;
-  // Dequant warps: per 32 lanes, PARTS that share a stage's columns, for the even and for the odd stages. With two
-  // parts (and few tokens to multiply) a stage's chain load -> convert -> store is half as long.
-  static constexpr int PARTS = kMid ? 2 : 1;
-  static constexpr int DQW = 8 * PARTS;
-  static constexpr int THREADS = (4 + DQW + 4) * 32;
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * B_BYTES + 1024 + 512;
 };
 
@@ -66,15 +62,6 @@ __device__ __forceinline__ __nv_bfloat162 lt_pair8_bf16(uint32_t w, int pair) {
   const uint32_t m = (v & 0x007F007Fu) | 0x43004300u, b = (v & 0x00800080u) | 0x43004300u;
   return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&b));
 }
-// q * (s1 + s2) as hi + lo
-__device__ __forceinline__ void lt_split(__nv_bfloat162 q, __nv_bfloat162 s1, __nv_bfloat162 s2, uint32_t& hi,
-                                         uint32_t& lo) {
-  const __nv_bfloat162 h = __hmul2(q, s1);
-  const __nv_bfloat162 l = __hfma2(q, s2, __hfma2(q, s1, __hneg2(h)));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
-}
-
 // f16x2 of two codes, exact. 4 bits: codes 2 byte, 2 byte + 1 of an 8-code word; w4 is the word >> 4.
 __device__ __forceinline__ __half2 lt_pair4(uint32_t w, uint32_t w4, int byte) {
   const uint32_t v = prmt(w, w4, byte | (byte + 4) << 8);  // low nibbles of bytes 0 and 2: the codes
@@ -132,7 +119,7 @@ __device__ __forceinline__ float lt_epilogue(const LinearArgs& a, float y, float
 }
 
 template <int kBits, bool kMid>
-__global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
+__global__ void __launch_bounds__(kLtThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, LinearArgs a, int ks, int box_rows) {
   using C = LtCfg<kMid>;
   extern __shared__ uint8_t lt_raw[];
@@ -141,9 +128,9 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::B_BYTES);
   uint64_t* full = bars;                  // a stage's weights and tokens are in place
   uint64_t* empty = full + C::STAGES;     // its MMAs are done
-  uint64_t* acc_full = empty + C::STAGES;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain = acc_empty + 1;
+  uint64_t* acc_full = empty + C::STAGES;  // [BUFS]
+  uint64_t* acc_empty = acc_full + C::BUFS;
+  uint64_t* drain = acc_empty + C::BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag_s;
   volatile int* abort_flag = &abort_flag_s;
@@ -151,11 +138,13 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      tc::mbar_init(full + s, 4 * C::PARTS + 1);  // the dequant warps of a stage and the TMA
+      tc::mbar_init(full + s, 5);   // the four dequant warps of a stage and the TMA
       tc::mbar_init(empty + s, 1);
     }
-    tc::mbar_init(acc_full, 1);
-    tc::mbar_init(acc_empty, 4);      // the epilogue warps
+    for (int i = 0; i < C::BUFS; ++i) {
+      tc::mbar_init(acc_full + i, 1);
+      tc::mbar_init(acc_empty + i, 4);  // the epilogue warps
+    }
     tc::mbar_init(drain, 1);
     tc::fence_barrier_init();
     abort_flag_s = 0;
@@ -169,7 +158,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tmem_a = tmem + C::TOK;
+  const uint32_t tmem_a = tmem + 256;
   griddep_wait();
   griddep_launch();
   if (kMid && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;  // (else the pass before has cleared it)
@@ -179,8 +168,11 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
   const int ttiles = static_cast<int>((a.T + C::TOK - 1) / C::TOK);
   const int n_items = mtiles * ttiles;
   const int rank = blockIdx.x % ks, step = gridDim.x / ks;
-  const int nk_all = a.K / kLtBK;
-  const int kb0 = nk_all * rank / ks, nk = nk_all * (rank + 1) / ks - kb0;  // this rank's stages
+  // a sum's stages: a scale group, or the whole contraction; and this rank's share of them
+  const int per = kMid ? a.group / kLtBK : a.K / kLtBK, share = kMid ? per : 1;
+  const int parts = a.K / kLtBK / share;
+  const int kb0 = parts * rank / ks * share, nk = parts * (rank + 1) / ks * share - kb0;
+  const int n_sums = kMid ? nk / per : 1;   // sums per tile
   auto tokens = [&](int item) {
     return static_cast<int>(min(static_cast<int64_t>(C::TOK), a.T - static_cast<int64_t>(item / mtiles) * C::TOK));
   };
@@ -212,17 +204,26 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
   } else if (warp == 1) {
     // The loop looks at the next stage's barrier while this stage's MMAs are issued: a wait costs about 100
     // clocks even when there is nothing to wait for.
-    int s = 0, tcount = 0;
+    int s = 0, sum = 0;  // stage, and sums begun
     uint32_t ph = 0;
     bool ok = true, ready = false;
     const uint64_t db0 = tc::sw128_desc(tc::smem_u32(smem));
-    for (int item = blockIdx.x / ks; ok && item < n_items; item += step, ++tcount) {
+    for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
       const int n_mma = (tokens(item) + 15) & ~15;
       const uint32_t idesc = kMid ? tc::idesc_bf16(kLtRows, n_mma) : tc::idesc_f16(kLtRows, n_mma);
-      ok = tcount == 0 || tc::warp_wait(acc_empty, (tcount - 1) & 1, abort_flag, a.status);
-      if (!ok) break;
-      tc::tc_fence_after();
+      int left = 0;      // stages of the sum in work still to come
+      uint32_t dt = tmem;
       for (int kb = 0; kb < nk; ++kb) {
+        const bool begins = kMid ? left == 0 : kb == 0;
+        if (begins) {
+          left = kMid ? per : nk;
+          const int buf = sum % C::BUFS;
+          dt = tmem + buf * C::TOK;
+          ok = sum < C::BUFS || tc::warp_wait(acc_empty + buf, (sum / C::BUFS - 1) & 1, abort_flag, a.status);
+          if (!ok) break;
+          ++sum;
+        }
+        --left;
         if (!ready) {
           ok = tc::warp_wait(full + s, ph, abort_flag, a.status);
           if (!ok) break;
@@ -233,14 +234,12 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
         const bool next = tc::mbar_test(full + s1, ph1);
         if (tc::elect_one()) {
           const uint64_t db = db0 + s * (C::B_BYTES >> 4);
-          const uint32_t da = tmem_a + s * C::A_COLS;
+          const uint32_t da = tmem_a + s * 32;
 #pragma unroll
-          for (int kk = 0; kk < kLtBK / 16; ++kk) {
-            tc::mma_f16_ts(tmem, da + 8 * kk, db + 2 * kk, idesc, (kb | kk) ? 1u : 0u);
-            if (kMid) tc::mma_f16_ts(tmem, da + 32 + 8 * kk, db + 2 * kk, idesc, 1u);
-          }
+          for (int kk = 0; kk < kLtBK / 16; ++kk)
+            tc::mma_f16_ts(dt, da + 8 * kk, db + 2 * kk, idesc, (kk > 0 || !begins) ? 1u : 0u);
           tc::mma_commit(empty + s);
-          if (kb == nk - 1) tc::mma_commit(acc_full);
+          if (left == 0) tc::mma_commit(acc_full + (sum - 1) % C::BUFS);
         }
         __syncwarp();
         ready = __all_sync(0xffffffffu, next);
@@ -254,12 +253,10 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
       tc::mbar_wait_drain(drain, 0);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 4 + C::DQW) {
-    const int q4 = warp & 3, part = ((warp - 4) >> 2) % C::PARTS, par = ((warp - 4) >> 2) / C::PARTS;
-    constexpr int CPT = kLtBK / C::PARTS;        // codes per thread and stage
-    constexpr int WR = CPT / 2;                  // 32-bit columns they fill
+  } else if (warp >= 4 && warp < 12) {
+    const int q4 = warp & 3, par = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem_a + (static_cast<uint32_t>(q4 * 32) << 16);
-    constexpr int NV = kBits * CPT / 128;        // 16-byte vectors of them
+    constexpr int NV = kBits * kLtBK / 128;      // 16-byte vectors of a row's stage: 2 or 4
     constexpr int PD = kBits == 4 ? 4 : 2;       // own stages in flight in registers
     const int gs = a.group == 64 ? 0 : a.group == 128 ? 1 : 2;
     const int64_t row_bytes = static_cast<int64_t>(a.K) * kBits / 8;
@@ -270,8 +267,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
       // rows past the end repeat the last one; their sums are not written
       const int64_t row = min(item % mtiles * kLtRows + q4 * 32 + lane, a.N - 1);
       const int first = (par ^ it0) & 1;
-      const uint8_t* cp = a.codes + row * row_bytes + static_cast<int64_t>(kb0 + first) * (kLtBK * kBits / 8) +
-                          part * (CPT * kBits / 8);
+      const uint8_t* cp = a.codes + row * row_bytes + static_cast<int64_t>(kb0 + first) * (kLtBK * kBits / 8);
       const unsigned short* sp = reinterpret_cast<const unsigned short*>(a.scales) + row * ng;
       const int mine = nk > first ? (nk - first + 1) / 2 : 0;
       uint4 cw[PD][NV];
@@ -281,7 +277,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
         const uint4* p = reinterpret_cast<const uint4*>(cp + static_cast<int64_t>(m) * (2 * kLtBK * kBits / 8));
 #pragma unroll
         for (int v = 0; v < NV; ++v) cw[u][v] = __ldg(p + v);
-        sw[u] = __ldg(sp + ((kb0 + first + 2 * m) >> gs));
+        if (!kMid) sw[u] = __ldg(sp + ((kb0 + first + 2 * m) >> gs));
       };
 #pragma unroll
       for (int u = 0; u < PD; ++u) load(u, u);
@@ -291,12 +287,9 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
           const int m = m0 + u;
           if (m >= mine) break;
           const int it = it0 + first + 2 * m, s = it % C::STAGES;
-          const __half sh = __ushort_as_half(sw[u]);
+          const __half sh = __ushort_as_half(kMid ? 0 : sw[u]);
           const __half2 s2 = __halves2half2(sh, sh);
-          const float sf = __half2float(sh);
-          const __nv_bfloat16 sb1 = __float2bfloat16_rn(sf), sb2 = __float2bfloat16_rn(sf - __bfloat162float(sb1));
-          const __nv_bfloat162 b1 = __halves2bfloat162(sb1, sb1), b2 = __halves2bfloat162(sb2, sb2);
-          uint32_t w[WR], wl[kMid ? WR : 1];
+          uint32_t w[32];
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
             const uint32_t c[4] = {cw[u][v].x, cw[u][v].y, cw[u][v].z, cw[u][v].w};
@@ -305,20 +298,21 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
               const uint32_t other = kBits == 4 ? c[j] >> 4 : c[j] ^ 0x80808080u;
 #pragma unroll
               for (int b = 0; b < 16 / kBits; ++b) {
-                const int at = 16 / kBits * (4 * v + j) + b;
-                if (kMid)
-                  lt_split(kBits == 4 ? lt_pair4_bf16(c[j], other, b) : lt_pair8_bf16(c[j], b), b1, b2, w[at],
-                           wl[kMid ? at : 0]);
-                else
-                  w[at] = lt_scaled(kBits == 4 ? lt_pair4(c[j], other, b) : lt_pair8(other, b), s2);
+                uint32_t& d = w[16 / kBits * (4 * v + j) + b];
+                if (kMid) {
+                  const __nv_bfloat162 q = kBits == 4 ? lt_pair4_bf16(c[j], other, b) : lt_pair8_bf16(c[j], b);
+                  d = *reinterpret_cast<const uint32_t*>(&q);
+                } else {
+                  d = lt_scaled(kBits == 4 ? lt_pair4(c[j], other, b) : lt_pair8(other, b), s2);
+                }
               }
             }
           }
           // weights of the largest fp16 magnitudes may round to inf: they stay finite (nan stays nan)
-          if (!kMid && sf > 65504.f / (kBits == 4 ? 8 : 128)) {
+          if (!kMid && __half2float(sh) > 65504.f / (kBits == 4 ? 8 : 128)) {
             const __half2 top = __floats2half2_rn(65504.f, 65504.f);
 #pragma unroll
-            for (int i = 0; i < WR; ++i) {
+            for (int i = 0; i < 32; ++i) {
               const __half2 r = __hmin2_nan(__hmax2_nan(*reinterpret_cast<__half2*>(&w[i]), __hneg2(top)), top);
               w[i] = *reinterpret_cast<const uint32_t*>(&r);
             }
@@ -328,12 +322,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
           ok = tc::warp_wait(empty + s, ((it / C::STAGES) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
           tc::tc_fence_after();
-          if constexpr (kMid) {
-            tc::tmem_st16(lane_addr + s * C::A_COLS + part * WR, w);
-            tc::tmem_st16(lane_addr + s * C::A_COLS + 32 + part * WR, wl);
-          } else {
-            tc::tmem_st32(lane_addr + s * C::A_COLS, w);
-          }
+          tc::tmem_st32(lane_addr + s * 32, w);
           tc::tmem_st_wait();
           tc::tc_fence_before();
           __syncwarp();
@@ -342,43 +331,82 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4 + C::DQW) {
+  } else if (warp >= 12) {
     const int q4 = warp & 3;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-    int tcount = 0;
-    for (int item = blockIdx.x / ks; item < n_items; item += step, ++tcount) {
-      if (!tc::warp_wait_long(acc_full, tcount & 1, abort_flag, a.status)) break;
-      tc::tc_fence_after();
+    int sum = 0;
+    bool ok = true;
+    for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
       const int n = item % mtiles * kLtRows + q4 * 32 + lane;
       const int64_t t0 = static_cast<int64_t>(item / mtiles) * C::TOK;
       const int nt = tokens(item);
       const float bias = a.bias && n < a.N ? a.bias[n] : 0.f;
       float* sums = reinterpret_cast<float*>(smem);  // ks > 1: [token][row], in place of the stages
-      for (int c = 0; c < nt; c += 32) {
-        uint32_t r[32];
-        tc::tmem_ld32(lane_addr + c, r);
-        const float my_up = !kMid && c + lane < nt ? exp2i(a.xexp[t0 + c + lane]) : 0.f;
-        tc::tmem_ld_wait();
-        if (!kMid) {
+      if constexpr (kMid) {
+        float acc[C::TOK];
+#pragma unroll
+        for (int c = 0; c < C::TOK; ++c) acc[c] = 0.f;
+        const __half* sp = a.scales + static_cast<int64_t>(min(n, a.N - 1)) * (a.K / a.group) + kb0 / per;
+        __half next = n_sums > 0 ? __ldg(sp) : __half(0.f);
+        for (int i = 0; i < n_sums; ++i, ++sum) {
+          const int buf = sum % C::BUFS;
+          const float sc = __half2float(next);
+          if (i + 1 < n_sums) next = __ldg(sp + i + 1);
+          ok = tc::warp_wait(acc_full + buf, (sum / C::BUFS) & 1, abort_flag, a.status);
+          if (!ok) break;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < C::TOK; c += 16) {
+            if (c >= nt) break;
+            uint32_t r[16];
+            tc::tmem_ld16(lane_addr + buf * C::TOK + c, r);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(sc, __uint_as_float(r[j]), acc[c + j]);
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(acc_empty + buf);
+        }
+        if (!ok) break;
+        // (the last sum is complete, so this rank's stages are free for its sums)
+#pragma unroll
+        for (int c = 0; c < C::TOK; ++c) {
+          if (c >= nt) break;
+          if (ks > 1)
+            sums[c * kLtRows + q4 * 32 + lane] = acc[c];
+          else if (n < a.N)
+            a.out[(t0 + c) * a.out_stride + n] = __float2bfloat16_rn(lt_epilogue(a, acc[c], bias, t0 + c, n));
+        }
+      } else {
+        ok = tc::warp_wait_long(acc_full, sum & 1, abort_flag, a.status);
+        if (!ok) break;
+        ++sum;
+        tc::tc_fence_after();
+        for (int c = 0; c < nt; c += 32) {
+          uint32_t r[32];
+          tc::tmem_ld32(lane_addr + c, r);
+          const float my_up = c + lane < nt ? exp2i(a.xexp[t0 + c + lane]) : 0.f;
+          tc::tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(0xffffffffu, my_up, j));
-        }
-        if (ks > 1) {
+          if (ks > 1) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < nt) sums[(c + j) * kLtRows + q4 * 32 + lane] = __uint_as_float(r[j]);
-        } else if (n < a.N) {
+            for (int j = 0; j < 32; ++j)
+              if (c + j < nt) sums[(c + j) * kLtRows + q4 * 32 + lane] = __uint_as_float(r[j]);
+          } else if (n < a.N) {
+            __nv_bfloat16* dst = a.out + (t0 + c) * a.out_stride + n;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < nt)
-              a.out[(t0 + c + j) * a.out_stride + n] =
-                  __float2bfloat16_rn(lt_epilogue(a, __uint_as_float(r[j]), bias, t0 + c + j, n));
+            for (int j = 0; j < 32; ++j)
+              if (c + j < nt)
+                dst[j * a.out_stride] = __float2bfloat16_rn(lt_epilogue(a, __uint_as_float(r[j]), bias, t0 + c + j, n));
+          }
         }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(acc_empty);
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(acc_empty);
     }
   }
   __syncwarp();
@@ -391,7 +419,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
     const int c0 = nt * rank / ks, items = (nt * (rank + 1) / ks - c0) * (kLtRows / 4);  // (token, four rows)
     const uint32_t base = tc::smem_u32(smem);
     constexpr int U = 4;  // items on their way per thread
-    for (int i0 = threadIdx.x; i0 < items && !abort_flag_s; i0 += U * C::THREADS) {
+    for (int i0 = threadIdx.x; i0 < items && !abort_flag_s; i0 += U * kLtThreads) {
       float4 y[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -400,7 +428,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
         float4 v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int i = min(i0 + u * C::THREADS, items - 1);
+          const int i = min(i0 + u * kLtThreads, items - 1);
           v[u] = tc::ld_cluster_f32x4(at + (c0 * (kLtRows / 4) + i) * 16);
         }
 #pragma unroll
@@ -410,7 +438,7 @@ __global__ void __launch_bounds__(LtCfg<kMid>::THREADS, 1)
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * C::THREADS;
+        const int i = i0 + u * kLtThreads;
         if (i >= items) break;
         const int64_t tok = t0 + c0 + i / (kLtRows / 4);
         const float f[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
@@ -470,15 +498,15 @@ cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const int64_t items = static_cast<int64_t>((a.N + kLtRows - 1) / kLtRows) * ((a.T + C::TOK - 1) / C::TOK);
-  const int nk = a.K / kLtBK;
+  const int nk = a.K / kLtBK, parts = kMid ? a.K / a.group : nk;
   // contraction splits: stages of a share + about 8 stages' worth of start, drain and join, only while a
   // tile per cluster fits the GPU at once. Clusters of k blocks of this size that 152 SMs hold (the
   // GPU processing clusters leave some SMs over): 76, 46, 36, 28, 23, 15, 15 for k = 2 .. 8.
   constexpr int kHeld[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
   int ks = 1;
   int64_t best = (items + num_sms - 1) / num_sms * (nk + 8);
-  for (int k = 2; k <= 8 && nk >= 4 * k; ++k) {
-    const int64_t cost = (nk + k - 1) / k + 8 + k;
+  for (int k = 2; k <= 8 && nk >= 4 * k && parts >= k; ++k) {
+    const int64_t cost = (parts + k - 1) / k * (nk / parts) + 8 + k;
     if (items * 152 <= static_cast<int64_t>(kHeld[k]) * num_sms && cost < best) best = cost, ks = k;
   }
   const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<kBits, kMid>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -486,7 +514,7 @@ cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ks > 1 ? items * ks : std::min<int64_t>(items, num_sms)));
-  cfg.blockDim = dim3(C::THREADS);
+  cfg.blockDim = dim3(kLtThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -34,7 +34,7 @@ class Twin:
 
     def linear(self, lin, x, out, residual=None):
         want, bound = ref.linear(x, lin.codes.cpu().numpy().view(np.uint8), lin.scales.cpu().numpy(), lin.bits, 128,
-                                 residual=residual, rounded_weights=len(x) > 128)
+                                 residual=residual, rounded_weights=len(x) > 64)
         assert (np.abs(out - want) <= bound).all()
 
     def check(self, x, batch_new, pages, slots, positions, b):
@@ -44,7 +44,7 @@ class Twin:
         # q in the buffer is rotated already: k and v show the projection, then q after the rotation
         w = np.s_[Hq * D:]
         full, bound = ref.linear(x, k.qkv.codes.cpu().numpy().view(np.uint8), k.qkv.scales.cpu().numpy(), 8, 128,
-                                 rounded_weights=T > 128)
+                                 rounded_weights=T > 64)
         assert (np.abs(qkv[:, w] - full[:, w]) <= bound[:, w]).all()
         rope = k.rope.cpu().numpy().astype(np.float64)
         h = k.rot // 2
