@@ -16,13 +16,19 @@
 // needs no reduction across lanes and no rescaling of O. A page's V scale, relative to the largest
 // that the warp has met, multiplies the weights.
 //
-// The work is cut by the lengths that the call finds on the device: a (sequence, K/V head) whose steps
-// exceed an even share of all steps is cut into equal pieces, and a block takes one piece. So the blocks
-// run in one wave where the batch allows it, whatever the mix of lengths. (Blocks that start in a
-// later wave cost the time to find their work, fill their slots and join: about 8 us a wave measured.)
-// A block's warps join their results in shared memory; pieces leave reference, sum and fp32 rows in the
-// workspace, the last piece to arrive in a group of up to 8 (or the root of the count) joins the group's,
-// and the last group the groups'. All sums are in the order of the pieces.
+// The work is cut by the lengths that the call finds on the device, in one of two ways.
+// Up to 228 pairs of (sequence, K/V head): a pair whose steps exceed an even share of all steps is cut into
+// equal pieces, and a block takes one piece; its warps join in shared memory. The share is the smallest of
+// three with which all blocks start at once: rounding up adds half a block a pair for mixed lengths, a
+// whole one at worst. (Eight heads of 16 sequences of 8192: 512 blocks for 456 places took 66 us, 384 take 51.)
+// More pairs: each warp takes an even share of all steps, through the middle of pairs, and goes through its
+// pairs alone, copying ahead from one to the next. Blocks that start in later waves cost the time to find
+// their work, fill their slots and join, about 8 us a wave: 500 sequences of 300 231 us against 74, 256 of
+// 1000 118 against 97, 64 of 4096 106 against 99. With few pairs a share means two joins, one after the
+// other, without help from other warps: 24 sequences of 8192 82 us against 70, one of 200 14 against 6.
+// Either way pieces leave reference, sum and fp32 rows in the workspace, the last to arrive in a
+// group of up to 8 (or the root of the count) joins the group's, and the last group the groups'. All sums are
+// in the order of the pieces.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -33,6 +39,7 @@ constexpr int kAttWarps = 4;
 constexpr int kAttStep = 32;  // tokens of one warp step
 constexpr int kAttSlots = 2;  // steps of a warp in shared memory
 constexpr int kAttMinSteps = 8;      // steps that a piece has at least: two a warp
+constexpr int kAttMinShare = 2;      // steps that a warp's share has at least (200 sequences of 50: 2 12.3 us, 4 18.7)
 constexpr int kAttResident = 456;    // blocks that run at once: three on each of 152 SMs
 
 // Transposes an 8x8 matrix of 16-bit elements held one row per quad.
@@ -50,6 +57,10 @@ __device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], u
 // 16 bytes to shared memory, or zeros when there is nothing to copy.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
 // Which token of a 16-token tile is row i (< 8) of an MMA tile, and i + 8 the one 8 further: chosen with
@@ -85,7 +96,13 @@ struct Piece {
 __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
   if (a.b.n_seq == 1) {
     const int steps = seq_steps(a, seq_view(a, 0, blockIdx.x == 0 && threadIdx.x == 0)).n, heads = a.c.n_kv_heads;
-    const int per = max(kAttMinSteps, (steps * heads + a.pieces - 1) / a.pieces), k = (steps + per - 1) / per;
+    int k = 1;
+    for (int q = 2; q <= 4; ++q) {
+      const int pieces = kAttResident - heads * q / 4;
+      const int per = max(kAttMinSteps, static_cast<int>((static_cast<int64_t>(steps) * heads + pieces - 1) / pieces));
+      k = (steps + per - 1) / per;
+      if (k * heads <= kAttResident) break;
+    }
     if (static_cast<int>(blockIdx.x) >= k * heads) return false;
     const int head = blockIdx.x / k;
     p = {0, head, static_cast<int>(blockIdx.x) - head * k, k, head * k};
@@ -99,17 +116,23 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
   int mine = 0;
   for (int s = s0; s < s1; ++s) mine += seq_steps(a, seq_view(a, s, flag)).n;
   const int kept = mine;  // per_lane == 1: the lane's steps
-  const int heads = a.c.n_kv_heads;
+  const int heads = a.c.n_kv_heads, pairs = heads * a.b.n_seq;
   const unsigned total = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)) * heads;  // < 2^31 (host)
-  const int per = max(kAttMinSteps, static_cast<int>((total + a.pieces - 1) / a.pieces));
+  int per = 0, blocks = 0, slots = 0;
   // blocks and workspace slots that a sequence's steps come to
   auto count = [&](int steps, int& blocks, int& slots) {
     const int k = (steps + per - 1) / per * heads;
     blocks += k;
     slots += k > heads ? k : 0;
   };
-  int blocks = 0, slots = 0;
-  for (int s = s0; s < s1; ++s) count(per_lane == 1 ? kept : seq_steps(a, seq_view(a, s, false)).n, blocks, slots);
+  // the smallest pieces of three that still start together
+  for (int q = 2; q <= 4; ++q) {
+    const int pieces = kAttResident - pairs * q / 4;
+    per = max(kAttMinSteps, static_cast<int>((total + pieces - 1) / pieces));
+    blocks = slots = 0;
+    for (int s = s0; s < s1; ++s) count(per_lane == 1 ? kept : seq_steps(a, seq_view(a, s, false)).n, blocks, slots);
+    if (__reduce_add_sync(0xffffffffu, static_cast<unsigned>(blocks)) <= kAttResident) break;
+  }
   int b_at = blocks, s_at = slots;  // inclusive scans
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -146,7 +169,71 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
   return true;
 }
 
-template <int kD, int kNT>
+// A place in the list of all steps: step `at` of the n of (sequence, head); sequences in order, heads within.
+struct Walk {
+  int seq, head, at;
+  SeqSteps st;
+  SeqView v;
+  __device__ __forceinline__ void open(const AttnArgs& a, int s) {
+    seq = s;
+    v = seq_view(a, s, false);
+    st = seq_steps(a, v);
+  }
+  // Moves on by m steps of this head, which has at least as many left. (Not called past the last step.)
+  __device__ __forceinline__ void move(const AttnArgs& a, int m) {
+    at += m;
+    if (at < st.n) return;
+    at = 0;
+    if (++head < a.c.n_kv_heads) return;
+    head = 0;
+    do open(a, seq + 1);
+    while (st.n == 0 && seq + 1 < a.b.n_seq);
+  }
+};
+// This warp's share of all steps: `per` of them from number `warp * per` on, and where that is.
+struct Share {
+  int per, total, todo;
+};
+__device__ __forceinline__ bool find_share(const AttnArgs& a, Share& sh, Walk& w) {
+  const int lane = threadIdx.x & 31, heads = a.c.n_kv_heads;
+  const int per_lane = (a.b.n_seq + 31) / 32;
+  const int s0 = min(a.b.n_seq, lane * per_lane), s1 = min(a.b.n_seq, s0 + per_lane);
+  const bool flag = blockIdx.x == 0 && threadIdx.x < 32;
+  int mine = 0;
+  for (int s = s0; s < s1; ++s) mine += seq_steps(a, seq_view(a, s, flag)).n * heads;
+  int end = mine;  // inclusive scan
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, end, d);
+    if (lane >= d) end += x;
+  }
+  sh.total = __shfl_sync(0xffffffffu, end, 31);  // < 2^31 (host)
+  const int warps = gridDim.x * kAttWarps, id = blockIdx.x * kAttWarps + (threadIdx.x >> 5);
+  sh.per = max(kAttMinShare, (sh.total + warps - 1) / warps);
+  const int64_t from = static_cast<int64_t>(id) * sh.per;
+  if (from >= sh.total) return false;
+  const int begin = static_cast<int>(from);
+  sh.todo = min(sh.per, sh.total - begin);
+  const int owner = __ffs(__ballot_sync(0xffffffffu, begin < end)) - 1;
+  int seq = 0, left = begin - (end - mine);
+  if (lane == owner) {
+    for (seq = s0; seq < s1; ++seq) {
+      const int n = seq_steps(a, seq_view(a, seq, false)).n * heads;
+      if (left < n) break;
+      left -= n;
+    }
+  }
+  seq = __shfl_sync(0xffffffffu, seq, owner);
+  left = __shfl_sync(0xffffffffu, left, owner);
+  w.open(a, seq);
+  w.head = left / w.st.n;
+  w.at = left % w.st.n;
+  return true;
+}
+
+// kSolo: each warp takes an even share of all steps and goes through its (sequence, head) pairs alone.
+// Otherwise a block takes one piece of a pair.
+template <int kD, int kNT, bool kSolo>
 __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a) {
   constexpr int COLS = 8 * kNT;
   constexpr int KW = kD / 64;       // 16-byte pieces of a K row per lane
@@ -165,26 +252,39 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     __device__ ~Last() { if (wait) griddep_wait(); }
   } last_wait{a.beside};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int G = a.group;
   Piece pc;
-  if (!find_piece(a, pc)) return;
-  const int h = pc.head, s = pc.seq;
-  const SeqView sv = seq_view(a, s, false);
-  const SeqSteps st = seq_steps(a, sv);
-  const int G = a.group, rows = sv.n * G;  // <= COLS
-  // positions of the first and last query; the tokens of the piece
-  const int p_lo = sv.len - sv.n, p_hi = sv.len - 1;
-  const int lo = (st.first + static_cast<int>(static_cast<int64_t>(st.n) * pc.index / pc.of)) * kAttStep;
-  const int hi = min(sv.len, (st.first + static_cast<int>(static_cast<int64_t>(st.n) * (pc.index + 1) / pc.of)) * kAttStep);
+  Walk now{}, ahead{};  // (kSolo) the step at hand, and the next to copy
+  Share share;
+  int h, s, rows;   // the (sequence, head) at hand and its rows: <= COLS
+  SeqView sv;
+  int p_lo, p_hi;   // positions of the first and last query
+  int lo, hi;       // the tokens of the piece
+  auto take = [&](int seq, int head, const SeqView& v) {
+    s = seq, h = head, sv = v, rows = v.n * G;
+    p_lo = v.len - v.n, p_hi = v.len - 1;
+  };
+  if constexpr (kSolo) {
+    if (!find_share(a, share, now)) return;
+    ahead = now;
+  } else {
+    if (!find_piece(a, pc)) return;
+    take(pc.seq, pc.head, seq_view(a, pc.seq, false));
+    const SeqSteps st = seq_steps(a, sv);
+    lo = (st.first + static_cast<int>(static_cast<int64_t>(st.n) * pc.index / pc.of)) * kAttStep;
+    hi = min(sv.len, (st.first + static_cast<int>(static_cast<int64_t>(st.n) * (pc.index + 1) / pc.of)) * kAttStep);
+  }
 
   // ---- copies: a lane moves piece lane % PIECES of rows lane / PIECES, + 32 / PIECES, ...
   constexpr int PIECES = kD / 16, RPI = 32 / PIECES, NI = kAttStep / RPI;
   const int pshift = 31 - __clz(a.c.page_size), pmask = a.c.page_size - 1;
-  const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
   uint8_t* ring = att_smem + warp * (kAttSlots * 2 * KB);
   const uint32_t ring_addr = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   // of each slot's two tiles: K scale, V scale (negative: the tile lies in a page that does not exist)
   __shared__ float2 s_scale[kAttWarps][kAttSlots][2];
-  auto issue = [&](int j0, int i_slot) {
+  const uint32_t scale_addr = static_cast<uint32_t>(__cvta_generic_to_shared(&s_scale[warp][0][0]));
+  auto issue = [&](int s, int h, int hi, int j0, int i_slot) {
+    const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
     const uint32_t slot = ring_addr + i_slot * 2 * KB;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -198,9 +298,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
         }
       }
       const int64_t ph = page < 0 ? 0 : static_cast<int64_t>(page) * a.c.n_kv_heads + h;
-      const float2 scale = page < 0 ? make_float2(0.f, page == -2 ? -1.f : 0.f)
-                                    : make_float2(input(a, a.c.k_scales + ph), input(a, a.c.v_scales + ph));
-      if (lane == 0) s_scale[warp][i_slot][u] = scale;
+      // (the scales arrive with the codes: waiting for them here would cost a warp a DRAM latency per step)
+      if (page >= 0 && !a.beside) {
+        if (lane < 2) copy4(scale_addr + (i_slot * 2 + u) * 8 + lane * 4, (lane ? a.c.v_scales : a.c.k_scales) + ph);
+      } else if (lane == 0) {
+        s_scale[warp][i_slot][u] = page < 0 ? make_float2(0.f, page == -2 ? -1.f : 0.f)
+                                            : make_float2(__ldcg(a.c.k_scales + ph), __ldcg(a.c.v_scales + ph));
+      }
       const int64_t base = ((ph << pshift) + (j & pmask)) * kD + lane * 16;
       const int n = page < 0 ? 0 : hi - j;  // tokens of the tile from here on; past them: zeros
 #pragma unroll
@@ -213,65 +317,84 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       }
     }
   };
-  int j_next = lo + warp * kAttStep;
+  int j_next = 0, to_copy = 0;
+  auto issue_ahead = [&](int i_slot) {
+    issue(ahead.seq, ahead.head, ahead.v.len, (ahead.st.first + ahead.at) * kAttStep, i_slot);
+    if (--to_copy > 0) ahead.move(a, 1);
+  };
+  if constexpr (kSolo) {
+    to_copy = share.todo;
 #pragma unroll 1
-  for (int i = 0; i < kAttSlots; ++i, j_next += kAttWarps * kAttStep) {
-    if (j_next < hi) issue(j_next, i);
-    cp_async_commit();
+    for (int i = 0; i < kAttSlots; ++i) {
+      if (to_copy > 0) issue_ahead(i);
+      cp_async_commit();
+    }
+  } else {
+    j_next = lo + warp * kAttStep;
+#pragma unroll 1
+    for (int i = 0; i < kAttSlots; ++i, j_next += kAttWarps * kAttStep) {
+      if (j_next < hi) issue(s, h, hi, j_next, i);
+      cp_async_commit();
+    }
   }
 
   // ---- the queries of column g of each tile as f16 B fragments, times 2^-e
   uint32_t qf[kNT][4 * KW][2];
   float cmul[kNT][2];   // columns 2t, 2t+1: what turns a product into the exponent of 2
   int pos[kNT][2];      // their positions
+  auto load_queries = [&] {
 #pragma unroll
-  for (int n = 0; n < kNT; ++n) {
-    const int r = n * 8 + g;
-    uint4 v[2 * KW];
-    uint32_t mag = 0;
+    for (int n = 0; n < kNT; ++n) {
+      const int r = n * 8 + g;
+      uint4 v[2 * KW];
+      uint32_t mag = 0;
 #pragma unroll
-    for (int i = 0; i < 2 * KW; ++i) {
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) {
-        const __nv_bfloat16* q = a.q + static_cast<int64_t>(sv.q0 + r / G) * a.q_stride +
-                                 (h * G + r % G) * kD + (i >> 1) * 64 + t * 16;
-        v[i] = input(a, reinterpret_cast<const uint4*>(q) + (i & 1));
+      for (int i = 0; i < 2 * KW; ++i) {
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const __nv_bfloat16* q = a.q + static_cast<int64_t>(sv.q0 + r / G) * a.q_stride +
+                                   (h * G + r % G) * kD + (i >> 1) * 64 + t * 16;
+          v[i] = input(a, reinterpret_cast<const uint4*>(q) + (i & 1));
+        }
+        mag = max(mag, bf16x8_mag(v[i]));
       }
-      mag = max(mag, bf16x8_mag(v[i]));
-    }
-    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    const int e = row_exp(mag);
-    const float sc = exp2i(-e);
+      mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+      mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+      const int e = row_exp(mag);
+      const float sc = exp2i(-e);
 #pragma unroll
-    for (int i = 0; i < 2 * KW; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      for (int i = 0; i < 2 * KW; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        qf[n][2 * i + (j >> 1)][j & 1] = pack_f16x2(bf16_lo_f32(w[j]) * sc, bf16_hi_f32(w[j]) * sc);
-    }
-    const float m = a.scale_log2 * exp2i(e);
+        for (int j = 0; j < 4; ++j)
+          qf[n][2 * i + (j >> 1)][j & 1] = pack_f16x2(bf16_lo_f32(w[j]) * sc, bf16_hi_f32(w[j]) * sc);
+      }
+      const float m = a.scale_log2 * exp2i(e);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      cmul[n][i] = __shfl_sync(0xffffffffu, m, (2 * t + i) * 4);
-      pos[n][i] = sv.len - sv.n + (n * 8 + 2 * t + i) / G;
+      for (int i = 0; i < 2; ++i) {
+        cmul[n][i] = __shfl_sync(0xffffffffu, m, (2 * t + i) * 4);
+        pos[n][i] = sv.len - sv.n + (n * 8 + 2 * t + i) / G;
+      }
     }
-  }
+  };
 
   float o[kNT][NJ][4];
   // ref: the reference in use, or 0 before any score; limit: how much of a score above it moves it
   float ref[kNT][2], limit[kNT][2], sum[kNT][2];
-  float v_ref = 1.17549435e-38f, v_inv = 8.50705917e37f;  // largest V scale met, and its inverse
+  float v_ref, v_inv;  // largest V scale met, and its inverse
+  auto reset = [&] {
+    v_ref = 1.17549435e-38f, v_inv = 8.50705917e37f;
 #pragma unroll
-  for (int n = 0; n < kNT; ++n) {
-    ref[n][0] = ref[n][1] = 0.f;
-    limit[n][0] = limit[n][1] = -INFINITY;
-    sum[n][0] = sum[n][1] = 0.f;
+    for (int n = 0; n < kNT; ++n) {
+      ref[n][0] = ref[n][1] = 0.f;
+      limit[n][0] = limit[n][1] = -INFINITY;
+      sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
-  }
+        for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
+    }
+  };
   const int tok_g = tile_token<kD>(g);
   // addresses of this lane's K rows and V rows in a slot, 16 tokens apart for the second tile
   int k_at[KW], v_at[2];
@@ -420,53 +543,31 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       }
     }
   };
-  int i_slot = 0;
-#pragma unroll 1
-  for (int j0 = lo + warp * kAttStep; j0 < hi; j0 += kAttWarps * kAttStep, j_next += kAttWarps * kAttStep) {
-    cp_async_wait<kAttSlots - 1>();
-    __syncwarp();
-    step(j0, i_slot);
-    __syncwarp();  // every lane has read the slot
-    if (j_next < hi) issue(j_next, i_slot);
-    cp_async_commit();
-    i_slot = i_slot + 1 == kAttSlots ? 0 : i_slot + 1;
-  }
 
-  // ---- join the warps: every column to the largest reference, then the sums in the warps' order
+  // ---- pieces that are joined through the workspace: by teams, a block or (kSolo) a warp
+  constexpr int TEAM = kSolo ? 32 : kAttWarps * 32;
+  constexpr int64_t PART = COLS * (kD + 2);  // floats of a slot: rows, then (reference, sum) per column
   __shared__ float s_ref[kAttWarps][COLS], s_sum[kAttWarps][COLS];
-#pragma unroll
-  for (int n = 0; n < kNT; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float v = sum[n][c];  // over the tokens of the eight quads
-      v += __shfl_xor_sync(0xffffffffu, v, 4);
-      v += __shfl_xor_sync(0xffffffffu, v, 8);
-      v += __shfl_xor_sync(0xffffffffu, v, 16);
-      if (g == 0) {
-        // (a column that has seen nothing but nan keeps its sum: nan)
-        s_ref[warp][n * 8 + 2 * t + c] = limit[n][c] == kLag ? ref[n][c] : -INFINITY;
-        s_sum[warp][n * 8 + 2 * t + c] = v;
-      }
-    }
-  cp_async_wait<0>();
-  __syncthreads();  // (and every warp is done with its slots)
-  float* s_o = reinterpret_cast<float*>(att_smem);  // [kAttWarps][COLS][kD + 4]
-  constexpr int OS = kD + 4;
-#pragma unroll
-  for (int n = 0; n < kNT; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = n * 8 + 2 * t + c;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
-      const float f = (top == -INFINITY ? 1.f : exp2_approx(s_ref[warp][col] - top)) * v_ref;
-      float* dst = s_o + (warp * COLS + col) * OS + g * (4 * VW);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[n][j][c] * f, o[n][j][2 + c] * f);
-    }
-  __syncthreads();
+  const int tid = kSolo ? lane : threadIdx.x, mine = kSolo ? warp : 0;
+  auto sync = [&] {
+    if constexpr (kSolo) __syncwarp();
+    else __syncthreads();
+  };
+  int share0 = 0;
+  // The slot of a pair's piece. (kSolo) A warp has one pair at most that began in an earlier share, and
+  // one at most that begins in its own and goes on in the next: two slots.
+  auto slot_of = [&](int i) -> int64_t {
+    if constexpr (kSolo) return 2 * (share0 + i) + (i == 0);
+    else return pc.slot0 + i;
+  };
+  // a column's sum over the tokens of the eight quads
+  auto column_sum = [&](int n, int c) {
+    float v = sum[n][c];
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    return v;
+  };
   auto write = [&](int r, int e, const float (&y)[4], float l) {
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const __nv_bfloat162 b0 = __floats2bfloat162_rn(y[0] * inv, y[1] * inv);
@@ -474,54 +575,30 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     uint2 w;
     w.x = *reinterpret_cast<const uint32_t*>(&b0);
     w.y = *reinterpret_cast<const uint32_t*>(&b1);
-    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(sv.q0 + r / G) * a.out_stride + (h * G + r % G) * kD + e) = w;
+    __nv_bfloat16* row = a.out + static_cast<int64_t>(sv.q0 + r / G) * a.out_stride + (h * G + r % G) * kD;
+    *reinterpret_cast<uint2*>(row + e) = w;
   };
-  // four elements of one column per thread
-  constexpr int64_t PART = COLS * (kD + 2);  // floats of a slot: rows, then (reference, sum) per column
-  float* part = a.part + (pc.slot0 + pc.index) * PART;
-  for (int i = threadIdx.x; i < rows * kD / 4; i += kAttWarps * 32) {
-    const int col = i / (kD / 4), e = i % (kD / 4) * 4;
-    float top = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
-#pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      l = fmaf(s_sum[w][col], top == -INFINITY ? 1.f : exp2_approx(s_ref[w][col] - top), l);
-      const float4 v = *reinterpret_cast<const float4*>(s_o + (w * COLS + col) * OS + e);
-      y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
-    }
-    if (pc.of == 1) {
-      write(col, e, y, l);
-    } else {
-      *reinterpret_cast<float4*>(part + col * kD + e) = make_float4(y[0], y[1], y[2], y[3]);
-      if (e == 0) *reinterpret_cast<float2*>(part + COLS * kD + 2 * col) = make_float2(top, l);
-    }
-  }
-  if (pc.of == 1) return;
-
   // ---- pieces meet in groups, then the groups
-  __shared__ int s_last;
+  __shared__ int s_last[kAttWarps];
   // true in the last of n blocks to arrive at a counter, with what the others wrote visible
   auto arrive_last = [&](uint32_t* counter, int n) {
-    __syncthreads();
-    if (threadIdx.x == 0) {  // wraps to zero at the last arrival: ready for the next call
+    sync();
+    if (tid == 0) {  // wraps to zero at the last arrival: ready for the next call
       uint32_t old;
       asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(n - 1) : "memory");
-      s_last = old == static_cast<uint32_t>(n - 1);
+      s_last[mine] = old == static_cast<uint32_t>(n - 1);
     }
-    __syncthreads();
-    return s_last != 0;
+    sync();
+    return s_last[mine] != 0;
   };
-  // joins n slots, `step` apart from slot `from` on, into that slot, or into the output: each thread its
-  // elements, eight slots in flight
+  // joins the slots of n pieces, `step` apart from piece `from` on, into the first of them, or into the
+  // output: each thread its elements, eight slots in flight
   auto join = [&](int from, int n, int step, bool final) {
-    float* base = a.part + from * PART;
-    const int64_t stride = step * PART;
+    float* base = a.part + slot_of(from) * PART;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < rows * kD / 4; i += kAttWarps * 32) {
+    for (int i = tid; i < rows * kD / 4; i += TEAM) {
       const int col = i / (kD / 4), e = i % (kD / 4) * 4;
-      const float* src = base + col * kD + e;
-      const float* stat = base + COLS * kD + 2 * col;
+      const int src = col * kD + e, stat = COLS * kD + 2 * col;
       float top = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
       for (int k0 = 0; k0 < n; k0 += 8) {
@@ -530,8 +607,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const bool in = k0 + k < n;
-          ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(stat + (k0 + k) * stride)) : make_float2(-INFINITY, 0.f);
-          v[k] = in ? __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float* at = a.part + slot_of(from + (k0 + k) * step) * PART;
+          ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(at + stat)) : make_float2(-INFINITY, 0.f);
+          v[k] = in ? __ldcg(reinterpret_cast<const float4*>(at + src)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float now = top;
 #pragma unroll
@@ -556,33 +634,160 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       } else {  // (this thread alone reads these elements of the slot; its statistics are read by others)
         *reinterpret_cast<float4*>(base + col * kD + e) = make_float4(y[0], y[1], y[2], y[3]);
         if (e == 0) {
-          s_ref[0][col] = top;
-          s_sum[0][col] = l;
+          s_ref[mine][col] = top;
+          s_sum[mine][col] = l;
         }
       }
     }
     if (!final) {
-      __syncthreads();  // all have read the statistics
-      if (threadIdx.x < rows)
-        *reinterpret_cast<float2*>(base + COLS * kD + 2 * threadIdx.x) = make_float2(s_ref[0][threadIdx.x], s_sum[0][threadIdx.x]);
+      sync();  // all have read the statistics
+      if (tid < rows)
+        *reinterpret_cast<float2*>(base + COLS * kD + 2 * tid) = make_float2(s_ref[mine][tid], s_sum[mine][tid]);
     }
   };
-  int gs = min(8, pc.of);
-  while (gs * gs < pc.of) ++gs;
-  const int groups = (pc.of + gs - 1) / gs, gi = pc.index / gs, g0 = gi * gs, gn = min(gs, pc.of - g0);
-  if (!arrive_last(a.counters + pc.slot0 + g0, gn)) return;
-  if (groups == 1) {
-    join(pc.slot0, pc.of, 1, true);
+  // what a team does after it has left a piece in its slot
+  auto meet = [&](int index, int of) {
+    int gs = min(8, of);
+    while (gs * gs < of) ++gs;
+    const int groups = (of + gs - 1) / gs, gi = index / gs, g0 = gi * gs, gn = min(gs, of - g0);
+    if (!arrive_last(a.counters + slot_of(g0), gn)) return;
+    if (groups == 1) {
+      join(0, of, 1, true);
+      return;
+    }
+    join(g0, gn, 1, false);
+    // (the second counter of piece 0's slot counts the groups)
+    if (arrive_last(a.counters + a.n_slots + slot_of(0), groups)) join(0, groups, gs, true);
+  };
+
+  if constexpr (kSolo) {
+    int i_slot = 0;
+#pragma unroll 1
+    for (int todo = share.todo; todo > 0;) {
+      take(now.seq, now.head, now.v);
+      const int m = min(todo, now.st.n - now.at);
+      hi = sv.len;
+      load_queries();
+      reset();
+      int j0 = (now.st.first + now.at) * kAttStep;
+#pragma unroll 1
+      for (int i = 0; i < m; ++i, j0 += kAttStep) {
+        cp_async_wait<kAttSlots - 1>();
+        __syncwarp();
+        step(j0, i_slot);
+        __syncwarp();  // every lane has read the slot
+        if (to_copy > 0) issue_ahead(i_slot);
+        cp_async_commit();
+        i_slot = i_slot + 1 == kAttSlots ? 0 : i_slot + 1;
+      }
+      // the pieces of this pair: in the shares from that of its first step to that of its last
+      const int done = share.per * (blockIdx.x * kAttWarps + warp) + share.todo - todo - now.at;  // first step
+      const bool whole = m == now.st.n;
+      share0 = whole ? 0 : done / share.per;
+      const int index = whole ? 0 : blockIdx.x * kAttWarps + warp - share0;
+      const int of = whole ? 1 : (done + now.st.n - 1) / share.per - share0 + 1;
+      float* part = a.part + slot_of(index) * PART;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = n * 8 + 2 * t + c;
+          const float l = column_sum(n, c);
+          const float f = whole ? (l == 0.f ? 0.f : 1.0f / l) * v_ref : v_ref;
+          if (col < rows) {
+#pragma unroll
+            for (int j = 0; j < NJ; j += 2) {
+              const int e = g * (4 * VW) + 2 * j;
+              const float y[4] = {o[n][j][c] * f, o[n][j][2 + c] * f, o[n][j + 1][c] * f, o[n][j + 1][2 + c] * f};
+              if (whole) write(col, e, y, 1.f);
+              else *reinterpret_cast<float4*>(part + col * kD + e) = make_float4(y[0], y[1], y[2], y[3]);
+            }
+            if (!whole && g == 0)
+              *reinterpret_cast<float2*>(part + COLS * kD + 2 * col) =
+                  make_float2(limit[n][c] == kLag ? ref[n][c] : -INFINITY, l);
+          }
+        }
+      if (!whole) meet(index, of);
+      todo -= m;
+      if (todo > 0) now.move(a, m);
+    }
+    cp_async_wait<0>();
     return;
+  } else {
+    load_queries();
+    reset();
+    int i_slot = 0;
+#pragma unroll 1
+    for (int j0 = lo + warp * kAttStep; j0 < hi; j0 += kAttWarps * kAttStep, j_next += kAttWarps * kAttStep) {
+      cp_async_wait<kAttSlots - 1>();
+      __syncwarp();
+      step(j0, i_slot);
+      __syncwarp();  // every lane has read the slot
+      if (j_next < hi) issue(s, h, hi, j_next, i_slot);
+      cp_async_commit();
+      i_slot = i_slot + 1 == kAttSlots ? 0 : i_slot + 1;
+    }
+
+    // ---- join the warps: every column to the largest reference, then the sums in the warps' order
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float v = column_sum(n, c);
+        if (g == 0) {
+          // (a column that has seen nothing but nan keeps its sum: nan)
+          s_ref[warp][n * 8 + 2 * t + c] = limit[n][c] == kLag ? ref[n][c] : -INFINITY;
+          s_sum[warp][n * 8 + 2 * t + c] = v;
+        }
+      }
+    cp_async_wait<0>();
+    __syncthreads();  // (and every warp is done with its slots)
+    float* s_o = reinterpret_cast<float*>(att_smem);  // [kAttWarps][COLS][kD + 4]
+    constexpr int OS = kD + 4;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = n * 8 + 2 * t + c;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
+        const float f = (top == -INFINITY ? 1.f : exp2_approx(s_ref[warp][col] - top)) * v_ref;
+        float* dst = s_o + (warp * COLS + col) * OS + g * (4 * VW);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[n][j][c] * f, o[n][j][2 + c] * f);
+      }
+    __syncthreads();
+    // four elements of one column per thread
+    float* part = a.part + slot_of(pc.index) * PART;
+    for (int i = threadIdx.x; i < rows * kD / 4; i += kAttWarps * 32) {
+      const int col = i / (kD / 4), e = i % (kD / 4) * 4;
+      float top = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w) {
+        l = fmaf(s_sum[w][col], top == -INFINITY ? 1.f : exp2_approx(s_ref[w][col] - top), l);
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * COLS + col) * OS + e);
+        y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
+      }
+      if (pc.of == 1) {
+        write(col, e, y, l);
+      } else {
+        *reinterpret_cast<float4*>(part + col * kD + e) = make_float4(y[0], y[1], y[2], y[3]);
+        if (e == 0) *reinterpret_cast<float2*>(part + COLS * kD + 2 * col) = make_float2(top, l);
+      }
+    }
+    if (pc.of > 1) meet(pc.index, pc.of);
   }
-  join(pc.slot0 + g0, gn, 1, false);
-  // (the second counter of piece 0's slot counts the groups)
-  if (arrive_last(a.counters + a.n_slots + pc.slot0, groups)) join(pc.slot0, groups, gs, true);
 }
 
 // Rows of a sequence and K/V head up to which its cache is streamed through this kernel; more go to
 // the tensor-core kernel.
 constexpr int kAttStreamRows = 16;
+// (sequence, K/V head) pairs above which each warp goes its own way: the figures are at the top.
+constexpr int kAttSoloPairs = kAttResident / 2;
 
 AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_heads) {
   AttnPlan p{};
@@ -596,34 +801,42 @@ AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_hea
     p.stream_rows = 0x7FFFFFFF;
   }
   p.nt = std::min<int64_t>(most_rows, kAttStreamRows) <= 8 ? 1 : 2;
-  // An even share of the steps for each resident block, less half a block per (sequence, head), which
-  // rounding the pieces up adds; with many pairs, several waves of smaller pieces, which end evenly.
   const int64_t heads = static_cast<int64_t>(c.n_kv_heads) * b.n_seq;
-  p.pieces = static_cast<int>(heads <= kAttResident / 2 ? kAttResident - heads / 2 : 3 * kAttResident);
-  p.grid = heads + p.pieces;               // sum of ceil(x) <= n + sum of x
-  p.n_slots = 2 * p.pieces;                // where x > 1, ceil(x) <= 2 x
-  const int64_t most_pieces = (b.max_kv + kAttStep * kAttMinSteps - 1) / (kAttStep * kAttMinSteps) + 1;
-  if (most_pieces * heads < p.grid) p.grid = most_pieces * heads;
+  p.solo = heads > kAttSoloPairs;
+  if (p.solo) {
+    p.grid = kAttResident;
+    p.n_slots = 2 * kAttResident * kAttWarps;
+  } else {
+    p.grid = p.n_slots = kAttResident;
+    const int64_t most_pieces = (b.max_kv + kAttStep * kAttMinSteps - 1) / (kAttStep * kAttMinSteps) + 1;
+    if (most_pieces * heads < p.grid) p.grid = most_pieces * heads;
+  }
   p.part_floats = static_cast<size_t>(p.n_slots) * (8 * p.nt) * (c.head_dim + 2);
   return p;
 }
 
-template <int kD, int kNT>
+template <int kD, int kNT, bool kSolo>
 static cudaError_t launch_attention_t(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
   constexpr size_t slots = static_cast<size_t>(kAttWarps) * kAttSlots * 2 * kAttStep * kD;
-  constexpr size_t join = sizeof(float) * kAttWarps * 8 * kNT * (kD + 4);
+  constexpr size_t join = kSolo ? 0 : sizeof(float) * kAttWarps * 8 * kNT * (kD + 4);
   constexpr size_t smem = slots > join ? slots : join;
-  const cudaError_t e = cudaFuncSetAttribute(attention_kernel<kD, kNT>,
+  const cudaError_t e = cudaFuncSetAttribute(attention_kernel<kD, kNT, kSolo>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attention_kernel<kD, kNT>, dim3(static_cast<unsigned>(grid)), dim3(kAttWarps * 32), smem, stream,
-                       true, a);
+  return launch_kernel(attention_kernel<kD, kNT, kSolo>, dim3(static_cast<unsigned>(grid)), dim3(kAttWarps * 32), smem,
+                       stream, true, a);
+}
+
+template <int kD, int kNT>
+static cudaError_t launch_attention_t(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream) {
+  return p.solo ? launch_attention_t<kD, kNT, true>(a, p.grid, stream)
+                : launch_attention_t<kD, kNT, false>(a, p.grid, stream);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream) {
   if (a.c.head_dim == 64)
-    return p.nt == 1 ? launch_attention_t<64, 1>(a, p.grid, stream) : launch_attention_t<64, 2>(a, p.grid, stream);
-  return p.nt == 1 ? launch_attention_t<128, 1>(a, p.grid, stream) : launch_attention_t<128, 2>(a, p.grid, stream);
+    return p.nt == 1 ? launch_attention_t<64, 1>(a, p, stream) : launch_attention_t<64, 2>(a, p, stream);
+  return p.nt == 1 ? launch_attention_t<128, 1>(a, p, stream) : launch_attention_t<128, 2>(a, p, stream);
 }
 
 }  // namespace strata

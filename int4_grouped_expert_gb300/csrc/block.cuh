@@ -64,7 +64,6 @@ struct AttnArgs {
   int rows_below;         // attention_tc.cu those with more
   // attention.cu
   bool beside;            // launched after attention_tc.cu's kernel, to run beside it
-  int pieces;             // blocks that an even share of the steps is meant for
   int n_slots;            // workspace slots
   float* part;            // partial results, a slot per piece of a cut (sequence, K/V head)
   uint32_t* counters;     // two per slot, zero between calls
@@ -73,7 +72,8 @@ struct AttnArgs {
 // How one attention call is laid out: chosen on the host from the limits the caller gives.
 struct AttnPlan {
   int nt;                 // attention.cu: 8-row tiles of query rows per block, 1 or 2
-  int pieces, n_slots;
+  bool solo;              // attention.cu: shares for warps instead of pieces for blocks
+  int n_slots;
   int64_t grid;
   size_t part_floats;
   int stream_rows;        // rows up to which a sequence goes to attention.cu: 0 none, INT_MAX all

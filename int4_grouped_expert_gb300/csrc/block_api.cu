@@ -241,7 +241,6 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.group = n_heads / cache->n_kv_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
-  a.pieces = p.pieces;
   a.n_slots = p.n_slots;
   a.part = reinterpret_cast<float*>(base + L.part);
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);

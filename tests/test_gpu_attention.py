@@ -289,3 +289,62 @@ def test_a_cache_of_more_than_4_gb():
     got = big.k_codes[-1, :, :2].float() * big.k_scales[-1][:, None, None]
     x = k.view(2, Hkv, D).transpose(0, 1).float()
     assert ((got - x).abs() <= x.abs() / 16 + big.k_scales[-1][:, None, None] * 2.0 ** -10).all()
+
+
+def many(n, seed, longest, rows=1):
+    """Lengths of n sequences: some empty, some without queries, a few long ones."""
+    rng = np.random.default_rng(seed)
+    seqs = [(int(L), int(q)) for L, q in zip(rng.integers(1, 260, n), rng.integers(1, rows + 1, n))]
+    for i in range(0, n, 7):
+        seqs[i] = (seqs[i][0], 0) if i % 2 else (0, 1)
+    for i, L in enumerate((longest, longest // 2 + 1, 32, 33, 31)):
+        seqs[(i * 17 + 3) % n] = (L, 1)
+    return seqs
+
+
+@pytest.mark.parametrize("window", [0, 75])
+@pytest.mark.parametrize("n,Hq,Hkv,D,rows", [(60, 16, 4, 128, 1), (60, 64, 4, 128, 1), (300, 2, 1, 64, 1),
+                                             (1100, 1, 1, 64, 1), (58, 32, 8, 64, 4), (77, 6, 3, 128, 3)])
+def test_many_sequences(n, Hq, Hkv, D, rows, window):
+    """More pairs of sequence and head than blocks that run at once: warps go from pair to pair, and
+    the long sequences are cut over many of them."""
+    Case(many(n, 5, 6000, rows), Hq, Hkv, D, 32).gpu().check(window)
+
+
+def test_many_equal_sequences():
+    Case([(96, 1)] * 64, 32, 8, 128, 32).gpu().check()
+    Case([(1, 1)] * 230, 2, 1, 64, 16).gpu().check()
+
+
+@pytest.mark.parametrize("n", [2, 9, 20, 33, 57])
+def test_pairs_that_do_not_fill_the_blocks_evenly(n):
+    Case([(1500, 1)] * n, 8, 4, 64, 64).gpu().check()
+
+
+def test_many_sequences_beside_prompts():
+    Case(many(130, 6, 2000) + [(700, 300), (90, 90)], 8, 2, 128, 64).gpu().check()
+
+
+def test_many_sequences_with_a_kept_workspace_give_the_same_bits():
+    import torch
+    import int4_grouped_expert_gb300 as st
+    c = Case(many(90, 7, 9000), 12, 3, 128, 64).gpu()
+    first = c.run()
+    ws = torch.zeros(st.strata_attention_workspace_size(c.cache.struct(), c.batch, c.Hq), dtype=torch.uint8,
+                     device="cuda")
+    c.run(ws=ws)
+    for _ in range(4):
+        assert (c.run(ws=ws, flags=st.STRATA_WS_REUSE) == first).all()
+
+
+def test_many_sequences_with_pages_that_do_not_exist():
+    """A page number out of range is flagged and its tokens count as unseen, whatever warp meets it."""
+    import int4_grouped_expert_gb300 as st
+    c = Case([(200, 1)] * 120, 4, 2, 64, 32)
+    want, bound = c.reference()
+    c.table[50, 2] = -5
+    c.gpu()
+    got = ref.bf16_bits_to_f64(c.run(expect_status=st.STRATA_DEV_BAD_SLOT)).reshape(c.T, c.Hq, c.D)
+    others = np.arange(c.T) != 50
+    assert (np.abs(got - want) <= bound)[others].all()
+    assert np.isfinite(got[50]).all()
