@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     }
     join(g0, gn, 1, false);
     // (the second counter of piece 0's slot counts the groups)
-    if (arrive_last(a.counters + a.n_slots + slot_of(0), groups)) join(0, groups, gs, true);
+    if (arrive_last(a.counters + kAttMaxSlots + slot_of(0), groups)) join(0, groups, gs, true);
   };
 
   if constexpr (kSolo) {
@@ -803,15 +803,17 @@ AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_hea
   p.nt = std::min<int64_t>(most_rows, kAttStreamRows) <= 8 ? 1 : 2;
   const int64_t heads = static_cast<int64_t>(c.n_kv_heads) * b.n_seq;
   p.solo = heads > kAttSoloPairs;
+  int64_t slots;
+  static_assert(2 * kAttResident * kAttWarps <= kAttMaxSlots, "every slot has counters");
   if (p.solo) {
     p.grid = kAttResident;
-    p.n_slots = 2 * kAttResident * kAttWarps;
+    slots = 2 * kAttResident * kAttWarps;
   } else {
-    p.grid = p.n_slots = kAttResident;
+    p.grid = slots = kAttResident;
     const int64_t most_pieces = (b.max_kv + kAttStep * kAttMinSteps - 1) / (kAttStep * kAttMinSteps) + 1;
     if (most_pieces * heads < p.grid) p.grid = most_pieces * heads;
   }
-  p.part_floats = static_cast<size_t>(p.n_slots) * (8 * p.nt) * (c.head_dim + 2);
+  p.part_floats = static_cast<size_t>(slots) * (8 * p.nt) * (c.head_dim + 2);
   return p;
 }
 

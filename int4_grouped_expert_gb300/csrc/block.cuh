@@ -51,6 +51,10 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int num_sms, cudaStream_t stream);
 
+// Slots of the attention workspace that have counters: the counters lie in the same place for every
+// batch, so that a workspace can go from one to another without being cleared.
+constexpr int kAttMaxSlots = 3648;
+
 struct AttnArgs {
   strata_kv_cache c;
   strata_kv_batch b;
@@ -64,16 +68,14 @@ struct AttnArgs {
   int rows_below;         // attention_tc.cu those with more
   // attention.cu
   bool beside;            // launched after attention_tc.cu's kernel, to run beside it
-  int n_slots;            // workspace slots
   float* part;            // partial results, a slot per piece of a cut (sequence, K/V head)
-  uint32_t* counters;     // two per slot, zero between calls
+  uint32_t* counters;     // [2][kAttMaxSlots], zero between calls
   uint32_t* status;
 };
 // How one attention call is laid out: chosen on the host from the limits the caller gives.
 struct AttnPlan {
   int nt;                 // attention.cu: 8-row tiles of query rows per block, 1 or 2
   bool solo;              // attention.cu: shares for warps instead of pieces for blocks
-  int n_slots;
   int64_t grid;
   size_t part_floats;
   int stream_rows;        // rows up to which a sequence goes to attention.cu: 0 none, INT_MAX all

@@ -97,7 +97,7 @@ struct AttnLayout {
 AttnLayout attn_layout(const AttnPlan& p) {
   AttnLayout L{};
   L.counters = sizeof(WsHeader);
-  L.part = round_up(L.counters + 2 * sizeof(uint32_t) * p.n_slots);
+  L.part = round_up(L.counters + 2 * sizeof(uint32_t) * kAttMaxSlots);
   L.total = round_up(L.part + sizeof(float) * p.part_floats);
   return L;
 }
@@ -228,7 +228,7 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(workspace);
   if (!(flags & STRATA_WS_REUSE) &&
-      cudaMemsetAsync(base, 0, L.counters + 2 * sizeof(uint32_t) * p.n_slots, st) != cudaSuccess)
+      cudaMemsetAsync(base, 0, L.part, st) != cudaSuccess)
     return STRATA_ERR_CUDA;
   AttnArgs a{};
   a.c = *cache;
@@ -241,7 +241,6 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.group = n_heads / cache->n_kv_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
-  a.n_slots = p.n_slots;
   a.part = reinterpret_cast<float*>(base + L.part);
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);
   a.status = &reinterpret_cast<WsHeader*>(base)->status;

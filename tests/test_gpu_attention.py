@@ -348,3 +348,18 @@ def test_many_sequences_with_pages_that_do_not_exist():
     others = np.arange(c.T) != 50
     assert (np.abs(got - want) <= bound)[others].all()
     assert np.isfinite(got[50]).all()
+
+
+def test_a_kept_workspace_serves_batches_of_other_shapes():
+    """What one call leaves in the workspace is clean for the next, whatever its lengths, heads and rows."""
+    import torch
+    import int4_grouped_expert_gb300 as st
+    cases = [Case([(20000, 1)], 8, 2, 128, 64), Case(many(90, 7, 5000), 12, 3, 128, 64),
+             Case([(3000, 1)] * 40, 16, 2, 64, 32), Case([(2000, 300), (900, 1)], 8, 2, 128, 64),
+             Case([(5000, 2)] * 3, 64, 4, 64, 16), Case([(6000, 70)], 8, 1, 128, 64)]
+    cases = [c.gpu() for c in cases]
+    first = [c.run() for c in cases]
+    size = max(st.strata_attention_workspace_size(c.cache.struct(), c.batch, c.Hq) for c in cases)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 4, 5, 1, 0, 3, 2, 5, 4, 1, 5, 0):
+        assert (cases[i].run(ws=ws, flags=st.STRATA_WS_REUSE) == first[i]).all(), i
