@@ -23,6 +23,8 @@
 // Bound by the softmax's instructions and by shared memory (scores of 64 tokens read 6 KB per 32 clocks
 // of MMA). Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every
 // role leaves its loop, MMAs in flight are drained (bounded) and TMEM is freed.
+#include <algorithm>
+
 #include "attention.cuh"
 #include "tc_ts_ptx.cuh"
 
@@ -34,6 +36,16 @@ constexpr int kAtTok = 64;      // tokens per tile
 constexpr int kAtRing = 4;      // stages of two tiles of codes converted to f16
 constexpr int kAtThreads = 640;
 constexpr int kAtBad = 8;       // ring of per-tile masks of tokens in pages that do not exist
+constexpr int kAtSms = 152;     // blocks that run at once
+constexpr int kAtMaxSlots = 3 * kAtSms;
+constexpr int kAtMinTiles = 8;  // tiles that a piece has at least
+// What a block costs beside its tiles, in tiles of 1.17 us: to start and to fill its ring; the same and to
+// leave a piece; for the kernel that joins. With a quarter of the SMs idle a tile takes a sixth less.
+// (32 query heads, 8 K/V heads, us whole and cut: 64 queries on 4096 tokens, 8 units, 77 and 27; 64 on
+// 32768 582 and 60; 512 on 8192, 64 units, 141 and 94; 1280 on 8192, of whose 160 units 8 are cut,
+// 244 and 170. Cutting 104 of 256 units took 276 for 245.)
+constexpr int kAtStart = 4, kAtPiece = 8, kAtJoin = 8;
+constexpr int kAtMostCut = kAtSms * 3 / 4;  // (more units than these are never worth cutting)
 
 template <int kD>
 struct AtCfg {
@@ -75,6 +87,96 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The units of a call: 256 rows of a (sequence, K/V head), sequence by sequence, those with the most tokens
+// to see first. As many as fill all SMs a whole number of times stay whole; the others, which run last, are
+// cut along the tokens where that ends sooner, into pieces of `per` tiles, at most k. The same in every warp.
+struct Units {
+  int whole, rest, k, per;
+  int s0, s1, mine, end;  // this lane's sequences, their units, and the units up to there
+};
+__device__ __forceinline__ int units_of(const AttnArgs& a, const SeqView& v) {
+  const int64_t rows = static_cast<int64_t>(v.n) * a.group;
+  return rows > a.rows_below ? static_cast<int>((rows + 255) / 256) * a.c.n_kv_heads : 0;
+}
+__device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
+  Units u;
+  const int lane = threadIdx.x & 31, per_lane = (a.b.n_seq + 31) / 32;
+  u.s0 = min(a.b.n_seq, lane * per_lane), u.s1 = min(a.b.n_seq, u.s0 + per_lane);
+  u.mine = 0;
+  float tiles = 0.f, most = 0.f;
+  for (int s = u.s0; s < u.s1; ++s) {
+    const SeqView v = seq_view(a, s, flag);
+    const int n = units_of(a, v);
+    // tokens that a unit sees, on average
+    float seen = max(0.f, v.len - 0.5f * v.n);
+    if (a.window > 0) seen = fminf(seen, a.window + 256.f / a.group);
+    u.mine += n;
+    tiles += n * (seen / kAtTok + 1.f);
+    if (n > 0) most = fmaxf(most, seen / kAtTok + 1.f);
+  }
+  u.end = u.mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, u.end, d);
+    if (lane >= d) u.end += x;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+  const int all = __shfl_sync(0xffffffffu, u.end, 31);
+  u.whole = all / kAtSms * kAtSms, u.rest = all - u.whole;
+  u.k = 1;
+  most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+  // (units that stay whole decide when a batch of very different lengths ends)
+  if (u.rest > 0 && (u.whole == 0 || most * all <= 1.25f * tiles)) {
+    // lane i weighs i + 1 pieces of the longest units, and in proportion of the others
+    const int n = static_cast<int>(most), c = lane + 1;
+    const int pieces = max(u.rest, static_cast<int>(u.rest * c * (tiles / all / most)));
+    int cost = (pieces + kAtSms - 1) / kAtSms * (n / c + 1 + (c > 1 ? kAtPiece : kAtStart)) + (c > 1 ? kAtJoin : 0);
+    if (pieces <= kAtMostCut) cost -= cost / 6;
+    if (c > 1 && (n < c * kAtMinTiles || u.rest * c > a.tc_slots)) cost = 0x3FFFFFF;
+    cost = min(cost, 0x3FFFFFF);
+    u.k = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(cost) << 5 | lane) % 32 + 1;
+  }
+  u.per = max(kAtMinTiles, static_cast<int>(most) / u.k + 1);
+  return u;
+}
+// One unit, and the tiles that its rows see.
+struct Unit {
+  int seq, head, row0, rows;  // first row; rows of the (sequence, head)
+  SeqView sv;
+  int tok_hi, j_lo, n_tiles, of;
+};
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int seq, int head, int row0, int k, int per, bool flag) {
+  Unit u;
+  u.seq = seq, u.head = head, u.row0 = row0;
+  u.sv = seq_view(a, seq, flag);
+  u.rows = u.sv.n * a.group;
+  const int p0 = u.sv.len - u.sv.n;  // position of the first query
+  u.tok_hi = min(u.sv.len, p0 + (min(row0 + 256, u.rows) - 1) / a.group + 1);
+  const int tok_lo = a.window > 0 ? max(0, p0 + row0 / a.group - a.window + 1) : 0;
+  u.j_lo = tok_lo / kAtTok;
+  u.n_tiles = u.tok_hi > tok_lo ? (u.tok_hi + kAtTok - 1) / kAtTok - u.j_lo : 0;
+  u.of = min(k, max(1, (u.n_tiles + per - 1) / per));
+  return u;
+}
+__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Units& us, int at) {
+  const int heads = a.c.n_kv_heads;
+  const int owner = __ffs(__ballot_sync(0xffffffffu, at < us.end)) - 1;
+  int seq = 0, left = at - (us.end - us.mine), n = 0;
+  if ((threadIdx.x & 31) == owner) {
+    for (seq = us.s0; seq < us.s1; ++seq) {
+      n = units_of(a, seq_view(a, seq, false));
+      if (left < n) break;
+      left -= n;
+    }
+  }
+  seq = __shfl_sync(0xffffffffu, seq, owner);
+  left = __shfl_sync(0xffffffffu, left, owner);
+  n = __shfl_sync(0xffffffffu, n, owner);
+  return unit_of(a, seq, left % heads, (n / heads - 1 - left / heads) * 256, at < us.whole ? 1 : us.k, us.per,
+                 false);
+}
+
 template <int kD>
 __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a) {
   using C = AtCfg<kD>;
@@ -94,24 +196,40 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bad + kAtBad);
   __shared__ int abort_flag_s;
   __shared__ float s_ref[2][8];
+  __shared__ volatile int s_end[6];  // what is wanted again at the end only: not kept in registers
   volatile int* abort_flag = &abort_flag_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   griddep_wait();
   griddep_launch();
-  const int h = blockIdx.y, s = blockIdx.z;
-  const SeqView sv = seq_view(a, s, threadIdx.x == 0 && blockIdx.x == 0 && h == 0);
-  const int G = a.group, rows = sv.n * G;
-  // the blocks with the most tokens to see start first
-  const int rb = gridDim.x - 1 - blockIdx.x;
-  const int row0 = rb * 256;
-  if (rows <= a.rows_below || row0 >= rows) return;
+  const int id = blockIdx.x;
+  int cut = 0, piece = 0;  // slot of the block's piece, its number among its unit's
+  Unit u;
+  if (a.tc_search) {
+    const Units us = find_units(a, id == 0 && threadIdx.x < 32);
+    cut = max(0, id - us.whole);
+    const int at = cut > 0 ? us.whole + cut / us.k : id;
+    if (at >= us.whole + us.rest) return;
+    u = find_unit(a, us, at);
+    piece = cut - max(0, at - us.whole) * us.k;
+  } else {  // the same order, as if every sequence had max_q rows
+    const int heads = a.c.n_kv_heads, of_seq = gridDim.x / a.b.n_seq, left = id % of_seq;
+    u = unit_of(a, id / of_seq, left % heads, (of_seq / heads - 1 - left / heads) * 256, 1, 1,
+                left == 0 && threadIdx.x == 0);
+    if (u.rows <= a.rows_below || u.row0 >= u.rows) return;
+  }
+  const int h = u.head, s = u.seq, row0 = u.row0, rows = u.rows, of = u.of;
+  const SeqView sv = u.sv;
+  const int G = a.group;
+  int j_lo = u.j_lo, n_tiles = u.n_tiles, tok_hi = u.tok_hi;
+  if (piece >= of) return;
+  if (of > 1) {
+    const int from = n_tiles * piece / of, to = n_tiles * (piece + 1) / of;
+    j_lo += from;
+    n_tiles = to - from;
+    tok_hi = min(tok_hi, (j_lo + n_tiles) * kAtTok);
+  }
   const int last_row = min(row0 + 256, rows) - 1;
-  const int p_lo = sv.len - sv.n + row0 / G, p_hi = sv.len - sv.n + last_row / G;
-  const int tok_hi = min(sv.len, p_hi + 1);
-  const int tok_lo = a.window > 0 ? max(0, p_lo - a.window + 1) : 0;
-  const int j_lo = tok_lo / kAtTok;
-  const int n_tiles = tok_hi > tok_lo ? (tok_hi + kAtTok - 1) / kAtTok - j_lo : 0;
   const int n_rt = last_row - row0 >= 128 ? 2 : 1;        // row tiles in use
   const int P = a.c.page_size;
   const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
@@ -144,6 +262,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     }
     tc::fence_barrier_init();
     abort_flag_s = 0;
+    s_end[0] = of > 1;
+    s_end[1] = cut;  // (a unit's pieces have k slots, from its first block's number on)
+    s_end[2] = sv.q0;
+    s_end[3] = rows;
+    s_end[4] = row0;
+    s_end[5] = h;
   }
   if (warp == 2) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -206,7 +330,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   if (v_ref == 0.f) v_ref = 1.f;
 
   // registers: 5 warpgroups are launched with 96 a thread (61440 in all) and go on with
-  // 48 + 2 * 136 + 2 * 80 (the same)
+  // 48 + 2 * 120 + 2 * 96 (the same)
   // stage 0 holds K_0 and K_1, stage j + 1 V_j and K_(j+2): what the product of step j and the scores after
   // it read
   // O_i += P_i(j) V_j is done. Barriers of step j are per buffer (j & 1): whoever waits for one knows that
@@ -278,7 +402,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     }
     __syncwarp();
   } else if (warp < 12) {
-    tc::reg_inc<136>();
+    tc::reg_inc<120>();
     if (tile < n_rt) {
     // ------------------------------------------------------------------ softmax
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -294,7 +418,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       tc::tc_fence_after();
       const int j0 = (j_lo + j) * kAtTok;
       // columns lo .. hi of the tile are seen
-      const int hi = min(pos, sv.len - 1) - j0, lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
+      const int hi = min(pos, tok_hi - 1) - j0, lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
       const unsigned long long gone = bad[j % kAtBad];
       const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && lo <= 0) && gone == 0;
       uint32_t r[2][32];
@@ -345,7 +469,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          float2 e = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(r[q][2 * i]), __uint_as_float(r[q][2 * i + 1])), cc, mm));
+          const uint64_t x = pack_f32x2(__uint_as_float(r[q][2 * i]), __uint_as_float(r[q][2 * i + 1]));
+          float2 e = unpack_f32x2(fma_f32x2(x, cc, mm));
           e.x = exp2_approx(e.x);
           e.y = exp2_approx(e.y);
           if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(e.x, e.y));
@@ -365,9 +490,27 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       ok = done(tile, n_tiles - 1);
       tc::tc_fence_after();
     }
-    if (ok) {
+    const int q0 = s_end[2], rows = s_end[3], h = s_end[5];
+    const int row = s_end[4] + tile * 128 + (warp & 3) * 32 + lane;
+    if (ok && s_end[0]) {
+      // this piece: fp32 rows in the order [four elements][row], then (reference, sum)
+      float* slot = a.tc_part + static_cast<int64_t>(s_end[1]) * (256 * (kD + 2));
+      const int r0 = row - s_end[4];
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 16) {
+        uint32_t x[16];
+        tc::tmem_ld16(to + c, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(slot + (c / 4 + i) * 1024 + r0 * 4) =
+              make_float4(__uint_as_float(x[4 * i]) * v_ref, __uint_as_float(x[4 * i + 1]) * v_ref,
+                          __uint_as_float(x[4 * i + 2]) * v_ref, __uint_as_float(x[4 * i + 3]) * v_ref);
+      }
+      *reinterpret_cast<float2*>(slot + 256 * kD + 2 * r0) = make_float2(m, l);
+    } else if (ok) {
       const float inv = l == 0.f ? 0.f : v_ref / l;
-      uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(sv.q0 + row / G) * a.out_stride +
+      uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(q0 + row / G) * a.out_stride +
                                             (h * G + row % G) * kD);
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
@@ -389,7 +532,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     }
     }
   } else {
-    tc::reg_dec<80>();
+    tc::reg_dec<96>();
     // ------------------------------------------------------------------ codes -> f16 tiles
     const int w = warp - 12;
     // K: this warp's 8 tokens of the tile (one page); a lane takes 16 bytes of row lane % 8 per 64-wide piece
@@ -419,7 +562,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       const uint8_t* src = a.c.k_codes + ((ph << pshift) + (tok & (P - 1)) + (lane & 7)) * kD + (lane >> 3) * 16;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
-        x[c] = on && tok + (lane & 7) < tok_hi ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+        x[c] = on && tok + (lane & 7) < tok_hi ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64))
+                                               : make_uint4(0u, 0u, 0u, 0u);
       k_page = page_of(tok + kAtTok);
     };
     auto load_v = [&](int j, uint32_t (&x)[8], float& scale) {
@@ -465,7 +609,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int d = (w >> 1) * 32 + dg * 4 + k;
-        *reinterpret_cast<uint4*>(dst + d * 128 + ((ch ^ (d & 7)) << 4)) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+        *reinterpret_cast<uint4*>(dst + d * 128 + ((ch ^ (d & 7)) << 4)) =
+            make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
       }
     };
     bool ok = true;
@@ -519,19 +664,103 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   }
 }
 
+// Joins the pieces of the units that were cut: a block takes 16 rows of a unit at a time, so that all SMs read
+// (one SM reads 65 GB/s from L2: the last piece's block took 16 us to join four).
+constexpr int kAtJoinRows = 16;
 template <int kD>
-cudaError_t launch_tc_t(const AttnArgs& a, int blocks, cudaStream_t stream) {
+__global__ void __launch_bounds__(kAtJoinRows * kD / 8) attention_tc_join_kernel(AttnArgs a) {
+  griddep_wait();
+  griddep_launch();
+  const Units us = find_units(a, false);
+  if (us.k == 1) return;
+  constexpr int SLICES = 256 / kAtJoinRows;
+  const int r16 = threadIdx.x % kAtJoinRows, c = threadIdx.x / kAtJoinRows * 2;  // a thread: eight elements of a row
+  for (int i = blockIdx.x; i < us.rest * SLICES; i += gridDim.x) {
+    const Unit u = find_unit(a, us, us.whole + i / SLICES);
+    const int r = i % SLICES * kAtJoinRows + r16, row = u.row0 + r;
+    if (u.of == 1 || row >= u.rows) continue;
+    constexpr int64_t PART = 256 * (kD + 2);
+    const float* first = a.tc_part + static_cast<int64_t>(i / SLICES) * us.k * PART;
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < u.of; ++k)
+      top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(first + k * PART + 256 * kD) + r).x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < u.of; ++k) {
+      const float* slot = first + k * PART;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot + 256 * kD) + r);
+      const float4 v0 = __ldcg(reinterpret_cast<const float4*>(slot) + c * 256 + r);
+      const float4 v1 = __ldcg(reinterpret_cast<const float4*>(slot) + (c + 1) * 256 + r);
+      const float w = exp2_approx(ml.x - ref);
+      sum = fmaf(ml.y, w, sum);
+      y[0] = fmaf(v0.x, w, y[0]); y[1] = fmaf(v0.y, w, y[1]); y[2] = fmaf(v0.z, w, y[2]); y[3] = fmaf(v0.w, w, y[3]);
+      y[4] = fmaf(v1.x, w, y[4]); y[5] = fmaf(v1.y, w, y[5]); y[6] = fmaf(v1.z, w, y[6]); y[7] = fmaf(v1.w, w, y[7]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * k] * inv, y[2 * k + 1] * inv);
+      o[k] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    __nv_bfloat16* dst = a.out + static_cast<int64_t>(u.sv.q0 + row / a.group) * a.out_stride +
+                         (u.head * a.group + row % a.group) * kD;
+    reinterpret_cast<uint4*>(dst)[c / 2] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+template <int kD>
+cudaError_t launch_join_t(const AttnArgs& a, cudaStream_t stream) {
+  return launch_kernel(attention_tc_join_kernel<kD>, dim3(std::min(a.tc_slots, 152) * 4), dim3(kAtJoinRows * kD / 8), 0,
+                       stream, true, a);
+}
+
+template <int kD>
+cudaError_t launch_tc_t(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(AtCfg<kD>::SMEM));
   if (e != cudaSuccess) return e;
-  return launch_kernel(attention_tc_kernel<kD>, dim3(blocks, a.c.n_kv_heads, a.b.n_seq), dim3(kAtThreads),
+  return launch_kernel(attention_tc_kernel<kD>, dim3(static_cast<unsigned>(grid)), dim3(kAtThreads),
                        AtCfg<kD>::SMEM, stream, true, a);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_tc(const AttnArgs& a, int blocks, cudaStream_t stream) {
-  return a.c.head_dim == 64 ? launch_tc_t<64>(a, blocks, stream) : launch_tc_t<128>(a, blocks, stream);
+// Units if every sequence had max_q rows, and a bound from the rows of all.
+static int64_t full_units(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group) {
+  return (b.max_q * group + 255) / 256 * b.n_seq * c.n_kv_heads;
+}
+static int64_t most_units(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group) {
+  return std::min(full_units(c, b, group), (b.T * group / 256 + b.n_seq) * c.n_kv_heads);
+}
+// Pieces that may come to lie in the workspace; 0: no unit is cut. Above one and a half times the SMs the
+// last units fill their gaps by themselves (512 units of 33 tiles: 165 us whole, 178 with 56 cut). Batches
+// that are not cut do without the kernel that joins: 3 us.
+int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int window) {
+  const int64_t units = most_units(c, b, group);
+  if (units > kAtSms * 3 / 2) return 0;
+  // (of sequences of equal length the units are known)
+  const int64_t rest = units % kAtSms;
+  if (b.T == static_cast<int64_t>(b.n_seq) * b.max_q && (rest == 0 || rest > kAtMostCut)) return 0;
+  const int64_t seen = window > 0 ? std::min<int64_t>(b.max_kv, window + 256 / group) : b.max_kv;
+  const int64_t cut = std::min<int64_t>(seen / kAtTok / kAtMinTiles, 32);  // (two short pieces do not pay: 28 us, 31)
+  return cut > 2 ? static_cast<int>(std::min<int64_t>(kAtMaxSlots, std::min<int64_t>(units, kAtSms - 1) * cut)) : 0;
+}
+size_t attn_tc_part_floats(const strata_kv_cache& c, int slots) {
+  return static_cast<size_t>(slots) * 256 * (c.head_dim + 2);
+}
+cudaError_t launch_attention_tc_join(const AttnArgs& a, cudaStream_t stream) {
+  return a.c.head_dim == 64 ? launch_join_t<64>(a, stream) : launch_join_t<128>(a, stream);
+}
+cudaError_t launch_attention_tc(AttnArgs a, cudaStream_t stream) {
+  // Blocks find their units in the lengths where units are cut, or where blocks by max_q would mostly be
+  // empty; the search is 1 us a block.
+  const int64_t full = full_units(a.c, a.b, a.group), most = most_units(a.c, a.b, a.group);
+  a.tc_search = a.tc_slots > 0 || full > 2 * most;
+  const int64_t grid = a.tc_search ? most + a.tc_slots : full;
+  return a.c.head_dim == 64 ? launch_tc_t<64>(a, grid, stream) : launch_tc_t<128>(a, grid, stream);
 }
 
 }  // namespace strata

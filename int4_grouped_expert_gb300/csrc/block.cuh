@@ -70,6 +70,10 @@ struct AttnArgs {
   bool beside;            // launched after attention_tc.cu's kernel, to run beside it
   float* part;            // partial results, a slot per piece of a cut (sequence, K/V head)
   uint32_t* counters;     // [2][kAttMaxSlots], zero between calls
+  // attention_tc.cu
+  bool tc_search;         // blocks find their units in the lengths
+  int tc_slots;           // pieces that may be left in the workspace; 0: nothing is cut
+  float* tc_part;
   uint32_t* status;
 };
 // How one attention call is laid out: chosen on the host from the limits the caller gives.
@@ -77,12 +81,15 @@ struct AttnPlan {
   int nt;                 // attention.cu: 8-row tiles of query rows per block, 1 or 2
   bool solo;              // attention.cu: shares for warps instead of pieces for blocks
   int64_t grid;
-  size_t part_floats;
+  size_t part_floats, tc_part_floats;
   int stream_rows;        // rows up to which a sequence goes to attention.cu: 0 none, INT_MAX all
-  int tc_blocks;          // 256-row blocks of attention_tc.cu per (sequence, K/V head); 0: not launched
+  bool tc;                // attention_tc.cu is launched
 };
 AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_heads);
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
-cudaError_t launch_attention_tc(const AttnArgs& a, int blocks, cudaStream_t stream);
+int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int window);
+size_t attn_tc_part_floats(const strata_kv_cache& c, int slots);
+cudaError_t launch_attention_tc(AttnArgs a, cudaStream_t stream);
+cudaError_t launch_attention_tc_join(const AttnArgs& a, cudaStream_t stream);  // after both others
 
 }  // namespace strata

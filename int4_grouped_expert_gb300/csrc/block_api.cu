@@ -92,13 +92,14 @@ strata_status check_batch(const strata_kv_cache* c, const strata_kv_batch* b, in
 }
 
 struct AttnLayout {
-  size_t counters, part, total;
+  size_t counters, part, tc_part, total;
 };
 AttnLayout attn_layout(const AttnPlan& p) {
   AttnLayout L{};
   L.counters = sizeof(WsHeader);
   L.part = round_up(L.counters + 2 * sizeof(uint32_t) * kAttMaxSlots);
-  L.total = round_up(L.part + sizeof(float) * p.part_floats);
+  L.tc_part = round_up(L.part + sizeof(float) * p.part_floats);
+  L.total = round_up(L.tc_part + sizeof(float) * p.tc_part_floats);
   return L;
 }
 
@@ -243,14 +244,17 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.window = window;
   a.part = reinterpret_cast<float*>(base + L.part);
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);
+  a.tc_slots = p.tc ? attn_tc_slots(*cache, *batch, a.group, window) : 0;
+  a.tc_part = reinterpret_cast<float*>(base + L.tc_part);
   a.status = &reinterpret_cast<WsHeader*>(base)->status;
   a.rows_above = a.rows_below = p.stream_rows;
-  if (p.tc_blocks > 0) {
-    const cudaError_t e = launch_attention_tc(a, p.tc_blocks, st);
+  if (p.tc) {
+    const cudaError_t e = launch_attention_tc(a, st);
     if (e != cudaSuccess) return STRATA_ERR_CUDA;
   }
-  a.beside = p.tc_blocks > 0;
-  return p.stream_rows > 0 ? of(launch_attention(a, p, st)) : STRATA_OK;
+  a.beside = p.tc;
+  if (p.stream_rows > 0 && launch_attention(a, p, st) != cudaSuccess) return STRATA_ERR_CUDA;
+  return a.tc_slots > 0 ? of(launch_attention_tc_join(a, st)) : STRATA_OK;
 }
 
 }  // extern "C"

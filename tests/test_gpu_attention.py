@@ -363,3 +363,31 @@ def test_a_kept_workspace_serves_batches_of_other_shapes():
     ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     for i in (0, 1, 2, 3, 4, 5, 1, 0, 3, 2, 5, 4, 1, 5, 0):
         assert (cases[i].run(ws=ws, flags=st.STRATA_WS_REUSE) == first[i]).all(), i
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,window", [
+    ([(4100, 64)], 32, 4, 128, 0),                       # few units: pieces of each
+    ([(4100, 64)], 32, 4, 128, 2000),
+    ([(2600, 300)], 8, 8, 64, 0),
+    ([(1030, 17), (6000, 33), (40, 40)], 8, 2, 128, 0),  # units too short for as many pieces as others
+    ([(1030, 17), (6000, 33), (40, 40)], 8, 2, 128, 1800),
+    ([(3000, 300), (9, 9), (2222, 1)], 28, 4, 64, 0),
+    ([(1560, 620)], 64, 32, 64, 0),                      # 160 units: the last ones are cut
+    ([(1600, 450)], 64, 2, 64, 0),
+])
+def test_units_cut_along_the_tokens(seqs, Hq, Hkv, D, window):
+    Case(seqs, Hq, Hkv, D, 64).gpu().check(window)
+
+
+def test_one_long_prompt_among_many_single_rows():
+    """Blocks by the longest sequence would mostly be empty: they find their units in the lengths."""
+    Case([(500, 400)] + [(300, 1)] * 40, 8, 2, 64, 32).gpu().check()
+
+
+def test_nan_in_one_piece_of_a_cut_unit():
+    c = Case([(4100, 40)], 16, 2, 128, 64)
+    c.codes["v"][c.table[0, 20], 1, 5, :] = 0x7F
+    c.codes["k"][c.table[0, 40], 0, 7, :] = 0x7F
+    c.gpu()
+    got = ref.bf16_bits_to_f64(c.run()).reshape(c.T, 16, 128)
+    assert np.isnan(got).all()          # every row sees both tokens: a head's K, the other's V
