@@ -171,18 +171,28 @@ __global__ void __launch_bounds__(kLinWarps * 32, kBlocks) linear_stream_kernel(
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[warp][16 * m + g + 8 * (i >> 1)][n * 8 + 2 * t + (i & 1)] = acc[m][n][i];
+  // what is added comes first, all of it at once: loads between the stores to out (which may be the
+  // residual) would wait for one another
+  constexpr int THREADS = kLinWarps * 32, ITEMS = (ROWS * COLS + THREADS - 1) / THREADS;
+  float plus[ITEMS];
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const int i = threadIdx.x + u * THREADS, r = i % ROWS, c = i / ROWS;
+    plus[u] = 0.f;
+    if (c >= COLS || n0 + r >= a.N || t0 + c >= a.T) continue;
+    if (a.bias) plus[u] = a.bias[n0 + r];
+    if (a.residual) plus[u] += __bfloat162float(a.residual[(t0 + c) * a.residual_stride + n0 + r]);
+  }
   __syncthreads();
   // the warps' sums in a fixed order, consecutive threads along the weight rows (output columns)
-  for (int i = threadIdx.x; i < ROWS * COLS; i += kLinWarps * 32) {
-    const int r = i % ROWS, c = i / ROWS;
-    const int64_t tok = t0 + c;
-    if (n0 + r >= a.N || tok >= a.T) continue;
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const int i = threadIdx.x + u * THREADS, r = i % ROWS, c = i / ROWS;
+    if (c >= COLS || n0 + r >= a.N || t0 + c >= a.T) continue;
     float y = 0.f;
 #pragma unroll
     for (int k = 0; k < kLinWarps; ++k) y += red[k][r][c];
-    if (a.bias) y += a.bias[n0 + r];
-    if (a.residual) y += __bfloat162float(a.residual[tok * a.residual_stride + n0 + r]);
-    a.out[tok * a.out_stride + n0 + r] = __float2bfloat16_rn(y);
+    a.out[(t0 + c) * a.out_stride + n0 + r] = __float2bfloat16_rn(y + plus[u]);
   }
 }
 
