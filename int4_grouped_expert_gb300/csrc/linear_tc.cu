@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 
   // tile = (token block, 128 weight rows), weight rows fastest
   const int mtiles = (a.N + kLtRows - 1) / kLtRows;
-  const int ttiles = static_cast<int>((a.T + C::TOK - 1) / C::TOK);
+  const int ttiles = static_cast<int>((a.T + box_rows - 1) / box_rows);
   const int n_items = mtiles * ttiles;
   const int rank = blockIdx.x % ks, step = gridDim.x / ks;
   // a sum's stages: a scale group, or the whole contraction; and this rank's share of them
@@ -185,14 +185,14 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const int kb0 = parts * rank / ks * share, nk = parts * (rank + 1) / ks * share - kb0;
   const int n_sums = kMid ? nk / per : 1;   // sums per tile
   auto tokens = [&](int item) {
-    return static_cast<int>(min(static_cast<int64_t>(C::TOK), a.T - static_cast<int64_t>(item / mtiles) * C::TOK));
+    return static_cast<int>(min(static_cast<int64_t>(box_rows), a.T - static_cast<int64_t>(item / mtiles) * box_rows));
   };
 
   if (warp == 0) {
     int it = 0;
     bool ok = true;
     for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
-      const int t0 = item / mtiles * C::TOK;
+      const int t0 = item / mtiles * box_rows;
       for (int kb = 0; kb < nk; ++kb, ++it) {
         const int s = it % C::STAGES;
         ok = tc::warp_wait(empty + s, ((it / C::STAGES) & 1) ^ 1, abort_flag, a.status);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     bool ok = true;
     for (int item = blockIdx.x / ks; ok && item < n_items; item += step) {
       const int n = item % mtiles * kLtRows + q4 * 32 + lane;
-      const int64_t t0 = static_cast<int64_t>(item / mtiles) * C::TOK;
+      const int64_t t0 = static_cast<int64_t>(item / mtiles) * box_rows;
       const int nt = tokens(item);
       const float bias = a.bias && n < a.N ? a.bias[n] : 0.f;
       float* sums = reinterpret_cast<float*>(smem);  // ks > 1: [token][row], in place of the stages
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     tc::cluster_sync();
     const int item = blockIdx.x / ks;
     const int nt = tokens(item), n0 = item % mtiles * kLtRows;
-    const int64_t t0 = static_cast<int64_t>(item / mtiles) * C::TOK;
+    const int64_t t0 = static_cast<int64_t>(item / mtiles) * box_rows;
     const int c0 = nt * rank / ks, items = (nt * (rank + 1) / ks - c0) * (kLtRows / 4);  // (token, four rows)
     const uint32_t base = tc::smem_u32(smem);
     constexpr int U = 4;  // items on their way per thread
@@ -525,19 +525,8 @@ cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
                                         true, a.x, a.x_stride, a.K, a.xh, a.xexp, a.status);
     if (e != cudaSuccess) return e;
   }
-  // the tokens (x itself, or its f16 copy) as a 2-d tensor: boxes of a tile's tokens x 64 columns (128 bytes),
-  // zero fill past the last token
-  const int box_rows = static_cast<int>(std::min<int64_t>(C::TOK, (a.T + 15) / 16 * 16));
-  CUtensorMap map;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kMid ? a.x_stride : a.K) * 2};
-  const cuuint32_t box[2] = {kLtBK, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
-  if (enc(&map, kMid ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-          kMid ? const_cast<void*>(static_cast<const void*>(a.x)) : static_cast<void*>(a.xh), dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  const int64_t items = static_cast<int64_t>((a.N + kLtRows - 1) / kLtRows) * ((a.T + C::TOK - 1) / C::TOK);
+  const int64_t mtiles = (a.N + kLtRows - 1) / kLtRows;
+  int64_t items = mtiles * ((a.T + C::TOK - 1) / C::TOK);
   const int nk = a.K / kLtBK, parts = kMid ? a.K / a.group : nk;
   // contraction splits: stages of a share + about 8 stages' worth of start, drain and join, only while a
   // tile per cluster fits the GPU at once. Clusters of k blocks of this size that 152 SMs hold (the
@@ -549,6 +538,24 @@ cudaError_t launch_tc_t(const LinearArgs& a, int num_sms, cudaStream_t stream) {
     const int64_t cost = (parts + k - 1) / k * (nk / parts) + 8 + k;
     if (items * 152 <= static_cast<int64_t>(kHeld[k]) * num_sms && cost < best) best = cost, ks = k;
   }
+  // Tokens of a tile: as few as take no more rounds of all SMs. (A round's time is mostly the conversion of
+  // its weights, a little the tokens': 1186 tokens 3200 -> 3844 at 8 bits, 31 rows of 5 tiles in two
+  // rounds, 59.5 us; 31 rows of 9 tiles of 144 tokens, in two rounds, 52.6.)
+  int64_t ttiles = (a.T + C::TOK - 1) / C::TOK;
+  if (!kMid && ks == 1) ttiles = std::max(ttiles, (items + num_sms - 1) / num_sms * num_sms / mtiles);
+  const int box_rows = static_cast<int>(std::min<int64_t>(C::TOK, ((a.T + ttiles - 1) / ttiles + 15) / 16 * 16));
+  items = mtiles * ((a.T + box_rows - 1) / box_rows);
+  // the tokens (x itself, or its f16 copy) as a 2-d tensor: boxes of a tile's tokens x 64 columns (128 bytes),
+  // zero fill past the last token
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kMid ? a.x_stride : a.K) * 2};
+  const cuuint32_t box[2] = {kLtBK, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
+  if (enc(&map, kMid ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+          kMid ? const_cast<void*>(static_cast<const void*>(a.x)) : static_cast<void*>(a.xh), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<kBits, kMid>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
