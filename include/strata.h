@@ -370,8 +370,8 @@ typedef struct {
  * 16-byte aligned). out may be the residual itself (same address and stride); otherwise out
  * overlaps no input. T == 0 is a no-op.
  * Up to STRATA_LINEAR_EXACT_T tokens the codes are multiplied as exact integers and the sums scaled in fp32;
- * longer batches multiply weights rounded once to f16 (2^-11 relative), with f16 copies of the rows of
- * x in the workspace, each times a power of two that keeps its range.
+ * longer batches may multiply weights rounded once to f16 (2^-11 relative), with f16 copies of the
+ * rows of x in the workspace, each times a power of two that keeps its range.
  * workspace >= strata_linear_workspace_size(w, T) bytes (0: the projection or T is invalid),
  * 256-byte aligned, device; it needs no initialisation. strata_workspace_status reads its status.
  */

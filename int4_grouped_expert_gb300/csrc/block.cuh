@@ -6,10 +6,13 @@
 
 namespace strata {
 
-// Up to this many tokens a projection streams its codes through registers (linear.cu).
+// Up to this many tokens a projection streams its codes through registers (linear.cu), whatever its size
+// (us, streamed / tcgen05, 32 tokens at 4 bits: 4096 -> 6144 12.7 / 14.8, 7168 -> 9216 22.1 / 21.9,
+// 1024 -> 1024 3.2 / 6.7); beyond that linear_streams() weighs.
 constexpr int kLinearStreamT = 32;
-// Beyond that and up to this many, tcgen05 multiplies x with the integer codes (linear_tc.cu); more tokens
-// take f16 operands.
+// Up to this many tcgen05 multiplies x with the integer codes (linear_tc.cu); more tokens take f16 operands
+// (us, integers / f16, 4 bits: 33 tokens 4096 -> 6144 15.1 / 16.0, 1024 -> 1024 6.7 / 8.9; 64 tokens 7168 ->
+// 9216 23.2 / 25.2; 128 tokens 4096 -> 6144 24 / 18.5).
 constexpr int kLinearMidT = STRATA_LINEAR_EXACT_T;
 
 // The power of two that a row of f16 operands is divided by, for its largest bf16 magnitude (key as
@@ -34,6 +37,7 @@ struct LinearArgs {
   __half* xh;
   int* xexp;
 };
+bool linear_streams(int64_t T, int64_t K, int64_t N);
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t stream);
 

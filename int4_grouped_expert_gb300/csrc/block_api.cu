@@ -150,7 +150,7 @@ strata_status strata_linear_forward(const strata_linear* w, const void* x_bf16, 
   a.xexp = reinterpret_cast<int*>(base + L.xexp);
   a.xh = reinterpret_cast<__half*>(base + L.xh);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (T <= kLinearStreamT) return of(launch_linear_stream(a, st));
+  if (linear_streams(T, w->K, w->N)) return of(launch_linear_stream(a, st));
   int sms = 0;
   if (!sm_count(&sms)) return STRATA_ERR_CUDA;
   return of(launch_linear_tc(a, sms, st));

@@ -1,4 +1,5 @@
-// Projections with group-quantized weights for few tokens: y[t,n] = sum_g s[n,g] sum_{c in g} x[t,c] q[n,c],
+// Projections with group-quantized weights for few tokens, or few weights:
+//   y[t,n] = sum_g s[n,g] sum_{c in g} x[t,c] q[n,c],
 // the format of "Strata" MoE tuning notes (lpnh.cn/news/2730718, §2.1: G codes share one fp16 scale).
 //
 // The weights are read once. A block owns 16 to 64 weight rows and its 8 warps take alternate pieces of the
@@ -6,10 +7,13 @@
 // cores (mma.sync m16n8k16, 16 rows as A, 8 tokens as B). The order of a contraction is free, so lane t
 // of a quad takes 16 or 32 consecutive codes of a row instead of the pairs the instruction names, and
 // the matching activations. What bounds it: at one token and 4 bits the ALU pipe (70% busy: shifts and
-// LOP3 that unpack the codes), with more tokens the reads of x from L2.
+// LOP3 that unpack the codes), with more tokens the reads of x from L2. Measured: 1 token at 4 bits 1024 ->
+// 1024 1.8 us, 4096 -> 6144 6.6 us (2.0 TB/s); 16 tokens at 8 bits 4096 -> 6144 10.4 us (2.5 TB/s).
 //
 // The codes are exact in bf16 (|q| <= 128), the activations are bf16, their products are exact in
 // fp32, and the group's scale multiplies the fp32 sum: nothing is rounded before the output.
+#include <algorithm>
+
 #include "block.cuh"
 
 namespace strata {
@@ -90,7 +94,8 @@ __global__ void __launch_bounds__(kLinWarps * 32, kBlocks) linear_stream_kernel(
 #pragma unroll
         for (int i = 0; i < WPL / 4; ++i) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-          w[slot][r][4 * i] = v.x; w[slot][r][4 * i + 1] = v.y; w[slot][r][4 * i + 2] = v.z; w[slot][r][4 * i + 3] = v.w;
+          w[slot][r][4 * i] = v.x; w[slot][r][4 * i + 1] = v.y;
+          w[slot][r][4 * i + 2] = v.z; w[slot][r][4 * i + 3] = v.w;
         }
       }
       sc[slot][r] = __ldg(sp[r] + (u >> ushift));
@@ -196,23 +201,46 @@ __global__ void __launch_bounds__(kLinWarps * 32, kBlocks) linear_stream_kernel(
   }
 }
 
+constexpr int kLinSms = 152;
+constexpr int kLinNarrowN = kLinSms * 16;  // up to here 16-row blocks take one round
+
+// Whether more than 32 tokens are streamed too, 32 at a time, or go to linear_tc.cu: by what either was
+// measured to take, in hundredths of us. A round of streaming blocks on all SMs grows with K; the other
+// kernel's time is mostly its start, a cluster's join and, beyond 64 tokens, the pass before it. (us, streamed
+// / tcgen05, at 4 bits: 64 tokens 1024 -> 1024 3.3 / 7.5, 4096 -> 1024 7.3 / 9.9, 4096 -> 2048 12.4 / 10.7;
+// 256 tokens 4096 -> 256 7.2 / 19.5, 4096 -> 1024 23.5 / 20.9; 33 tokens 7168 -> 9216 38.9 / 22.4.)
+bool linear_streams(int64_t T, int64_t K, int64_t N) {
+  if (T <= kLinearStreamT) return true;
+  const bool narrow = N <= kLinNarrowN;
+  const int64_t rows = narrow ? 16 : 64;
+  const int64_t rounds = ((N + rows - 1) / rows * ((T + 31) / 32) + kLinSms - 1) / kLinSms;
+  const int64_t stream = narrow ? 200 + rounds * (60 + 115 * K / 1024) : 150 + rounds * (250 + 205 * K / 1024);
+  const int64_t other = T <= kLinearMidT ? 550 + 65 * K / 1024 + 3 * T / 2
+                                         : 830 + 85 * K / 1024 + 5 * std::min<int64_t>(T, 300) / 2;
+  return stream < other;
+}
+
 template <int kBits, int kUnit, int kNT, int kMT, int kPF, int kLinWarps, int kBlocks>
 static cudaError_t launch_stream_n(const LinearArgs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.N + 16 * kMT - 1) / (16 * kMT)),
                   static_cast<unsigned>((a.T + 8 * kNT - 1) / (8 * kNT)));
-  return launch_kernel(linear_stream_kernel<kBits, kUnit, kNT, kMT, kPF, kLinWarps, kBlocks>, grid, kLinWarps * 32, 0, stream, true, a);
+  return launch_kernel(linear_stream_kernel<kBits, kUnit, kNT, kMT, kPF, kLinWarps, kBlocks>, grid, kLinWarps * 32, 0,
+                       stream, true, a);
 }
 // Up to 8 tokens the weights are all the traffic: 16 rows a block, the next step's codes on their way. With
 // more, every block reads all of x, and wider blocks (32 rows, 64 beyond 16 tokens) read it less
 // often; where 16-row blocks leave SMs idle, they are faster (us, wide / 16 rows: 16 tokens, 8 bits,
-// 7168 -> 9216 19.6 / 32.1, 4 bits, 1024 -> 1024 2.7 / 2.2; 32 tokens 30.4 / 67 and 5.6 / 3.2).
+// 7168 -> 9216 19.6 / 32.1, 4 bits, 1024 -> 1024 2.7 / 2.2; 32 tokens 30.4 / 67 and 5.6 / 3.2). Blocks of 48
+// rows and 16 warps where they take one round of the SMs and 32-row blocks two (us, 32 / 48 rows: 16
+// tokens, 4096 -> 6144 9.5 / 8.1 at 4 bits, 11.1 / 10.4 at 8; in one round both, 4096 -> 4096 5.9 / 8.2).
 template <int kBits, int kUnit>
 static cudaError_t launch_stream_t(const LinearArgs& a, cudaStream_t stream) {
-  const bool narrow = a.N <= 152 * 16;
+  const bool narrow = a.N <= kLinNarrowN;
   if (a.T <= 8) return launch_stream_n<kBits, kUnit, 1, 1, 2, 8, 3>(a, stream);
   if (a.T <= 16)
-    return narrow ? launch_stream_n<kBits, kUnit, 2, 1, 1, 8, 3>(a, stream)
-                  : launch_stream_n<kBits, kUnit, 2, 2, 1, 8, 2>(a, stream);
+    return narrow                                   ? launch_stream_n<kBits, kUnit, 2, 1, 1, 8, 3>(a, stream)
+           : a.N > kLinSms * 32 && a.N <= kLinSms * 48 ? launch_stream_n<kBits, kUnit, 2, 3, 1, 16, 1>(a, stream)
+                                                    : launch_stream_n<kBits, kUnit, 2, 2, 1, 8, 2>(a, stream);
   return narrow ? launch_stream_n<kBits, kUnit, 4, 1, 1, 8, 2>(a, stream)
                 : launch_stream_n<kBits, kUnit, 4, 4, 1, 8, 1>(a, stream);
 }

@@ -152,3 +152,40 @@ def test_quantized_from_fp16(bits):
     # a code is off by at most half a scale: uniform, 1/sqrt(12) of a scale in the mean per weight
     s = lin.scales.cpu().numpy().astype(np.float64).max()
     assert np.abs(got - y).max() < 6 * s / np.sqrt(12) * np.sqrt(512) + 0.01
+
+
+
+@pytest.mark.parametrize("T", [33, 64, 65, 200, 513])
+@pytest.mark.parametrize("N", [8, 100, 256, 1030])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_few_weights_for_many_tokens(T, N, bits):
+    """Small matrices are streamed for longer batches than large ones."""
+    check(T, N, 512, bits, 128, with_bias=True, with_res=True)
+
+
+@pytest.mark.parametrize("bits,group", [(4, 64), (4, 128), (4, 256), (8, 64), (8, 128), (8, 256)])
+@pytest.mark.parametrize("T", [33, 64, 65, 130, 257])
+def test_every_format_and_batch_of_a_wide_layer(T, bits, group):
+    check(T, 5003, 768, bits, group)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("K,group", [(64, 64), (192, 64), (128, 128), (384, 128), (1152, 128), (256, 256)])
+@pytest.mark.parametrize("T", [40, 90])
+def test_contraction_lengths_of_a_wide_layer(T, K, group, bits):
+    check(T, 5003, K, bits, group)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T,N", [(40, 1500), (61, 2100), (128, 1024), (250, 700)])
+def test_long_contractions_are_shared(T, N, bits):
+    """Few tiles and a long contraction: blocks share a tile, with bias, residual and odd rows."""
+    check(T, N, 7168, bits, 128, with_bias=True, with_res=True, out_pad=5)
+    check(T, N, 7168, bits, 64, with_bias=True, with_res=True, in_place=True)
+
+
+@pytest.mark.parametrize("T,N,K", [(40, 5003, 256), (300, 5003, 256), (1100, 2049, 256), (3000, 1030, 128)])
+def test_bias_residual_and_strides_of_a_wide_layer(T, N, K):
+    """Several rounds of tiles, token tiles below the largest, rows at any alignment."""
+    check(T, N, K, 4, 64, with_bias=True, with_res=True, x_pad=8, out_pad=3)
+    check(T, N, K, 8, 128, with_bias=True, with_res=True, x_pad=40, out_pad=1, in_place=True)
