@@ -29,6 +29,9 @@
 // Either way pieces leave reference, sum and fp32 rows in the workspace, the last to arrive in a
 // group of up to 8 (or the root of the count) joins the group's, and the last group the groups'. All sums are
 // in the order of the pieces.
+//
+// Bound by memory, but for its start and end: 8 sequences of 131072 tokens 7.0 TB/s, one 51 us (5.2 TB/s), of
+// which about 9 us are launch, the search for the piece, the first copies and the join.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -38,7 +41,10 @@ namespace strata {
 constexpr int kAttWarps = 4;
 constexpr int kAttStep = 32;  // tokens of one warp step
 constexpr int kAttSlots = 2;  // steps of a warp in shared memory
-constexpr int kAttMinSteps = 8;      // steps that a piece has at least: two a warp
+// A pair of up to kAttWholeSteps, two a warp, is not cut: a second step takes less than the join. Longer ones may
+// be cut down to kAttMinSteps, one a warp. (us, pieces of 4 steps at least / of 8: 200 tokens 6.7 / 6.2,
+// 500 7.2 / 8.0, 1000 7.6 / 8.3; of 16: 6.2, 8.5, 10.0.)
+constexpr int kAttWholeSteps = 8, kAttMinSteps = 4;
 constexpr int kAttMinShare = 2;      // steps that a warp's share has at least (200 sequences of 50: 2 12.3 us, 4 18.7)
 constexpr int kAttResident = 456;    // blocks that run at once: three on each of 152 SMs
 
@@ -88,6 +94,9 @@ __device__ __forceinline__ SeqSteps seq_steps(const AttnArgs& a, const SeqView& 
   return {lo, max(1, (v.len + kAttStep - 1) / kAttStep - lo)};  // (no tokens: one empty step, zeros)
 }
 
+__device__ __forceinline__ int pieces_of(int steps, int per) {
+  return steps <= kAttWholeSteps ? (steps + kAttWholeSteps - 1) / kAttWholeSteps : (steps + per - 1) / per;
+}
 // This block's piece: found by a scan over the sequences, the same in every block.
 struct Piece {
   int seq, head, index, of;  // piece `index` of `of`
@@ -100,7 +109,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
     for (int q = 2; q <= 4; ++q) {
       const int pieces = kAttResident - heads * q / 4;
       const int per = max(kAttMinSteps, static_cast<int>((static_cast<int64_t>(steps) * heads + pieces - 1) / pieces));
-      k = (steps + per - 1) / per;
+      k = pieces_of(steps, per);
       if (k * heads <= kAttResident) break;
     }
     if (static_cast<int>(blockIdx.x) >= k * heads) return false;
@@ -121,7 +130,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
   int per = 0, blocks = 0, slots = 0;
   // blocks and workspace slots that a sequence's steps come to
   auto count = [&](int steps, int& blocks, int& slots) {
-    const int k = (steps + per - 1) / per * heads;
+    const int k = pieces_of(steps, per) * heads;
     blocks += k;
     slots += k > heads ? k : 0;
   };
@@ -153,7 +162,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
       if (id < b0 + nb) {
         seq = s;
         local = id - b0;
-        k = (steps + per - 1) / per;
+        k = pieces_of(steps, per);
         slot0 = l0;
         break;
       }
@@ -784,7 +793,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
 }
 
 // Rows of a sequence and K/V head up to which its cache is streamed through this kernel; more go to
-// the tensor-core kernel.
+// attention_tc.cu. (us, streamed / there, 16 rows: one sequence of 32768 26 / 44, 16 of 4096 29 / 61,
+// 64 of 2000 61 / 85; 12 rows, 4 of 8192 31 / 55. A third tile of 8 rows would not fit the registers.)
 constexpr int kAttStreamRows = 16;
 // (sequence, K/V head) pairs above which each warp goes its own way: the figures are at the top.
 constexpr int kAttSoloPairs = kAttResident / 2;

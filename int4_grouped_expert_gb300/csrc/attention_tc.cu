@@ -20,8 +20,10 @@
 // Queries become f16 with a power of two per row; a token that no row sees or in a page that does not
 // exist becomes zeros and a masked score, so what lies there does not matter.
 //
-// Bound by the softmax's instructions and by shared memory (scores of 64 tokens read 6 KB per 32 clocks
-// of MMA). Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every
+// Measured: 2048 queries on 8192 tokens, 32 query and 8 K/V heads of 128: 242 us, 993 TFLOP/s; a tile of 64
+// tokens takes a block 1.17 us, half of it MMA. Softmax and conversion instructions (issue 60% of active
+// cycles), shared memory (67%) and the tensor pipe (45%) wait for one another over the score buffers; none is full.
+// Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every
 // role leaves its loop, MMAs in flight are drained (bounded) and TMEM is freed.
 #include <algorithm>
 
@@ -38,12 +40,13 @@ constexpr int kAtThreads = 640;
 constexpr int kAtBad = 8;       // ring of per-tile masks of tokens in pages that do not exist
 constexpr int kAtSms = 152;     // blocks that run at once
 constexpr int kAtMaxSlots = 3 * kAtSms;
-constexpr int kAtMinTiles = 8;  // tiles that a piece has at least
+constexpr int kAtMinTiles = 4;  // tiles that a piece has at least
 // What a block costs beside its tiles, in tiles of 1.17 us: to start and to fill its ring; the same and to
-// leave a piece; for the kernel that joins. With a quarter of the SMs idle a tile takes a sixth less.
-// (32 query heads, 8 K/V heads, us whole and cut: 64 queries on 4096 tokens, 8 units, 77 and 27; 64 on
-// 32768 582 and 60; 512 on 8192, 64 units, 141 and 94; 1280 on 8192, of whose 160 units 8 are cut,
-// 244 and 170. Cutting 104 of 256 units took 276 for 245.)
+// leave a piece; for the kernel that joins (and half a tile a piece). Where a quarter of the SMs idle after
+// full rounds, a tile takes a sixth less. (32 query heads, 8 K/V heads, us whole and cut: 64 queries on 4096
+// tokens, 8 units, 77 and 28; 64 on 32768 582 and 60; 512 on 8192, 64 units, 141 and 97; 1280 on 8192, of whose
+// 160 units 8 are cut, 244 and 170. Cutting 104 of 256 units took 276 for 245. Pieces of 4 tiles at
+// least or of 8: 64 queries on 1600 tokens 23 / 28.)
 constexpr int kAtStart = 4, kAtPiece = 8, kAtJoin = 8;
 constexpr int kAtMostCut = kAtSms * 3 / 4;  // (more units than these are never worth cutting)
 
@@ -131,8 +134,9 @@ __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
     // lane i weighs i + 1 pieces of the longest units, and in proportion of the others
     const int n = static_cast<int>(most), c = lane + 1;
     const int pieces = max(u.rest, static_cast<int>(u.rest * c * (tiles / all / most)));
-    int cost = (pieces + kAtSms - 1) / kAtSms * (n / c + 1 + (c > 1 ? kAtPiece : kAtStart)) + (c > 1 ? kAtJoin : 0);
-    if (pieces <= kAtMostCut) cost -= cost / 6;
+    const int rounds = (pieces + kAtSms - 1) / kAtSms;
+    int cost = c == 1 ? rounds * (n + 1 + kAtStart) : rounds * (n / c + 1 + kAtPiece) + kAtJoin + c / 2;
+    if (c == 1 && u.whole > 0 && u.rest <= kAtMostCut) cost -= cost / 6;
     if (c > 1 && (n < c * kAtMinTiles || u.rest * c > a.tc_slots)) cost = 0x3FFFFFF;
     cost = min(cost, 0x3FFFFFF);
     u.k = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(cost) << 5 | lane) % 32 + 1;
@@ -712,9 +716,10 @@ __global__ void __launch_bounds__(kAtJoinRows * kD / 8) attention_tc_join_kernel
 }
 
 template <int kD>
-cudaError_t launch_join_t(const AttnArgs& a, cudaStream_t stream) {
-  return launch_kernel(attention_tc_join_kernel<kD>, dim3(std::min(a.tc_slots, 152) * 4), dim3(kAtJoinRows * kD / 8), 0,
-                       stream, true, a);
+cudaError_t launch_join_t(const AttnArgs& a, int64_t units, cudaStream_t stream) {
+  const int64_t slices = units * (256 / kAtJoinRows);
+  return launch_kernel(attention_tc_join_kernel<kD>, dim3(static_cast<unsigned>(std::min<int64_t>(slices, kAtSms * 4))),
+                       dim3(kAtJoinRows * kD / 8), 0, stream, true, a);
 }
 
 template <int kD>
@@ -745,14 +750,16 @@ int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t gr
   const int64_t rest = units % kAtSms;
   if (b.T == static_cast<int64_t>(b.n_seq) * b.max_q && (rest == 0 || rest > kAtMostCut)) return 0;
   const int64_t seen = window > 0 ? std::min<int64_t>(b.max_kv, window + 256 / group) : b.max_kv;
-  const int64_t cut = std::min<int64_t>(seen / kAtTok / kAtMinTiles, 32);  // (two short pieces do not pay: 28 us, 31)
-  return cut > 2 ? static_cast<int>(std::min<int64_t>(kAtMaxSlots, std::min<int64_t>(units, kAtSms - 1) * cut)) : 0;
+  if (seen / kAtTok < 6 * kAtMinTiles) return 0;  // (1024 tokens: 28 us, 31 with the kernel that joins)
+  const int64_t cut = std::min<int64_t>(seen / kAtTok / kAtMinTiles, 32);
+  return static_cast<int>(std::min<int64_t>(kAtMaxSlots, std::min<int64_t>(units, kAtSms - 1) * cut));
 }
 size_t attn_tc_part_floats(const strata_kv_cache& c, int slots) {
   return static_cast<size_t>(slots) * 256 * (c.head_dim + 2);
 }
 cudaError_t launch_attention_tc_join(const AttnArgs& a, cudaStream_t stream) {
-  return a.c.head_dim == 64 ? launch_join_t<64>(a, stream) : launch_join_t<128>(a, stream);
+  const int64_t units = most_units(a.c, a.b, a.group);
+  return a.c.head_dim == 64 ? launch_join_t<64>(a, units, stream) : launch_join_t<128>(a, units, stream);
 }
 cudaError_t launch_attention_tc(AttnArgs a, cudaStream_t stream) {
   // Blocks find their units in the lengths where units are cut, or where blocks by max_q would mostly be
