@@ -804,7 +804,8 @@ AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_hea
   const int64_t G = n_heads / c.n_kv_heads, most_rows = b.max_q * G;
   if (most_rows > kAttStreamRows) {
     p.tc = true;
-    p.tc_part_floats = attn_tc_part_floats(c, attn_tc_slots(c, b, G, 0));
+    p.tc_slots = attn_tc_slots(c, b, G, 0);
+    p.tc_part_floats = attn_tc_part_floats(c, p.tc_slots);
     // sequences of equal length: none is below the limit
     if (b.T == static_cast<int64_t>(b.n_seq) * b.max_q) return p;
     p.stream_rows = kAttStreamRows;

@@ -1,7 +1,7 @@
 // Causal attention over the paged cache of e4m3 codes for many query rows, on tcgen05 (the formula and
 // the cache are those of attention.cu).
 //
-// A block owns 256 query rows of one sequence and K/V head (query rows x the heads that share it): two
+// A block owns up to 256 query rows of one sequence and K/V head (query rows x the heads that share it): two
 // tiles of 128 rows, a TMEM lane each. It walks the cache in tiles of 64 tokens:
 //   S_i = Q_i K^T (f16, fp32 sums in TMEM) -> softmax weights P_i (f16, in TMEM over S_i) -> O_i += P_i V
 // Each row tile has two score buffers, so that its next scores are ready when a softmax ends, and the
@@ -47,7 +47,7 @@ constexpr int kAtMinTiles = 4;  // tiles that a piece has at least
 // tokens, 8 units, 77 and 28; 64 on 32768 582 and 60; 512 on 8192, 64 units, 141 and 97; 1280 on 8192, of whose
 // 160 units 8 are cut, 244 and 170. Cutting 104 of 256 units took 276 for 245. Pieces of 4 tiles at
 // least or of 8: 64 queries on 1600 tokens 23 / 28.)
-constexpr int kAtStart = 4, kAtPiece = 8, kAtJoin = 8;
+constexpr int kAtStart = 4, kAtPiece = 8, kAtJoin = 6;
 constexpr int kAtMostCut = kAtSms * 3 / 4;  // (more units than these are never worth cutting)
 
 template <int kD>
@@ -90,7 +90,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// The units of a call: 256 rows of a (sequence, K/V head), sequence by sequence, those with the most tokens
+// The units of a call: tc_rows rows of a (sequence, K/V head), sequence by sequence, those with the most tokens
 // to see first. As many as fill all SMs a whole number of times stay whole; the others, which run last, are
 // cut along the tokens where that ends sooner, into pieces of `per` tiles, at most k. The same in every warp.
 struct Units {
@@ -99,7 +99,7 @@ struct Units {
 };
 __device__ __forceinline__ int units_of(const AttnArgs& a, const SeqView& v) {
   const int64_t rows = static_cast<int64_t>(v.n) * a.group;
-  return rows > a.rows_below ? static_cast<int>((rows + 255) / 256) * a.c.n_kv_heads : 0;
+  return rows > a.rows_below ? static_cast<int>((rows + a.tc_rows - 1) / a.tc_rows) * a.c.n_kv_heads : 0;
 }
 __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
   Units u;
@@ -112,7 +112,7 @@ __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
     const int n = units_of(a, v);
     // tokens that a unit sees, on average
     float seen = max(0.f, v.len - 0.5f * v.n);
-    if (a.window > 0) seen = fminf(seen, a.window + 256.f / a.group);
+    if (a.window > 0) seen = fminf(seen, a.window + static_cast<float>(a.tc_rows) / a.group);
     u.mine += n;
     tiles += n * (seen / kAtTok + 1.f);
     if (n > 0) most = fmaxf(most, seen / kAtTok + 1.f);
@@ -156,7 +156,7 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int seq, int head, in
   u.sv = seq_view(a, seq, flag);
   u.rows = u.sv.n * a.group;
   const int p0 = u.sv.len - u.sv.n;  // position of the first query
-  u.tok_hi = min(u.sv.len, p0 + (min(row0 + 256, u.rows) - 1) / a.group + 1);
+  u.tok_hi = min(u.sv.len, p0 + (min(row0 + a.tc_rows, u.rows) - 1) / a.group + 1);
   const int tok_lo = a.window > 0 ? max(0, p0 + row0 / a.group - a.window + 1) : 0;
   u.j_lo = tok_lo / kAtTok;
   u.n_tiles = u.tok_hi > tok_lo ? (u.tok_hi + kAtTok - 1) / kAtTok - u.j_lo : 0;
@@ -177,7 +177,7 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Units& us, in
   seq = __shfl_sync(0xffffffffu, seq, owner);
   left = __shfl_sync(0xffffffffu, left, owner);
   n = __shfl_sync(0xffffffffu, n, owner);
-  return unit_of(a, seq, left % heads, (n / heads - 1 - left / heads) * 256, at < us.whole ? 1 : us.k, us.per,
+  return unit_of(a, seq, left % heads, (n / heads - 1 - left / heads) * a.tc_rows, at < us.whole ? 1 : us.k, us.per,
                  false);
 }
 
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     piece = cut - max(0, at - us.whole) * us.k;
   } else {  // the same order, as if every sequence had max_q rows
     const int heads = a.c.n_kv_heads, of_seq = gridDim.x / a.b.n_seq, left = id % of_seq;
-    u = unit_of(a, id / of_seq, left % heads, (of_seq / heads - 1 - left / heads) * 256, 1, 1,
+    u = unit_of(a, id / of_seq, left % heads, (of_seq / heads - 1 - left / heads) * a.tc_rows, 1, 1,
                 left == 0 && threadIdx.x == 0);
     if (u.rows <= a.rows_below || u.row0 >= u.rows) return;
   }
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     n_tiles = to - from;
     tok_hi = min(tok_hi, (j_lo + n_tiles) * kAtTok);
   }
-  const int last_row = min(row0 + 256, rows) - 1;
+  const int last_row = min(row0 + a.tc_rows, rows) - 1;
   const int n_rt = last_row - row0 >= 128 ? 2 : 1;        // row tiles in use
   const int P = a.c.page_size;
   const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
@@ -734,11 +734,11 @@ cudaError_t launch_tc_t(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
 }  // namespace
 
 // Units if every sequence had max_q rows, and a bound from the rows of all.
-static int64_t full_units(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group) {
-  return (b.max_q * group + 255) / 256 * b.n_seq * c.n_kv_heads;
+static int64_t full_units(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int rows = 256) {
+  return (b.max_q * group + rows - 1) / rows * b.n_seq * c.n_kv_heads;
 }
-static int64_t most_units(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group) {
-  return std::min(full_units(c, b, group), (b.T * group / 256 + b.n_seq) * c.n_kv_heads);
+static int64_t most_units(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int rows = 256) {
+  return std::min(full_units(c, b, group, rows), (b.T * group / rows + b.n_seq) * c.n_kv_heads);
 }
 // Pieces that may come to lie in the workspace; 0: no unit is cut. Above one and a half times the SMs the
 // last units fill their gaps by themselves (512 units of 33 tiles: 165 us whole, 178 with 56 cut). Batches
@@ -747,24 +747,35 @@ int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t gr
   const int64_t units = most_units(c, b, group);
   if (units > kAtSms * 3 / 2) return 0;
   // (of sequences of equal length the units are known)
+  const bool equal = b.T == static_cast<int64_t>(b.n_seq) * b.max_q;
   const int64_t rest = units % kAtSms;
-  if (b.T == static_cast<int64_t>(b.n_seq) * b.max_q && (rest == 0 || rest > kAtMostCut)) return 0;
+  if (equal && (rest == 0 || rest > kAtMostCut)) return 0;
   const int64_t seen = window > 0 ? std::min<int64_t>(b.max_kv, window + 256 / group) : b.max_kv;
-  if (seen / kAtTok < 6 * kAtMinTiles) return 0;  // (1024 tokens: 28 us, 31 with the kernel that joins)
+  // What whole units take, of 128 rows where those start together, against pieces, in tiles as above; of unequal
+  // sequences the longest are cut in two at least. (us, whole / cut, 1472 tokens: 64 queries 28.9 / 23.7,
+  // 512 queries 29.3 / 40.0.)
+  const int64_t n = seen / kAtTok + 1;
+  const int64_t k = std::max<int64_t>(equal ? 1 : 2, std::min(n / kAtMinTiles, kAtSms / units));
+  const int64_t whole = most_units(c, b, group, 128) <= kAtSms ? n * 3 / 4 + 8 : n + 1 + kAtStart;
+  if (units <= kAtSms ? n / k + 1 + kAtPiece + kAtJoin + k / 2 >= whole : n < 24) return 0;
   const int64_t cut = std::min<int64_t>(seen / kAtTok / kAtMinTiles, 32);
   return static_cast<int>(std::min<int64_t>(kAtMaxSlots, std::min<int64_t>(units, kAtSms - 1) * cut));
 }
 size_t attn_tc_part_floats(const strata_kv_cache& c, int slots) {
   return static_cast<size_t>(slots) * 256 * (c.head_dim + 2);
 }
-cudaError_t launch_attention_tc_join(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_attention_tc_join(AttnArgs a, cudaStream_t stream) {
+  a.tc_rows = 256;
   const int64_t units = most_units(a.c, a.b, a.group);
   return a.c.head_dim == 64 ? launch_join_t<64>(a, units, stream) : launch_join_t<128>(a, units, stream);
 }
 cudaError_t launch_attention_tc(AttnArgs a, cudaStream_t stream) {
   // Blocks find their units in the lengths where units are cut, or where blocks by max_q would mostly be
   // empty; the search is 1 us a block.
-  const int64_t full = full_units(a.c, a.b, a.group), most = most_units(a.c, a.b, a.group);
+  // Units of one row tile where they still start together and are not cut: a tile takes them a sixth less.
+  // (us, 256 / 128 rows, 8 K/V heads, 256 rows on 64 tokens 12.2 / 10.4, on 512 19.2 / 16.4, on 1024 27.4 / 23.3.)
+  a.tc_rows = a.tc_slots == 0 && most_units(a.c, a.b, a.group, 128) <= kAtSms ? 128 : 256;
+  const int64_t full = full_units(a.c, a.b, a.group, a.tc_rows), most = most_units(a.c, a.b, a.group, a.tc_rows);
   a.tc_search = a.tc_slots > 0 || full > 2 * most;
   const int64_t grid = a.tc_search ? most + a.tc_slots : full;
   return a.c.head_dim == 64 ? launch_tc_t<64>(a, grid, stream) : launch_tc_t<128>(a, grid, stream);

@@ -75,6 +75,7 @@ struct AttnArgs {
   float* part;            // partial results, a slot per piece of a cut (sequence, K/V head)
   uint32_t* counters;     // [2][kAttMaxSlots], zero between calls
   // attention_tc.cu
+  int tc_rows;            // rows of a block at most: 256, or 128 (attention_tc_join_kernel: 256)
   bool tc_search;         // blocks find their units in the lengths
   int tc_slots;           // pieces that may be left in the workspace; 0: nothing is cut
   float* tc_part;
@@ -88,12 +89,13 @@ struct AttnPlan {
   size_t part_floats, tc_part_floats;
   int stream_rows;        // rows up to which a sequence goes to attention.cu: 0 none, INT_MAX all
   bool tc;                // attention_tc.cu is launched
+  int tc_slots;           // its pieces in the workspace at most
 };
 AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_heads);
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
 int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int window);
 size_t attn_tc_part_floats(const strata_kv_cache& c, int slots);
 cudaError_t launch_attention_tc(AttnArgs a, cudaStream_t stream);
-cudaError_t launch_attention_tc_join(const AttnArgs& a, cudaStream_t stream);  // after both others
+cudaError_t launch_attention_tc_join(AttnArgs a, cudaStream_t stream);  // after both others
 
 }  // namespace strata

@@ -244,7 +244,8 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.window = window;
   a.part = reinterpret_cast<float*>(base + L.part);
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);
-  a.tc_slots = p.tc ? attn_tc_slots(*cache, *batch, a.group, window) : 0;
+  // (a window shortens what is seen, and so the pieces; the workspace is laid out for none)
+  a.tc_slots = p.tc ? std::min(p.tc_slots, attn_tc_slots(*cache, *batch, a.group, window)) : 0;
   a.tc_part = reinterpret_cast<float*>(base + L.tc_part);
   a.status = &reinterpret_cast<WsHeader*>(base)->status;
   a.rows_above = a.rows_below = p.stream_rows;

@@ -391,3 +391,14 @@ def test_nan_in_one_piece_of_a_cut_unit():
     c.gpu()
     got = ref.bf16_bits_to_f64(c.run()).reshape(c.T, 16, 128)
     assert np.isnan(got).all()          # every row sees both tokens: a head's K, the other's V
+
+
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("seqs,Hq,Hkv,D", [
+    ([(150, 150)] * 6, 64, 32, 64),                 # 300 rows a head: a block of 256 and one of 44
+    ([(300, 200), (129, 129), (70, 1), (256, 256)], 40, 40, 128),
+    ([(190, 64)] * 3, 96, 24, 128),                 # exactly 256 rows
+])
+def test_blocks_of_two_row_tiles(seqs, Hq, Hkv, D, window):
+    """Enough units of 128 rows to fill the GPU: a block takes 256."""
+    Case(seqs, Hq, Hkv, D, 32).gpu().check(window)
