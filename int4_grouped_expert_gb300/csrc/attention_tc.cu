@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     n_tiles = to - from;
     tok_hi = min(tok_hi, (j_lo + n_tiles) * kAtTok);
   }
-  const int last_row = min(row0 + a.tc_rows, rows) - 1;
-  const int n_rt = last_row - row0 >= 128 ? 2 : 1;        // row tiles in use
+  const int row_end = min(row0 + a.tc_rows, rows);        // the rows from here on are another block's
+  const int n_rt = row_end - row0 > 128 ? 2 : 1;          // row tiles in use
   const int P = a.c.page_size;
   const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
   const bool softmax_warp = warp >= 4 && warp < 12;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   const int row = row0 + tile * 128 + (warp & 3) * 32 + lane;
 
   if (n_tiles == 0) {  // nothing to see for any row: zeros
-    if (softmax_warp && row < rows) {
+    if (softmax_warp && row < row_end) {
       uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(sv.q0 + row / G) * a.out_stride +
                                             (h * G + row % G) * kD);
       for (int i = 0; i < kD / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     const __nv_bfloat16* q = a.q + static_cast<int64_t>(sv.q0 + row / G) * a.q_stride + (h * G + row % G) * kD;
 #pragma unroll
     for (int i = 0; i < kD / 8; ++i) {
-      v[i] = row < rows ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0u, 0u, 0u, 0u);
+      v[i] = row < row_end ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0u, 0u, 0u, 0u);
       mag = max(mag, bf16x8_mag(v[i]));
     }
     const int e = row_exp(mag);
