@@ -404,7 +404,7 @@ typedef struct {
 /*
  * strata_kv_append — rotates the T rows of k (and of q) by their positions and stores k and v in the
  * cache. Row t goes to slot slots[t]; a negative slot marks a padding row, of which nothing is
- * read or written.
+ * used or written (its elements may be loaded with those of the rows before it).
  *   rotation of pair (a, b) of a head's first rot_dim elements, in fp32:
  *     a' = a*cos - b*sin, b' = b*cos + a*sin,   cos = rope[pos][i], sin = rope[pos][rot_dim/2 + i]
  *     with a, b = elements i and i + rot_dim/2, or 2i and 2i + 1 with STRATA_ROPE_NEIGHBOURS
@@ -422,7 +422,8 @@ typedef struct {
  * rot_dim: 0 (no rotation: rope and positions may be NULL) or a multiple of 16 up to head_dim.
  * The rows of a call that fall into one page must be consecutive rows with consecutive slots. A
  * slot >= n_pages * page_size or a position outside [0, n_pos) sets STRATA_DEV_BAD_SLOT and the row
- * is skipped. dev_status: device uint32 or NULL. T == 0 is a no-op; T <= 2^22.
+ * is skipped: its slot keeps what it holds, and it has no part in the scale. (A page whose first token
+ * was skipped by a call that stored nothing in it has not begun.) dev_status: device uint32 or NULL. T == 0 is a no-op; T <= 2^22.
  */
 strata_status strata_kv_append(const strata_kv_cache* cache, const void* q_bf16, int64_t q_stride,
                                int32_t n_heads, const void* k_bf16, int64_t k_stride,

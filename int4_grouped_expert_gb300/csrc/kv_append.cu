@@ -1,8 +1,9 @@
 // Rotation of q and k by position and the append of k and v to a paged cache of e4m3 codes with one
 // power-of-two scale per (page, head).
 //
-// A run is a stretch of rows with consecutive slots in one page; one block owns a run of one K/V head,
-// so the scale of a (page, head) has one writer and needs no atomics. The block holds the run's rows in
+// A run is a stretch of rows with consecutive slots in one page, found from the slots alone; one block owns a
+// run of one K/V head, so the scale of a (page, head) has one writer and needs no atomics. A row whose position
+// is out of range is a hole in its run: not stored, and no part of the scale. The block holds the run's rows in
 // registers as they came, finds the largest magnitude of the rotated rows, settles the new scale with
 // the page's old one, rewrites the older codes if the scale grew, rotates again and writes the codes:
 // the rotation is elementwise in fp32 with each product and sum rounded once, so both times give the
@@ -118,22 +119,22 @@ __device__ __forceinline__ uint2 codes8(const float* y, float inv) {
   return d;
 }
 
+__device__ __forceinline__ bool in_cache(const KvAppendArgs& a, int slot) {
+  return slot >= 0 && slot < a.c.n_pages * a.c.page_size;
+}
+__device__ __forceinline__ bool in_table(const KvAppendArgs& a, int position) {
+  return position >= 0 && position < a.n_pos;
+}
 // 0: padding, 1: good, 2: out of range
 __device__ __forceinline__ int row_state(const KvAppendArgs& a, int r) {
   const int s = a.slots[r];
   if (s < 0) return 0;
-  if (s >= a.c.n_pages * a.c.page_size) return 2;
-  if (a.rot_dim > 0) {
-    const int p = a.positions[r];
-    if (p < 0 || p >= a.n_pos) return 2;
-  }
-  return 1;
+  return in_cache(a, s) && (a.rot_dim == 0 || in_table(a, a.positions[r])) ? 1 : 2;
 }
-// Row r continues the run that row r - 1 is in.
+// Row r, whose slot is in the cache, continues the run that row r - 1 is in, whether that one is stored or not.
 __device__ __forceinline__ bool continues(const KvAppendArgs& a, int r) {
-  if (r == 0 || row_state(a, r - 1) != 1) return false;
   const int s = a.slots[r];
-  return s % a.c.page_size != 0 && s == a.slots[r - 1] + 1;
+  return r > 0 && s % a.c.page_size != 0 && a.slots[r - 1] == s - 1;
 }
 
 // The older codes of a (page, head) times old / now, when the scale grew.
@@ -182,19 +183,20 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     vw[j][0] = on ? v[kp.a] : z;
     vw[j][1] = on ? v[kp.b] : z;
   }
-  // its first row's cosines (a position out of range is no row of the run: any table row will do) and the
+  // its first row's cosines (a row with a position out of range is not stored: any table row will do) and the
   // page's scales as well
   Turn t_first = none;
+  int p_first = 0;
   if (a.rot_dim > 0) {
-    const int r = min(row0 + ri, a.T - 1);
-    t_first = turn_at(a, kp, min(static_cast<int64_t>(max(a.positions[r], 0)), a.n_pos - 1));
+    p_first = a.positions[min(row0 + ri, a.T - 1)];
+    t_first = turn_at(a, kp, min(static_cast<int64_t>(max(p_first, 0)), a.n_pos - 1));
   }
   const int64_t ph = page * a.c.n_kv_heads + head;
   const float k_old = off ? a.c.k_scales[ph] : 0.f, v_old = off ? a.c.v_scales[ph] : 0.f;
   // the run's length: the first row that does not continue it (P <= kAppThreads)
   {
     const int i = threadIdx.x, r = row0 + i;
-    const bool in = off + i < P && r < a.T && a.slots[r] == slot + i && row_state(a, r) == 1;
+    const bool in = off + i < P && r < a.T && a.slots[r] == slot + i;
     const unsigned out = __ballot_sync(0xffffffffu, !in);
     if (lane == 0) s_len[warp] = out ? 32 * warp + __ffs(out) - 1 : kAppThreads;
   }
@@ -203,9 +205,16 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) n = min(n, s_len[w]);
 
+  unsigned skipped = 0;  // bit j: this thread's row of iteration j is past the run, or a hole in it
 #pragma unroll
-  for (int j = 0; j < kIter; ++j)
-    if (j * RPI + ri >= n) kw[j][0] = kw[j][1] = vw[j][0] = vw[j][1] = make_uint4(0u, 0u, 0u, 0u);
+  for (int j = 0; j < kIter; ++j) {
+    const int i = j * RPI + ri;
+    bool on = i < n;
+    if (on && a.rot_dim > 0) on = in_table(a, j == 0 ? p_first : a.positions[row0 + i]);
+    if (on) continue;
+    skipped |= 1u << j;
+    kw[j][0] = kw[j][1] = vw[j][0] = vw[j][1] = make_uint4(0u, 0u, 0u, 0u);
+  }
   // a row is good when all its threads hold finite values
   auto good_row = [&](const float (&k)[16], const float (&v)[16]) {
     const unsigned bad = __ballot_sync(0xffffffffu, !(finite16(k) && finite16(v)));
@@ -218,12 +227,12 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     if (j * RPI >= n) break;
     float k[16], v[16];
     const int i = j * RPI + ri;
-    rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : i < n ? turn_of(a, kp, row0 + i) : none, k);
+    rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : skipped >> j & 1u ? none : turn_of(a, kp, row0 + i), k);
     rotated(vw[j][0], vw[j][1], vp, none, v);
     if (good_row(k, v)) {
       km = fmaxf(km, max16(k));
       vm = fmaxf(vm, max16(v));
-    } else {
+    } else if (!(skipped >> j & 1u)) {
       bad_rows |= 1u << j;
     }
   }
@@ -233,7 +242,8 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     s_max[0][warp] = km;
     s_max[1][warp] = vm;
   }
-  __syncthreads();
+  // a run of holes changes nothing (kIter bits: all of this thread's rows)
+  if (!__syncthreads_or(skipped != (1u << kIter) - 1u)) return;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     km = fmaxf(km, s_max[0][w]);
@@ -251,6 +261,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   for (int j = 0; j < kIter; ++j) {
     const int i = j * RPI + ri;
     if (i >= n) break;
+    if (skipped >> j & 1u) continue;
     float k[16], v[16];
     rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : turn_of(a, kp, row0 + i), k);
     rotated(vw[j][0], vw[j][1], vp, none, v);
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(kAppThreads, kIter > 2 ? 1 : 3) kv_append_kern
   const int st = threadIdx.x < a.rows_per_block && r < a.T ? row_state(a, r) : 0;
   if (st == 2) set_status(a.status, STRATA_DEV_BAD_SLOT);
   __shared__ unsigned s_starts[kAppThreads / 32];
-  const unsigned starts = __ballot_sync(0xffffffffu, st == 1 && !continues(a, r));
+  const unsigned starts = __ballot_sync(0xffffffffu, st != 0 && in_cache(a, a.slots[r]) && !continues(a, r));
   if ((threadIdx.x & 31) == 0) s_starts[threadIdx.x >> 5] = starts;
   __syncthreads();
   for (int w = 0; w < kAppThreads / 32; ++w)
