@@ -90,7 +90,7 @@ struct SeqSteps {
 __device__ __forceinline__ SeqSteps seq_steps(const AttnArgs& a, const SeqView& v) {
   const int64_t rows = static_cast<int64_t>(v.n) * a.group;
   if (rows == 0 || rows > a.rows_above) return {0, 0};
-  const int lo = a.window > 0 ? max(0, v.len - v.n - a.window + 1) / kAttStep : 0;
+  const int lo = first_seen(a, v.len - v.n) / kAttStep;
   return {lo, max(1, (v.len + kAttStep - 1) / kAttStep - lo)};  // (no tokens: one empty step, zeros)
 }
 

@@ -47,5 +47,10 @@ __device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s, bool flag)
   if (bad && flag) set_status(a.status, STRATA_DEV_BAD_SLOT);
   return v;
 }
+// First token that a row of the sequence sees whose first row stands at position p (below 0: before the first
+// token). No step of it leaves 32 bits, whatever the window.
+__device__ __forceinline__ int first_seen(const AttnArgs& a, int p) {
+  return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
 
 }  // namespace strata

@@ -157,7 +157,7 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int seq, int head, in
   u.rows = u.sv.n * a.group;
   const int p0 = u.sv.len - u.sv.n;  // position of the first query
   u.tok_hi = min(u.sv.len, p0 + (min(row0 + a.tc_rows, u.rows) - 1) / a.group + 1);
-  const int tok_lo = a.window > 0 ? max(0, p0 + row0 / a.group - a.window + 1) : 0;
+  const int tok_lo = first_seen(a, p0 + row0 / a.group);
   u.j_lo = tok_lo / kAtTok;
   u.n_tiles = u.tok_hi > tok_lo ? (u.tok_hi + kAtTok - 1) / kAtTok - u.j_lo : 0;
   u.of = min(k, max(1, (u.n_tiles + per - 1) / per));

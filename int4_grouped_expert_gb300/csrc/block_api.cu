@@ -241,7 +241,8 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.n_heads = n_heads;
   a.group = n_heads / cache->n_kv_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.window = window;
+  // (a window that no position reaches past is none: below max_kv, position - window stays in 32 bits)
+  a.window = window < batch->max_kv ? window : 0;
   a.part = reinterpret_cast<float*>(base + L.part);
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);
   // (a window shortens what is seen, and so the pieces; the workspace is laid out for none)

@@ -1,5 +1,5 @@
-"""Attention where the first rows of a sequence see nothing: rows before its first token, and what a
-block of such rows may write."""
+"""Attention where the first rows of a sequence see nothing: rows before its first token, what a block of
+such rows may write, and windows longer than any sequence."""
 import numpy as np
 import pytest
 
@@ -22,3 +22,13 @@ def test_blocks_of_empty_rows_leave_the_next_block_alone(n, L, Hq, Hkv, D):
     assert (got[:n - L] == 0).all() and (np.abs(got[n - L:n]).max((1, 2)) > 0).all()
     for _ in range(5):
         assert np.array_equal(c.run(), first)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 30])
+def test_windows_beyond_every_length(window):
+    """As no window at all, where rows stand before the first token too."""
+    for seqs in ([(0, 3), (2, 9), (10, 200), (0, 150), (300, 1)], [(2, 3), (0, 1), (50, 4)]):
+        c = Case(seqs, 8, 2, 64, 16).gpu()
+        whole = c.run()
+        assert np.array_equal(c.run(window), whole)
+        c.check(window)
