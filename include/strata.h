@@ -452,8 +452,10 @@ typedef struct {
  *   out = sum_j softmax_j(scale * q . k_j) v_j     (statistics and sums in fp32; no token: zeros)
  * Head h reads K/V head h / (n_heads / n_kv_heads). q, out [T, n_heads * head_dim] bf16 (device,
  * 16-byte aligned rows, strides in elements, multiples of 8); rows of no sequence are not written.
- * Any lengths may be mixed in one call. What the cache holds past kv_len is not used, whatever it
- * is. A page index outside [0, n_pages) sets STRATA_DEV_BAD_SLOT and its tokens count as unseen;
+ * Any lengths may be mixed in one call. What the cache holds past kv_len, or before the first token
+ * that a row of the sequence sees through the window, is not used, whatever it is, and the page
+ * table's entries for pages that lie there whole are not looked at: such pages may be given back.
+ * A page index outside [0, n_pages) sets STRATA_DEV_BAD_SLOT and its tokens count as unseen;
  * so does a row range outside [0, T], a length below 0 or above max_kv, or more rows than max_q:
  * they are cut to the limit.
  * flags: STRATA_WS_REUSE (the workspace is zero-filled, or was left by a completed call of this

@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   SeqView sv;
   int p_lo, p_hi;   // positions of the first and last query
   int lo, hi;       // the tokens of the piece
+  int seen_lo = 0;  // first token that a row sees
   auto take = [&](int seq, int head, const SeqView& v) {
     s = seq, h = head, sv = v, rows = v.n * G;
     p_lo = v.len - v.n, p_hi = v.len - 1;
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     if (!find_piece(a, pc)) return;
     take(pc.seq, pc.head, seq_view(a, pc.seq, false));
     const SeqSteps st = seq_steps(a, sv);
+    seen_lo = first_seen(a, sv.len - sv.n);
     lo = (st.first + static_cast<int>(static_cast<int64_t>(st.n) * pc.index / pc.of)) * kAttStep;
     hi = min(sv.len, (st.first + static_cast<int>(static_cast<int64_t>(st.n) * (pc.index + 1) / pc.of)) * kAttStep);
   }
@@ -292,14 +294,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   // of each slot's two tiles: K scale, V scale (negative: the tile lies in a page that does not exist)
   __shared__ float2 s_scale[kAttWarps][kAttSlots][2];
   const uint32_t scale_addr = static_cast<uint32_t>(__cvta_generic_to_shared(&s_scale[warp][0][0]));
-  auto issue = [&](int s, int h, int hi, int j0, int i_slot) {
+  // (tokens lo .. hi - 1 are the ones that a row sees: of the others nothing is looked up or used)
+  auto issue = [&](int s, int h, int lo, int hi, int j0, int i_slot) {
     const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
     const uint32_t slot = ring_addr + i_slot * 2 * KB;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int j = j0 + 16 * u;
       int page = -1;
-      if (j < hi) {
+      if (j < hi && j + 16 > lo) {
         page = input(a, table + (j >> pshift));
         if (page < 0 || page >= a.c.n_pages) {
           if (lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
@@ -315,20 +318,22 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
                                             : make_float2(__ldcg(a.c.k_scales + ph), __ldcg(a.c.v_scales + ph));
       }
       const int64_t base = ((ph << pshift) + (j & pmask)) * kD + lane * 16;
-      const int n = page < 0 ? 0 : hi - j;  // tokens of the tile from here on; past them: zeros
+      const int m = lo - j, n = page < 0 ? 0 : hi - j;  // rows m .. n - 1 of the tile; zeros elsewhere
 #pragma unroll
       for (int i = 0; i < NI / 2; ++i) {
         const int r = lane / PIECES + RPI * i;
         const uint32_t dst = slot + slot_offset<kD>(16 * u + r, lane % PIECES);
-        const int64_t at = r < n ? base + i * 512 : 0;
-        copy16(dst, a.c.k_codes + at, r < n);
-        copy16(dst + KB, a.c.v_codes + at, r < n);
+        const bool on = r >= m && r < n;
+        const int64_t at = on ? base + i * 512 : 0;
+        copy16(dst, a.c.k_codes + at, on);
+        copy16(dst + KB, a.c.v_codes + at, on);
       }
     }
   };
   int j_next = 0, to_copy = 0;
   auto issue_ahead = [&](int i_slot) {
-    issue(ahead.seq, ahead.head, ahead.v.len, (ahead.st.first + ahead.at) * kAttStep, i_slot);
+    issue(ahead.seq, ahead.head, first_seen(a, ahead.v.len - ahead.v.n), ahead.v.len,
+          (ahead.st.first + ahead.at) * kAttStep, i_slot);
     if (--to_copy > 0) ahead.move(a, 1);
   };
   if constexpr (kSolo) {
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     j_next = lo + warp * kAttStep;
 #pragma unroll 1
     for (int i = 0; i < kAttSlots; ++i, j_next += kAttWarps * kAttStep) {
-      if (j_next < hi) issue(s, h, hi, j_next, i);
+      if (j_next < hi) issue(s, h, seen_lo, hi, j_next, i);
       cp_async_commit();
     }
   }
@@ -732,7 +737,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       __syncwarp();
       step(j0, i_slot);
       __syncwarp();  // every lane has read the slot
-      if (j_next < hi) issue(s, h, hi, j_next, i_slot);
+      if (j_next < hi) issue(s, h, seen_lo, hi, j_next, i_slot);
       cp_async_commit();
       i_slot = i_slot + 1 == kAttSlots ? 0 : i_slot + 1;
     }

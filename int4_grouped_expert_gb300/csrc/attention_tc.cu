@@ -148,7 +148,7 @@ __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
 struct Unit {
   int seq, head, row0, rows;  // first row; rows of the (sequence, head)
   SeqView sv;
-  int tok_hi, j_lo, n_tiles, of;
+  int tok_lo, tok_hi, j_lo, n_tiles, of;  // tokens tok_lo .. tok_hi - 1
 };
 __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int seq, int head, int row0, int k, int per, bool flag) {
   Unit u;
@@ -157,9 +157,9 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int seq, int head, in
   u.rows = u.sv.n * a.group;
   const int p0 = u.sv.len - u.sv.n;  // position of the first query
   u.tok_hi = min(u.sv.len, p0 + (min(row0 + a.tc_rows, u.rows) - 1) / a.group + 1);
-  const int tok_lo = first_seen(a, p0 + row0 / a.group);
-  u.j_lo = tok_lo / kAtTok;
-  u.n_tiles = u.tok_hi > tok_lo ? (u.tok_hi + kAtTok - 1) / kAtTok - u.j_lo : 0;
+  u.tok_lo = first_seen(a, p0 + row0 / a.group);
+  u.j_lo = u.tok_lo / kAtTok;
+  u.n_tiles = u.tok_hi > u.tok_lo ? (u.tok_hi + kAtTok - 1) / kAtTok - u.j_lo : 0;
   u.of = min(k, max(1, (u.n_tiles + per - 1) / per));
   return u;
 }
@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   const int h = u.head, s = u.seq, row0 = u.row0, rows = u.rows, of = u.of;
   const SeqView sv = u.sv;
   const int G = a.group;
+  const int tok_lo = u.tok_lo;  // before it, and from tok_hi on, nothing is looked up or used
   int j_lo = u.j_lo, n_tiles = u.n_tiles, tok_hi = u.tok_hi;
   if (piece >= of) return;
   if (of > 1) {
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   } else if (warp >= 12) {
     // the largest scales of the pages that are read
     float km = 0.f, vm = 0.f;
-    const int first = j_lo * kAtTok / P, end = (tok_hi + P - 1) / P;
+    const int first = max(tok_lo, j_lo * kAtTok) / P, end = (tok_hi + P - 1) / P;
     for (int i = first + threadIdx.x - 12 * 32; i < end; i += 256) {
       const int64_t page = table[i];
       if (page < 0 || page >= a.c.n_pages) continue;
@@ -551,22 +552,23 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     uint32_t k_gone[2];
     const int pshift = 31 - __clz(P);
     const float k_inv = 1.0f / k_ref, v_inv = 1.0f / v_ref;
-    // page of a token, -1 for one that no row sees; looked up one more tile ahead
-    auto page_of = [&](int tok) { return tok < tok_hi ? table[tok >> pshift] : -1; };
+    // whether a row sees any of the 8 tokens from tok on, and their page (-1 if not); looked up one more tile ahead
+    auto seen = [&](int tok) { return tok < tok_hi && tok + 8 > tok_lo; };
+    auto page_of = [&](int tok) { return seen(tok) ? table[tok >> pshift] : -1; };
     auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
     const int k_tok = j_lo * kAtTok + w * 8, v_tok = j_lo * kAtTok + (w & 1) * 32 + tg * 8;
     int k_page = page_of(k_tok), v_page = page_of(v_tok);
     auto load_k = [&](int j, uint4 (&x)[KC], float& scale, uint32_t& gone) {
       const int tok = k_tok + j * kAtTok;
       const bool on = good(k_page);
-      gone = !on && tok < tok_hi;
+      gone = !on && seen(tok);
       if (gone && lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
       const int64_t ph = on ? static_cast<int64_t>(k_page) * a.c.n_kv_heads + h : 0;
       scale = on ? a.c.k_scales[ph] : 0.f;
       const uint8_t* src = a.c.k_codes + ((ph << pshift) + (tok & (P - 1)) + (lane & 7)) * kD + (lane >> 3) * 16;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
-        x[c] = on && tok + (lane & 7) < tok_hi ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64))
+        x[c] = on && tok + (lane & 7) < tok_hi && tok + (lane & 7) >= tok_lo ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64))
                                                : make_uint4(0u, 0u, 0u, 0u);
       k_page = page_of(tok + kAtTok);
     };
@@ -576,9 +578,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       const int64_t ph = on ? static_cast<int64_t>(v_page) * a.c.n_kv_heads + h : 0;
       scale = on ? a.c.v_scales[ph] : 0.f;
       const uint8_t* src = a.c.v_codes + ((ph << pshift) + (tok & (P - 1))) * kD + (w >> 1) * 32 + dg * 4;
-      const int n = on ? tok_hi - tok : 0;
+      const int m = tok_lo - tok, n = on ? tok_hi - tok : 0;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) x[t] = t < n ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
+      for (int t = 0; t < 8; ++t) x[t] = t >= m && t < n ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
       v_page = page_of(tok + kAtTok);
     };
     auto store_k = [&](uint8_t* dst, const uint4 (&x)[KC], float scale) {
