@@ -160,6 +160,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   constexpr int RPI = kAppThreads / TPR;    // rows per iteration
   constexpr int WARPS = kAppThreads / 32;
   __shared__ int s_len[WARPS];
+  __shared__ unsigned s_holes[WARPS];
   __shared__ float s_max[2][WARPS];
   const int P = a.c.page_size;
   const int slot = a.slots[row0], off = slot % P;
@@ -186,32 +187,42 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   // its first row's cosines (a row with a position out of range is not stored: any table row will do) and the
   // page's scales as well
   Turn t_first = none;
-  int p_first = 0;
   if (a.rot_dim > 0) {
-    p_first = a.positions[min(row0 + ri, a.T - 1)];
-    t_first = turn_at(a, kp, min(static_cast<int64_t>(max(p_first, 0)), a.n_pos - 1));
+    const int r = min(row0 + ri, a.T - 1);
+    t_first = turn_at(a, kp, min(static_cast<int64_t>(max(a.positions[r], 0)), a.n_pos - 1));
   }
   const int64_t ph = page * a.c.n_kv_heads + head;
   const float k_old = off ? a.c.k_scales[ph] : 0.f, v_old = off ? a.c.v_scales[ph] : 0.f;
-  // the run's length: the first row that does not continue it (P <= kAppThreads)
+  // the run's length: the first row that does not continue it (P <= kAppThreads); and its holes
   {
     const int i = threadIdx.x, r = row0 + i;
     const bool in = off + i < P && r < a.T && a.slots[r] == slot + i;
     const unsigned out = __ballot_sync(0xffffffffu, !in);
-    if (lane == 0) s_len[warp] = out ? 32 * warp + __ffs(out) - 1 : kAppThreads;
+    const unsigned holes = __ballot_sync(0xffffffffu, in && row_state(a, r) != 1);
+    if (lane == 0) {
+      s_len[warp] = out ? 32 * warp + __ffs(out) - 1 : kAppThreads;
+      s_holes[warp] = holes;
+    }
   }
   __syncthreads();
-  int n = kAppThreads;
+  constexpr int WORDS = kIter * RPI / 32;  // (a page has at most kIter * RPI rows)
+  int n = kIter * RPI;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) n = min(n, s_len[w]);
+  for (int w = 0; w < WORDS; ++w) n = min(n, s_len[w]);
 
+  bool any = false;  // of n rows, one that is no hole
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w)
+    if (32 * w < n) any |= (~s_holes[w] & (0xffffffffu >> max(0, 32 * w + 32 - n))) != 0;
+  if (!any) {  // nothing changes
+    __syncthreads();
+    return;
+  }
   unsigned skipped = 0;  // bit j: this thread's row of iteration j is past the run, or a hole in it
 #pragma unroll
   for (int j = 0; j < kIter; ++j) {
     const int i = j * RPI + ri;
-    bool on = i < n;
-    if (on && a.rot_dim > 0) on = in_table(a, j == 0 ? p_first : a.positions[row0 + i]);
-    if (on) continue;
+    if (i < n && !(s_holes[i >> 5] >> (i & 31) & 1u)) continue;
     skipped |= 1u << j;
     kw[j][0] = kw[j][1] = vw[j][0] = vw[j][1] = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -242,8 +253,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     s_max[0][warp] = km;
     s_max[1][warp] = vm;
   }
-  // a run of holes changes nothing (kIter bits: all of this thread's rows)
-  if (!__syncthreads_or(skipped != (1u << kIter) - 1u)) return;
+  __syncthreads();
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     km = fmaxf(km, s_max[0][w]);
