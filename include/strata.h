@@ -397,7 +397,7 @@ typedef struct {
   int64_t n_pages;    /* n_pages * page_size <= 2^31 - 1 */
   uint8_t* k_codes;   /* [n_pages, n_kv_heads, page_size, head_dim] e4m3, 16-byte aligned */
   uint8_t* v_codes;   /* the same */
-  float* k_scales;    /* [n_pages, n_kv_heads] */
+  float* k_scales;    /* [n_pages, n_kv_heads], positive */
   float* v_scales;    /* the same */
 } strata_kv_cache;
 
@@ -450,6 +450,10 @@ typedef struct {
  * query rows and kv_len = L stands at position p = L - n + i and sees tokens j <= p, and
  * j > p - window when window > 0:
  *   out = sum_j softmax_j(scale * q . k_j) v_j     (statistics and sums in fp32; no token: zeros)
+ * A token's weight times its page's V scale enters the sum of values in f16, relative to the row's
+ * largest: rounded to 2^-11 of itself, or to 2^-25 of that largest one. Codes, queries (f16 times a
+ * power of two a row, exact but for entries 2^-17 below the row's largest) and page scales are used
+ * as they are, however far apart the scales of pages lie; V scales below 2^-100 count as 2^-100.
  * Head h reads K/V head h / (n_heads / n_kv_heads). q, out [T, n_heads * head_dim] bf16 (device,
  * 16-byte aligned rows, strides in elements, multiples of 8); rows of no sequence are not written.
  * Any lengths may be mixed in one call. What the cache holds past kv_len, or before the first token

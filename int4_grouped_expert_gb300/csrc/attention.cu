@@ -10,11 +10,10 @@
 // is free, so a lane takes 16 consecutive bytes of a K row; V bytes are paired token by token with
 // PRMT, and the weights turn from S^T's layout to P^T's with movmatrix.
 //
-// Queries are f16, exact from bf16 (rows are held times a power of two); weights are f16 (2^-11); sums,
-// statistics and scales are fp32. The reference that is subtracted in the exponent moves only when a
-// score exceeds it by 2^8: weights up to 2^8 are as exact in f16 and the sums fp32, and the common step
-// needs no reduction across lanes and no rescaling of O. A page's V scale, relative to the largest
-// that the warp has met, multiplies the weights.
+// Queries are f16, exact from bf16 (rows are held times a power of two); weights, with the page's V scale in their
+// exponent (attention.cuh), are f16 (2^-11); sums, statistics and scales are fp32. The reference that is
+// subtracted in the exponent moves only when one exceeds it by 8: weights up to 2^8 are as exact in f16 and the
+// sums fp32, and the common step needs no reduction across lanes and no rescaling of O.
 //
 // The work is cut by the lengths that the call finds on the device, in one of two ways.
 // Up to 228 pairs of (sequence, K/V head): a pair whose steps exceed an even share of all steps is cut into
@@ -355,8 +354,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   // ---- the queries of column g of each tile as f16 B fragments, times 2^-e
   uint32_t qf[kNT][4 * KW][2];
   float cmul[kNT][2];   // columns 2t, 2t+1: what turns a product into the exponent of 2
-  int pos[kNT][2];      // their positions
+  uint32_t after;       // their positions after p_lo, a byte each (at most 16 rows)
   auto load_queries = [&] {
+    after = 0;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       const int r = n * 8 + g;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         cmul[n][i] = __shfl_sync(0xffffffffu, m, (2 * t + i) * 4);
-        pos[n][i] = sv.len - sv.n + (n * 8 + 2 * t + i) / G;
+        after |= static_cast<uint32_t>((n * 8 + 2 * t + i) / G) << (16 * n + 8 * i);
       }
     }
   };
@@ -395,9 +395,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   float o[kNT][NJ][4];
   // ref: the reference in use, or 0 before any score; limit: how much of a score above it moves it
   float ref[kNT][2], limit[kNT][2], sum[kNT][2];
-  float v_ref, v_inv;  // largest V scale met, and its inverse
   auto reset = [&] {
-    v_ref = 1.17549435e-38f, v_inv = 8.50705917e37f;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       ref[n][0] = ref[n][1] = 0.f;
@@ -423,7 +421,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   auto step = [&](int j0, int i_slot) {
     const uint8_t* slot = ring + i_slot * 2 * KB;
     const float2 sc0 = s_scale[warp][i_slot][0], sc1 = s_scale[warp][i_slot][1];
-    const float k_scale[2] = {sc0.x, sc1.x}, v_scale[2] = {fmaxf(sc0.y, 0.f), fmaxf(sc1.y, 0.f)};
+    const float k_scale[2] = {sc0.x, sc1.x}, lv[2] = {log2_scale(sc0.y), log2_scale(sc1.y)};
     const int lost = (sc0.y < 0.f ? 1 : 0) | (sc1.y < 0.f ? 2 : 0);
     // S^T: tokens tok_g, tok_g + 8 of each tile x columns 2t, 2t+1
     float sc[kNT][2][4];
@@ -464,13 +462,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float f = cmul[n][c] * k_scale[u];
+          const float f = cmul[n][c] * k_scale[u], base = lv[u] - ref[n][c];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = fmaf(sc[n][u][2 * i + c], f, -ref[n][c]);
+            float x = fmaf(sc[n][u][2 * i + c], f, base);
             if (!whole) {
               const int r = tok_g + 8 * i, j = j0 + 16 * u + r;
-              const bool seen = j < hi && j <= pos[n][c] && (a.window <= 0 || j > pos[n][c] - a.window) &&
+              const int pos = p_lo + static_cast<int>(after >> (16 * n + 8 * c) & 255u);
+              const bool seen = j < hi && j <= pos && (a.window <= 0 || j > pos - a.window) &&
                                 !(lost >> u & 1);
               if (!seen) x = -INFINITY;
             }
@@ -479,7 +478,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
           }
         }
       }
-    if (__any_sync(0xffffffffu, over)) {  // some column's reference moves to its largest score so far
+    if (__any_sync(0xffffffffu, over)) {  // some column's reference moves to its largest exponent so far
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -507,31 +506,26 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
           }
         }
     }
-    // O^T += vs * V^T P^T, tile by tile (the scale is the page's)
+    // O^T += V^T P^T, tile by tile (the scale is the page's)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      if (v_scale[u] > v_ref) {
-        const float f = v_ref / v_scale[u];
-        v_ref = v_scale[u];
-        v_inv = 1.0f / v_ref;
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
-      }
-      const float vf = v_scale[u] * v_inv;
       uint32_t pf[kNT][2];
+      const float per_scale = exp2_approx(-lv[u]);
+      const bool small = lv[u] < kSmallScale;
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         float p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = exp2_approx(sc[n][u][i]);
-        sum[n][0] += p[0] + p[2];
-        sum[n][1] += p[1] + p[3];
-        pf[n][0] = movm_trans(pack_f16x2(p[0] * vf, p[1] * vf));
-        pf[n][1] = movm_trans(pack_f16x2(p[2] * vf, p[3] * vf));
+        if (!small) {
+          sum[n][0] = fmaf(p[0] + p[2], per_scale, sum[n][0]);
+          sum[n][1] = fmaf(p[1] + p[3], per_scale, sum[n][1]);
+        } else {
+          sum[n][0] += exp2_approx(sc[n][u][0] - lv[u]) + exp2_approx(sc[n][u][2] - lv[u]);
+          sum[n][1] += exp2_approx(sc[n][u][1] - lv[u]) + exp2_approx(sc[n][u][3] - lv[u]);
+        }
+        pf[n][0] = movm_trans(pack_f16x2(p[0], p[1]));
+        pf[n][1] = movm_trans(pack_f16x2(p[2], p[3]));
       }
       uint32_t vr[4][VW];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the MMA's order
 #pragma unroll
@@ -707,7 +701,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
         for (int c = 0; c < 2; ++c) {
           const int col = n * 8 + 2 * t + c;
           const float l = column_sum(n, c);
-          const float f = whole ? (l == 0.f ? 0.f : 1.0f / l) * v_ref : v_ref;
+          const float f = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
           if (col < rows) {
 #pragma unroll
             for (int j = 0; j < NJ; j += 2) {
@@ -766,7 +760,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
-        const float f = (top == -INFINITY ? 1.f : exp2_approx(s_ref[warp][col] - top)) * v_ref;
+        const float f = top == -INFINITY ? 1.f : exp2_approx(s_ref[warp][col] - top);
         float* dst = s_o + (warp * COLS + col) * OS + g * (4 * VW);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)

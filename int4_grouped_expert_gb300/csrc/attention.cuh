@@ -22,6 +22,22 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// How both kernels use a page's scales: the K scale multiplies the scores, in fp32, and the V scale goes into the
+// exponent, so that a token's weight in the product with the V codes (exact in f16) is
+//   w = 2^(score + log2(V scale) - ref),   ref a running reference of these exponents, per row,
+// rounded to f16: 2^-11 of itself, or 2^-25 of the row's largest once it is below 2^-14 of that. The sum of the softmax
+// takes w / V scale in fp32 and has the same reference, so output = (sum of w code) / (sum of w / V scale). A page
+// that a row does not see, or whose tokens weigh little, changes nothing for the others, however large its scales are.
+// Scales are positive; V scales below 2^-100, the least that the append writes, count as 2^-100.
+__device__ __forceinline__ float log2_scale(float s) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s < 7.88860905e-31f ? 7.88860905e-31f : s));
+  return y;
+}
+// Below this log2(V scale) w may be flushed to zero (2^-126) though its part in the sum is not negligible: there the sum
+// takes 2^(score - ref) instead. (Pages of zeros have such scales.)
+constexpr float kSmallScale = -24.f;
+
 // The rows and tokens of one sequence, cut to the call's limits.
 struct SeqView {
   int q0, n;  // first row, rows

@@ -10,13 +10,14 @@
 // needed 2048.)
 //   warps 0, 1     an elected lane issues the MMAs of row tile 0, 1
 //   warp 2         owns the TMEM allocation: the score buffers (4 x 64 columns), O_0, O_1 (head_dim each)
+//   warp 3         looks up the pages' scales, many tiles ahead, and lays out a tile's with its stage
 //   warps 4-11     softmax, one thread per row: running reference and sum in fp32. O is rescaled only when
 //                  a score has grown by more than 2^8 over the reference (weights up to 2^8 are as exact
 //                  in f16 and the sums fp32), which after the first tiles is rare
 //   warps 12-19    codes -> f16 tiles in shared memory, K as it lies and V transposed (bytes of two
 //                  tokens paired with PRMT), a ring of 4 stages: (K0, K1), (V0, K2), (V1, K3), ...
-// A page's scale relative to the largest of the block's pages multiplies its codes on the way: exact for
-// powers of two down to 2^-15, absolute error below 2^-25 of the largest scale beyond.
+// Codes are f16 as they are, exactly; a page's scales, one pair for every 16 tokens of a tile, go to the softmax
+// (attention.cuh).
 // Queries become f16 with a power of two per row; a token that no row sees or in a page that does not
 // exist becomes zeros and a masked score, so what lies there does not matter.
 //
@@ -37,7 +38,7 @@ namespace {
 constexpr int kAtTok = 64;      // tokens per tile
 constexpr int kAtRing = 4;      // stages of two tiles of codes converted to f16
 constexpr int kAtThreads = 640;
-constexpr int kAtBad = 8;       // ring of per-tile masks of tokens in pages that do not exist
+constexpr int kAtScales = 8;    // tiles whose scales are in shared memory
 constexpr int kAtSms = 152;     // blocks that run at once
 constexpr int kAtMaxSlots = 3 * kAtSms;
 constexpr int kAtMinTiles = 4;  // tiles that a piece has at least
@@ -56,12 +57,6 @@ struct AtCfg {
   static constexpr int TILE = kAtTok * kD * 2; // of a tile of K or V
   static constexpr size_t SMEM = 2 * QTILE + static_cast<size_t>(kAtRing) * 2 * TILE + 1024 + 512;
 };
-
-__device__ __forceinline__ uint32_t scaled_codes(uint32_t two, __half2 s) {
-  const uint32_t v = e4m3x2_f16x2(two);
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), s);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // Two fp32 values as one operand of the packed fp32 instructions.
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
@@ -181,7 +176,16 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Units& us, in
                  false);
 }
 
-template <int kD>
+// The largest of 16 scores.
+__device__ __forceinline__ float max16(const uint32_t* x) {
+  float t = __uint_as_float(x[0]);
+#pragma unroll
+  for (int i = 1; i < 15; i += 2) t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+  return fmaxf(t, __uint_as_float(x[15]));
+}
+
+// kGroups: pairs of scales in a tile, 1 where it lies in one page (of 64 or 128 tokens), else one for every 16 tokens.
+template <int kD, int kGroups>
 __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a) {
   using C = AtCfg<kD>;
   constexpr int KC = kD / 64;   // 64-wide pieces of a head
@@ -196,10 +200,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   uint64_t* p_full = s_full + 4;          // [row tile][buffer]
   uint64_t* pv_done = p_full + 4;         // [row tile][buffer]
   uint64_t* drain = pv_done + 4;
-  uint64_t* bad = drain + 2;              // [kAtBad], a byte per 8 tokens
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bad + kAtBad);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   __shared__ int abort_flag_s;
-  __shared__ float s_ref[2][8];
+  // of each group: K scale, log2 of the V scale, the inverse V scale (0 below kSmallScale), and whether all is well (0),
+  // the page does not exist (1), has a scale of inf or nan (2: nan for the rows that see it) or a small V scale (3)
+  __shared__ float4 s_scale[kAtScales][kGroups];
+  __shared__ volatile int s_any_small;  // a tile so far has a page of a small V scale
   __shared__ volatile int s_end[6];  // what is wanted again at the end only: not kept in registers
   volatile int* abort_flag = &abort_flag_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kAtRing; ++i) {
-      tc::mbar_init(kv_full + i, 8);
+      tc::mbar_init(kv_full + i, 9);        // the conversion warps and the one of the scales
       tc::mbar_init(kv_empty + i, n_rt);  // each row tile's MMAs
     }
     for (int i = 0; i < 2; ++i) {
@@ -267,6 +273,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     }
     tc::fence_barrier_init();
     abort_flag_s = 0;
+    s_any_small = 0;
     s_end[0] = of > 1;
     s_end[1] = cut;  // (a unit's pieces have k slots, from its first block's number on)
     s_end[2] = sv.q0;
@@ -304,35 +311,34 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
           make_uint4(o[0], o[1], o[2], o[3]);
     }
     tc::fence_proxy_async_smem();
-  } else if (warp >= 12) {
-    // the largest scales of the pages that are read
-    float km = 0.f, vm = 0.f;
-    const int first = max(tok_lo, j_lo * kAtTok) / P, end = (tok_hi + P - 1) / P;
-    for (int i = first + threadIdx.x - 12 * 32; i < end; i += 256) {
-      const int64_t page = table[i];
-      if (page < 0 || page >= a.c.n_pages) continue;
-      km = fmaxf(km, a.c.k_scales[page * a.c.n_kv_heads + h]);
-      vm = fmaxf(vm, a.c.v_scales[page * a.c.n_kv_heads + h]);
-    }
-    km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(km)));
-    vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
-    if (lane == 0) {
-      s_ref[0][warp - 12] = km;
-      s_ref[1][warp - 12] = vm;
-    }
   }
-  tc::tc_fence_before();
-  __syncthreads();
-  tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  float k_ref = 0.f, v_ref = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    k_ref = fmaxf(k_ref, s_ref[0][i]);
-    v_ref = fmaxf(v_ref, s_ref[1][i]);
+  // the scales of a tile's groups: a lane a group, of kBatch tiles
+  constexpr int kBatch = 32 / kGroups, kWide = kAtTok / kGroups;
+  auto scales_of = [&](int batch) {
+    const int t = batch * kBatch + lane / kGroups, tok = (j_lo + t) * kAtTok + lane % kGroups * kWide;
+    float3 x = make_float3(0.f, 1.f, 0.f);
+    if (t < n_tiles && tok < tok_hi && tok + kWide > tok_lo) {
+      const int64_t page = table[tok >> (31 - __clz(P))];
+      if (page >= 0 && page < a.c.n_pages) {
+        x.x = a.c.k_scales[page * a.c.n_kv_heads + h];
+        x.y = a.c.v_scales[page * a.c.n_kv_heads + h];
+      } else {
+        set_status(a.status, STRATA_DEV_BAD_SLOT);
+        x.z = 1.f;
+      }
+    }
+    return x;
+  };
+  float3 scales_now = {}, scales_next = {};
+  if (warp == 3) scales_now = scales_of(0), scales_next = scales_of(1);
+  // (the conversion warps start their first copies before they come to this barrier)
+  uint32_t tmem = 0;
+  if (warp < 12) {
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    tmem = *tmem_slot;
   }
-  if (k_ref == 0.f) k_ref = 1.f;
-  if (v_ref == 0.f) v_ref = 1.f;
 
   // registers: 5 warpgroups are launched with 96 a thread (61440 in all) and go on with
   // 48 + 2 * 120 + 2 * 96 (the same)
@@ -404,6 +410,32 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         __syncwarp();
         tc::mbar_wait_drain(drain + i, 0);
       }
+    } else if (warp == 3) {
+      // -------------------------------------------------------------- scales
+      int batch = 0;
+      float3 now = scales_now, next = scales_next;
+      auto lay_out = [&](int t) {
+        if (t >= n_tiles) return;
+        if (t / kBatch > batch) {
+          now = next;
+          next = scales_of(++batch + 1);
+        }
+        const bool fine = now.x < INFINITY && now.y < INFINITY;
+        const float lv = fine ? log2_scale(now.y) : 0.f;
+        const bool small = lv < kSmallScale;
+        if (lane / kGroups == t % kBatch) {
+          s_scale[t % kAtScales][lane % kGroups] =
+              make_float4(fine ? now.x : 1.f, lv, small ? 0.f : exp2_approx(-lv), !fine ? 2.f : small ? 3.f : now.z);
+          if (small) s_any_small = 1;
+        }
+      };
+      for (int t = 0; t <= n_tiles; ++t) {  // stage t
+        if (!tc::warp_wait(kv_empty + t % kAtRing, ((t / kAtRing) & 1) ^ 1, abort_flag, a.status)) break;
+        if (t == 0) lay_out(0);
+        lay_out(t + 1);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(kv_full + t % kAtRing);
+      }
     }
     __syncwarp();
   } else if (warp < 12) {
@@ -413,8 +445,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t to = tmem + 256 + tile * 128 + lanes;
     const int pos = sv.len - sv.n + row / G;
-    cmul = fmaxf(cmul * k_ref, 1.17549435e-38f);  // (never 0: a masked score, -inf, stays -inf under it)
     float m = -INFINITY, l = 0.f;
+    // The sum over pages of small scales has a reference of its own, the largest of their scores. (In local memory:
+    // registers are short, and 2 KB more of shared memory would leave L1 28 KB instead of 60: 241 us became 314.)
+    volatile float small_top = -INFINITY, small_sum = 0.f;
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
       const uint32_t ts = tmem + tile * 128 + (j & 1) * 64 + lanes;
@@ -424,8 +458,35 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       const int j0 = (j_lo + j) * kAtTok;
       // columns lo .. hi of the tile are seen
       const int hi = min(pos, tok_hi - 1) - j0, lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
-      const unsigned long long gone = bad[j % kAtBad];
-      const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && lo <= 0) && gone == 0;
+      const float4* scale = s_scale[j % kAtScales];
+      // what turns a product into the exponent of 2 (never 0: a masked score, -inf, stays -inf under it)
+      float cg[kGroups], lv[kGroups], per_scale;
+      bool well = true;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float4 s = scale[g];
+        cg[g] = fmaxf(cmul * s.x, 1.17549435e-38f);
+        lv[g] = s.y;
+        per_scale = s.z;  // (of several groups: looked up again, for want of registers)
+        well = well && s.w == 0.f;
+      }
+      const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && lo <= 0 && well);
+      const bool odd = !whole && !__all_sync(0xffffffffu, well);
+      if (odd) {
+        float top = small_top, sum = small_sum;
+#pragma unroll 1
+        for (int c = 0; c < kAtTok; ++c) {  // (short code: it is rarely run)
+          const float4 sc = scale[c * kGroups / kAtTok];
+          const float score = __uint_as_float(tc::tmem_ld1(ts + c));
+          const bool on = sc.y < kSmallScale && c <= hi && c >= lo;
+          const float x = on ? score * fmaxf(cmul * sc.x, 1.17549435e-38f) : -INFINITY, before = top;
+          top = fmaxf(top, x);
+          const float ref = top == -INFINITY ? 0.f : top;
+          sum = fmaf(sum, exp2_approx(before - ref), exp2_approx(x - ref));
+          __syncwarp();
+        }
+        small_top = top, small_sum = sum;
+      }
       uint32_t r[2][32];
       tc::tmem_ld32(ts, r[0]);
       tc::tmem_ld32(ts + 32, r[1]);
@@ -433,18 +494,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < kAtTok; ++i) {
-          const bool seen = i <= hi && i >= lo && !((gone >> (i / 8 * 8)) & 1);
+          const bool seen = i <= hi && i >= lo;
           r[i / 32][i % 32] = seen ? r[i / 32][i % 32] : 0xFF800000u;  // -inf
         }
       }
-      float t0 = __uint_as_float(r[0][0]), t1 = __uint_as_float(r[1][0]);
+      if (odd) {
 #pragma unroll
-      for (int i = 1; i < 31; i += 2) {
-        t0 = max3(t0, __uint_as_float(r[0][i]), __uint_as_float(r[0][i + 1]));
-        t1 = max3(t1, __uint_as_float(r[1][i]), __uint_as_float(r[1][i + 1]));
+        for (int i = 0; i < kAtTok; ++i) {
+          const float state = scale[i * kGroups / kAtTok].w;
+          if (state == 1.f) r[i / 32][i % 32] = 0xFF800000u;
+          if (state == 2.f && i <= hi && i >= lo) r[i / 32][i % 32] = 0x7FC00000u;  // nan
+        }
       }
-      t0 = max3(t0, t1, __uint_as_float(r[0][31]));
-      const float top = fmaxf(t0, __uint_as_float(r[1][31])) * cmul;
+      const float t[4] = {max16(r[0]), max16(r[0] + 16), max16(r[1]), max16(r[1] + 16)};
+      const float top = kGroups == 1 ? fmaf(fmaxf(max3(t[0], t[1], t[2]), t[3]), cg[0], lv[0])
+                                     : fmaxf(max3(fmaf(t[0], cg[0], lv[0]),
+                                                  fmaf(t[1], cg[1 % kGroups], lv[1 % kGroups]),
+                                                  fmaf(t[2], cg[2 % kGroups], lv[2 % kGroups])),
+                                             fmaf(t[3], cg[3 % kGroups], lv[3 % kGroups]));
       if (__any_sync(0xffffffffu, top > m + 8.f)) {
         const float now = fmaxf(m, top);
         const float f = now == -INFINITY ? 1.f : exp2_approx(m - now);
@@ -467,25 +534,30 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         }
       }
       const float ref = m == -INFINITY ? 0.f : m;
-      const uint64_t cc = pack_f32x2(cmul, cmul), mm = pack_f32x2(-ref, -ref);
-      uint64_t sum0 = 0, sum1 = 0;  // (two zeros)
+      uint64_t sum[4] = {0, 0, 0, 0};  // (pairs of zeros) of 16 columns each
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
+          const int g = (2 * q + i / 8) % kGroups;
+          const uint64_t cc = pack_f32x2(cg[g], cg[g]), mm = pack_f32x2(lv[g] - ref, lv[g] - ref);
           const uint64_t x = pack_f32x2(__uint_as_float(r[q][2 * i]), __uint_as_float(r[q][2 * i + 1]));
           float2 e = unpack_f32x2(fma_f32x2(x, cc, mm));
           e.x = exp2_approx(e.x);
           e.y = exp2_approx(e.y);
-          if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(e.x, e.y));
-          else sum0 = add_f32x2(sum0, pack_f32x2(e.x, e.y));
+          uint64_t& s = sum[kGroups == 1 ? i & 1 : 2 * q + i / 8];
+          s = add_f32x2(s, pack_f32x2(e.x, e.y));
           p[i] = pack_f16x2(e.x, e.y);
         }
         tc::tmem_st16(ts + 32 + 16 * q, p);  // f16 pairs, over scores that this thread has read
       }
-      const float2 sums = unpack_f32x2(add_f32x2(sum0, sum1));
-      l += sums.x + sums.y;
+      if constexpr (kGroups == 1) sum[0] = add_f32x2(sum[0], sum[1]);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float2 s = unpack_f32x2(sum[g]);
+        l = fmaf(s.x + s.y, kGroups == 1 ? per_scale : scale[g].z, l);
+      }
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -494,6 +566,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     if (ok) {
       ok = done(tile, n_tiles - 1);
       tc::tc_fence_after();
+    }
+    if (s_any_small) {  // (m is finite where top is)
+      const float top = small_top, sum = small_sum;
+      if (top != -INFINITY || sum != 0.f) l += sum * exp2_approx(top - (m == -INFINITY ? 0.f : m));
     }
     const int q0 = s_end[2], rows = s_end[3], h = s_end[5];
     const int row = s_end[4] + tile * 128 + (warp & 3) * 32 + lane;
@@ -509,12 +585,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4*>(slot + (c / 4 + i) * 1024 + r0 * 4) =
-              make_float4(__uint_as_float(x[4 * i]) * v_ref, __uint_as_float(x[4 * i + 1]) * v_ref,
-                          __uint_as_float(x[4 * i + 2]) * v_ref, __uint_as_float(x[4 * i + 3]) * v_ref);
+              make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]), __uint_as_float(x[4 * i + 2]),
+                          __uint_as_float(x[4 * i + 3]));
       }
       *reinterpret_cast<float2*>(slot + 256 * kD + 2 * r0) = make_float2(m, l);
     } else if (ok) {
-      const float inv = l == 0.f ? 0.f : v_ref / l;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
       uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(q0 + row / G) * a.out_stride +
                                             (h * G + row % G) * kD);
 #pragma unroll 1
@@ -545,47 +621,42 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     // lanes store to eight different 16-byte columns of the swizzled rows
     const bool v_on = w < 2 * kD / 32;               // (64-wide heads have 4 pieces)
     const int tg = lane & 3, dg = ((lane >> 2) & 1) | (lane >> 3) << 1;
-    // codes and scales of the tiles j (even) and j (odd), on their way two tiles ahead
+    // codes of the tiles j (even) and j (odd), on their way two tiles ahead
     uint4 kr[2][KC];
     uint32_t vr[2][8];
-    float k_scale[2], v_scale[2];
-    uint32_t k_gone[2];
     const int pshift = 31 - __clz(P);
-    const float k_inv = 1.0f / k_ref, v_inv = 1.0f / v_ref;
-    // whether a row sees any of the 8 tokens from tok on, and their page (-1 if not); looked up one more tile ahead
-    auto seen = [&](int tok) { return tok < tok_hi && tok + 8 > tok_lo; };
+    // whether a row sees any token of the group that tok is in, and their page (-1 if not); looked up one more
+    // tile ahead
+    constexpr int kLast = kAtTok / kGroups - 1;
+    const int lo_g = tok_lo & ~kLast, n_g = ((tok_hi - 1) | kLast) + 1 - lo_g;
+    auto seen = [&](int tok) { return static_cast<unsigned>(tok - lo_g) < static_cast<unsigned>(n_g); };
     auto page_of = [&](int tok) { return seen(tok) ? table[tok >> pshift] : -1; };
+    auto in_span = [&](int tok) { return tok < tok_hi && tok >= tok_lo; };
     auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
     const int k_tok = j_lo * kAtTok + w * 8, v_tok = j_lo * kAtTok + (w & 1) * 32 + tg * 8;
     int k_page = page_of(k_tok), v_page = page_of(v_tok);
-    auto load_k = [&](int j, uint4 (&x)[KC], float& scale, uint32_t& gone) {
+    auto load_k = [&](int j, uint4 (&x)[KC]) {
       const int tok = k_tok + j * kAtTok;
       const bool on = good(k_page);
-      gone = !on && seen(tok);
-      if (gone && lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
       const int64_t ph = on ? static_cast<int64_t>(k_page) * a.c.n_kv_heads + h : 0;
-      scale = on ? a.c.k_scales[ph] : 0.f;
       const uint8_t* src = a.c.k_codes + ((ph << pshift) + (tok & (P - 1)) + (lane & 7)) * kD + (lane >> 3) * 16;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
-        x[c] = on && tok + (lane & 7) < tok_hi && tok + (lane & 7) >= tok_lo ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64))
+        x[c] = on && in_span(tok + (lane & 7)) ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64))
                                                : make_uint4(0u, 0u, 0u, 0u);
       k_page = page_of(tok + kAtTok);
     };
-    auto load_v = [&](int j, uint32_t (&x)[8], float& scale) {
+    auto load_v = [&](int j, uint32_t (&x)[8]) {
       const int tok = v_tok + j * kAtTok;
       const bool on = good(v_page) && v_on;
       const int64_t ph = on ? static_cast<int64_t>(v_page) * a.c.n_kv_heads + h : 0;
-      scale = on ? a.c.v_scales[ph] : 0.f;
       const uint8_t* src = a.c.v_codes + ((ph << pshift) + (tok & (P - 1))) * kD + (w >> 1) * 32 + dg * 4;
-      const int m = tok_lo - tok, n = on ? tok_hi - tok : 0;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) x[t] = t >= m && t < n ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
+      for (int t = 0; t < 8; ++t)
+        x[t] = on && in_span(tok + t) ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
       v_page = page_of(tok + kAtTok);
     };
-    auto store_k = [&](uint8_t* dst, const uint4 (&x)[KC], float scale) {
-      const float r = scale * k_inv;
-      const __half2 s2 = __floats2half2_rn(r, r);
+    auto store_k = [&](uint8_t* dst, const uint4 (&x)[KC]) {
       uint8_t* rowp = dst + (w * 8 + (lane & 7)) * 128;
       const int ch = 2 * (lane >> 3);
 #pragma unroll
@@ -594,23 +665,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
           *reinterpret_cast<uint4*>(rowp + c * (kAtTok * 128) + (((ch + b) ^ (lane & 7)) << 4)) =
-              make_uint4(scaled_codes(y[2 * b], s2), scaled_codes(y[2 * b] >> 16, s2), scaled_codes(y[2 * b + 1], s2),
-                         scaled_codes(y[2 * b + 1] >> 16, s2));
+              make_uint4(e4m3x2_f16x2(y[2 * b]), e4m3x2_f16x2(y[2 * b] >> 16), e4m3x2_f16x2(y[2 * b + 1]),
+                         e4m3x2_f16x2(y[2 * b + 1] >> 16));
       }
     };
-    auto store_v = [&](uint8_t* dst, const uint32_t (&x)[8], float scale) {
+    auto store_v = [&](uint8_t* dst, const uint32_t (&x)[8]) {
       if (!v_on) return;
-      const float r = scale * v_inv;
-      const __half2 s2 = __floats2half2_rn(r, r);
       const int ch = (w & 1) * 4 + tg;  // 8-token column
       uint32_t o[4][4];                 // [element][token pair]
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const uint32_t y = prmt(x[2 * t], x[2 * t + 1], 0x5140), z = prmt(x[2 * t], x[2 * t + 1], 0x7362);
-        o[0][t] = scaled_codes(y, s2);
-        o[1][t] = scaled_codes(y >> 16, s2);
-        o[2][t] = scaled_codes(z, s2);
-        o[3][t] = scaled_codes(z >> 16, s2);
+        o[0][t] = e4m3x2_f16x2(y);
+        o[1][t] = e4m3x2_f16x2(y >> 16);
+        o[2][t] = e4m3x2_f16x2(z);
+        o[3][t] = e4m3x2_f16x2(z >> 16);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -629,36 +698,33 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(kv_full + t % kAtRing);
     };
-    auto put_k = [&](int j, uint8_t* dst, const uint4 (&x)[KC], float scale, uint32_t gone) {
-      if (lane == 0) reinterpret_cast<volatile uint8_t*>(bad + j % kAtBad)[w] = static_cast<uint8_t>(gone);
-      store_k(dst, x, scale);
-    };
     // stage j + 1: V_j and K_(j+2); then the codes of V_(j+2) and K_(j+4) start
-    auto put = [&](int j, uint32_t (&xv)[8], float& sv_, uint4 (&xk)[KC], float& sk, uint32_t& gone) {
+    auto put = [&](int j, uint32_t (&xv)[8], uint4 (&xk)[KC]) {
       if (j >= n_tiles || !ok) return;
       uint8_t* dst = begin(j + 1);
       if (!ok) return;
-      store_v(dst, xv, sv_);
-      if (j + 2 < n_tiles) put_k(j + 2, dst + C::TILE, xk, sk, gone);
+      store_v(dst, xv);
+      if (j + 2 < n_tiles) store_k(dst + C::TILE, xk);
       end(j + 1);
-      if (j + 2 < n_tiles) load_v(j + 2, xv, sv_);
-      if (j + 4 < n_tiles) load_k(j + 4, xk, sk, gone);
+      if (j + 2 < n_tiles) load_v(j + 2, xv);
+      if (j + 4 < n_tiles) load_k(j + 4, xk);
     };
-    load_k(0, kr[0], k_scale[0], k_gone[0]);
-    load_k(1, kr[1], k_scale[1], k_gone[1]);
-    load_v(0, vr[0], v_scale[0]);
-    load_v(1, vr[1], v_scale[1]);
+    load_k(0, kr[0]);
+    load_k(1, kr[1]);
+    load_v(0, vr[0]);
+    load_v(1, vr[1]);
+    __syncthreads();  // the barrier of the other warps above
     uint8_t* dst = begin(0);
     if (ok) {
-      put_k(0, dst, kr[0], k_scale[0], k_gone[0]);
-      put_k(1, dst + C::TILE, kr[1], k_scale[1], k_gone[1]);
+      store_k(dst, kr[0]);
+      store_k(dst + C::TILE, kr[1]);
       end(0);
-      load_k(2, kr[0], k_scale[0], k_gone[0]);
-      load_k(3, kr[1], k_scale[1], k_gone[1]);
+      load_k(2, kr[0]);
+      load_k(3, kr[1]);
     }
     for (int j = 0; ok && j < n_tiles; j += 2) {
-      put(j, vr[0], v_scale[0], kr[0], k_scale[0], k_gone[0]);
-      put(j + 1, vr[1], v_scale[1], kr[1], k_scale[1], k_gone[1]);
+      put(j, vr[0], kr[0]);
+      put(j + 1, vr[1], kr[1]);
     }
   }
   __syncwarp();
@@ -724,13 +790,18 @@ cudaError_t launch_join_t(const AttnArgs& a, int64_t units, cudaStream_t stream)
                        dim3(kAtJoinRows * kD / 8), 0, stream, true, a);
 }
 
-template <int kD>
-cudaError_t launch_tc_t(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int kD, int kGroups>
+cudaError_t launch_tc_g(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<kD, kGroups>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(AtCfg<kD>::SMEM));
   if (e != cudaSuccess) return e;
-  return launch_kernel(attention_tc_kernel<kD>, dim3(static_cast<unsigned>(grid)), dim3(kAtThreads),
+  return launch_kernel(attention_tc_kernel<kD, kGroups>, dim3(static_cast<unsigned>(grid)), dim3(kAtThreads),
                        AtCfg<kD>::SMEM, stream, true, a);
+}
+template <int kD>
+cudaError_t launch_tc_t(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
+  return a.c.page_size >= kAtTok ? launch_tc_g<kD, 1>(a, grid, stream) : launch_tc_g<kD, 4>(a, grid, stream);
 }
 
 }  // namespace
