@@ -87,7 +87,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // The units of a call: tc_rows rows of a (sequence, K/V head), sequence by sequence, those with the most tokens
 // to see first. As many as fill all SMs a whole number of times stay whole; the others, which run last, are
-// cut along the tokens where that ends sooner, into pieces of `per` tiles, at most k. The same in every warp.
+// cut along the tokens where that ends sooner, into pieces of `per` tiles, at most k. The same in every warp, and in
+// the kernel that joins: each product and sum is rounded where it is written, whatever the compiler fuses elsewhere.
 struct Units {
   int whole, rest, k, per;
   int s0, s1, mine, end;  // this lane's sequences, their units, and the units up to there
@@ -106,11 +107,14 @@ __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
     const SeqView v = seq_view(a, s, flag);
     const int n = units_of(a, v);
     // tokens that a unit sees, on average
-    float seen = max(0.f, v.len - 0.5f * v.n);
-    if (a.window > 0) seen = fminf(seen, a.window + static_cast<float>(a.tc_rows) / a.group);
+    float seen = fmaxf(0.f, __fsub_rn(static_cast<float>(v.len), __fmul_rn(0.5f, static_cast<float>(v.n))));
+    if (a.window > 0)
+      seen = fminf(seen, __fadd_rn(static_cast<float>(a.window), __fdiv_rn(static_cast<float>(a.tc_rows),
+                                                                           static_cast<float>(a.group))));
+    const float of_unit = __fadd_rn(__fmul_rn(seen, 1.f / kAtTok), 1.f);
     u.mine += n;
-    tiles += n * (seen / kAtTok + 1.f);
-    if (n > 0) most = fmaxf(most, seen / kAtTok + 1.f);
+    tiles = __fadd_rn(tiles, __fmul_rn(static_cast<float>(n), of_unit));
+    if (n > 0) most = fmaxf(most, of_unit);
   }
   u.end = u.mine;
 #pragma unroll
@@ -119,16 +123,18 @@ __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
     if (lane >= d) u.end += x;
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+  for (int d = 16; d > 0; d >>= 1) tiles = __fadd_rn(tiles, __shfl_xor_sync(0xffffffffu, tiles, d));
   const int all = __shfl_sync(0xffffffffu, u.end, 31);
   u.whole = all / kAtSms * kAtSms, u.rest = all - u.whole;
   u.k = 1;
   most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
   // (units that stay whole decide when a batch of very different lengths ends)
-  if (u.rest > 0 && (u.whole == 0 || most * all <= 1.25f * tiles)) {
+  if (u.rest > 0 &&
+      (u.whole == 0 || __fmul_rn(most, static_cast<float>(all)) <= __fmul_rn(1.25f, tiles))) {
     // lane i weighs i + 1 pieces of the longest units, and in proportion of the others
     const int n = static_cast<int>(most), c = lane + 1;
-    const int pieces = max(u.rest, static_cast<int>(u.rest * c * (tiles / all / most)));
+    const float share = __fdiv_rn(__fdiv_rn(tiles, static_cast<float>(all)), most);
+    const int pieces = max(u.rest, static_cast<int>(__fmul_rn(static_cast<float>(u.rest * c), share)));
     const int rounds = (pieces + kAtSms - 1) / kAtSms;
     int cost = c == 1 ? rounds * (n + 1 + kAtStart) : rounds * (n / c + 1 + kAtPiece) + kAtJoin + c / 2;
     if (c == 1 && u.whole > 0 && u.rest <= kAtMostCut) cost -= cost / 6;
