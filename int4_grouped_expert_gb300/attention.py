@@ -3,12 +3,25 @@
 QuantLinear holds one projection's codes and scales, PagedKVCache the pages of
 8-bit keys and values, kv_batch the lengths and page tables of one call. All hold
 torch tensors (for device memory only) and fill the C structs with their
-addresses; the arithmetic runs in the library.
+addresses; the arithmetic runs in the library, which sees addresses only: element
+types and layouts are checked here.
 """
 from __future__ import annotations
 
 from . import (GROUP, StrataError, check, ptr, strata_kv_batch, strata_kv_cache, strata_linear,
                strata_linear_workspace_size, strata_quantize_groups_bits, strata_read_status)
+
+
+def _held(t, name: str, dtype: str, numel: int):
+    """t: a tensor of `numel` elements that follow one another, of the dtype named ("codes": any of one byte), or an
+    address, which cannot be checked."""
+    if hasattr(t, "dtype"):
+        kind = str(t.dtype).removeprefix("torch.")
+        if t.element_size() != 1 if dtype == "codes" else kind != dtype:
+            raise TypeError(f"{name} holds {kind}, not {'elements of one byte' if dtype == 'codes' else dtype}")
+        if t.numel() != numel or not t.is_contiguous():
+            raise ValueError(f"{name} {tuple(t.shape)} with strides {t.stride()}: {numel} consecutive elements expected")
+    return t
 
 
 class QuantLinear:
@@ -18,6 +31,10 @@ class QuantLinear:
     (from_fp16). bias: fp32 [N] or None."""
 
     def __init__(self, codes, scales, N: int, K: int, bits: int = 4, group: int = GROUP, bias=None):
+        _held(codes, "codes", "codes", N * K * bits // 8)
+        _held(scales, "scales", "float16", N * (K // group))
+        if bias is not None:
+            _held(bias, "bias", "float32", N)
         self.codes, self.scales, self.bias = codes, scales, bias
         self.N, self.K, self.bits, self.group = N, K, bits, group
         s = strata_linear()
@@ -61,15 +78,20 @@ class PagedKVCache:
         self.n_pages, self.n_kv_heads = n_pages, n_kv_heads
         self.head_dim, self.page_size = head_dim, page_size
         shape = (n_pages, n_kv_heads, page_size, head_dim)
+        n_scales = n_pages * n_kv_heads
 
-        def codes(t):
-            return torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) if t is None else t
+        def codes(t, name):
+            if t is None:
+                return torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
+            return _held(t, name, "codes", n_scales * page_size * head_dim)
 
-        def scales(t):
-            return torch.empty(shape[:2], dtype=torch.float32, device=device) if t is None else t
+        def scales(t, name):
+            if t is None:
+                return torch.empty(shape[:2], dtype=torch.float32, device=device)
+            return _held(t, name, "float32", n_scales)
 
-        self.k_codes, self.v_codes = codes(k_codes), codes(v_codes)
-        self.k_scales, self.v_scales = scales(k_scales), scales(v_scales)
+        self.k_codes, self.v_codes = codes(k_codes, "k_codes"), codes(v_codes, "v_codes")
+        self.k_scales, self.v_scales = scales(k_scales, "k_scales"), scales(v_scales, "v_scales")
         s = strata_kv_cache()
         s.n_kv_heads, s.head_dim, s.page_size, s.n_pages = n_kv_heads, head_dim, page_size, n_pages
         s.k_codes, s.v_codes = ptr(self.k_codes), ptr(self.v_codes)
@@ -82,9 +104,16 @@ class PagedKVCache:
 
 def kv_batch(q_start, kv_len, page_table, T: int, max_q: int, max_kv: int) -> strata_kv_batch:
     """Descriptor of one attention call: int32 device tensors q_start [n_seq + 1], kv_len [n_seq],
-    page_table [n_seq, stride], and the host's limits. It keeps the tensors alive."""
+    page_table [n_seq, stride] (rows may lie apart), and the host's limits. It keeps the tensors alive."""
+    n_seq = kv_len.shape[0]
+    _held(kv_len, "kv_len", "int32", n_seq)
+    _held(q_start[:n_seq + 1], "q_start", "int32", n_seq + 1)
+    _held(page_table[:1, :1], "page_table", "int32", min(1, page_table.numel()))
+    if page_table.shape[0] < n_seq or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table {tuple(page_table.shape)} with strides {page_table.stride()}: "
+                         f"{n_seq} rows of consecutive elements expected")
     b = strata_kv_batch()
-    b.n_seq, b.max_q, b.T, b.max_kv = kv_len.shape[0], max_q, T, max_kv
+    b.n_seq, b.max_q, b.T, b.max_kv = n_seq, max_q, T, max_kv
     b.q_start, b.kv_len, b.page_table = ptr(q_start), ptr(kv_len), ptr(page_table)
     b.table_stride = page_table.stride(0)
     b.tensors = (q_start, kv_len, page_table)
