@@ -51,6 +51,8 @@ class QuantLinear:
         codes = torch.empty(N, K * bits // 8, dtype=torch.uint8, device=src.device)
         scales = torch.empty(N, K // group, dtype=torch.float16, device=src.device)
         status = torch.zeros(1, dtype=torch.int32, device=src.device)
+        if stream is not None:  # the copy and the cleared word were made on torch's current stream
+            torch.cuda.current_stream(src.device).synchronize()
         check(strata_quantize_groups_bits(src, N, K, codes, scales, status, group_size=group,
                                           bits=bits, stream=stream), "strata_quantize_groups_bits")
         rc, v = strata_read_status(status, stream)
