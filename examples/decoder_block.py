@@ -71,6 +71,7 @@ class DecoderBlock:
                  "ws_moe": self.moe.workspace_size(T)}
         for name, n in sizes.items():
             b[name] = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        b["words"] = [b[name][:4].view(torch.int32) for name in ("ws_qkv", "ws_o", "ws_moe")]
         return b
 
     def forward(self, x, cache, batch, slots, positions, b):
@@ -89,7 +90,18 @@ class DecoderBlock:
                                           residual=x), "output projection")
         st.check(st.strata_moe_forward(self.moe.struct(), b["mid"], T, b["out"], b["ws_moe"], b["ws_moe"].numel()),
                  "MoE layer")
+        # projections and the MoE layer clear their status words at every call: what they found is kept here
+        for word in b["words"]:
+            b["status"] |= word
         return b["out"]
+
+    @staticmethod
+    def check(b):
+        """Raises if a call since the last check reported a fault. Waits for the current stream."""
+        for name, (rc, bits) in (("attention", st.strata_workspace_status(b["ws_att"])),
+                                 ("append, projections, MoE layer", st.strata_read_status(b["status"]))):
+            if rc != 0:
+                raise st.StrataError(rc, f"{name}: device status 0x{bits:x}")
 
 
 def random_block(H=1024, I=512, E=16, k=2, Hq=8, Hkv=2, D=128, seed=0):
@@ -157,6 +169,7 @@ def main():
     b = block.buffers(cache, batch)
     x = torch.randn(batch.T, block.H, device="cuda").bfloat16()
     out = block.forward(x, cache, batch, slots, positions, b)
+    block.check(b)
     last = np.cumsum(prompts) - 1
     graph = DecodeGraph(block, cache, pages, len(prompts), max_len)
     tok = out[to_gpu(last)]
@@ -171,10 +184,7 @@ def main():
         tok = graph.step(next_input(tok), pages)
     end.record()
     torch.cuda.synchronize()
-    for name, rc in (("append", st.strata_read_status(b["status"])), ("append", st.strata_read_status(graph.b["status"])),
-                     ("attention", st.strata_workspace_status(graph.b["ws_att"])),
-                     ("MoE layer", st.strata_workspace_status(graph.b["ws_moe"]))):
-        assert rc[0] == 0, f"{name}: device status 0x{rc[1]:x}"
+    block.check(graph.b)
     assert torch.isfinite(tok.float()).all()
     print(f"{sum(prompts)} prompt tokens, then {steps} steps of {len(prompts)} tokens: "
           f"{begin.elapsed_time(end) / steps * 1e3:.0f} us a step (host work between replays included)")

@@ -373,7 +373,8 @@ typedef struct {
  * longer batches may multiply weights rounded once to f16 (2^-11 relative), with f16 copies of the
  * rows of x in the workspace, each times a power of two that keeps its range.
  * workspace >= strata_linear_workspace_size(w, T) bytes (0: the projection or T is invalid),
- * 256-byte aligned, device; it needs no initialisation. strata_workspace_status reads its status.
+ * 256-byte aligned, device; it needs no initialisation. strata_workspace_status reads its status, that
+ * of the last call: every call clears the word first.
  */
 #define STRATA_LINEAR_EXACT_T 64
 size_t strata_linear_workspace_size(const strata_linear* w, int64_t T_max);
