@@ -231,16 +231,20 @@ static cudaError_t launch_stream_n(const LinearArgs& a, cudaStream_t stream) {
 // more, every block reads all of x, and wider blocks (32 rows, 64 beyond 16 tokens) read it less
 // often; where 16-row blocks leave SMs idle, they are faster (us, wide / 16 rows: 16 tokens, 8 bits,
 // 7168 -> 9216 19.6 / 32.1, 4 bits, 1024 -> 1024 2.7 / 2.2; 32 tokens 30.4 / 67 and 5.6 / 3.2). Blocks of 48
-// rows and 16 warps where they take one round of the SMs and 32-row blocks two (us, 32 / 48 rows: 16
-// tokens, 4096 -> 6144 9.5 / 8.1 at 4 bits, 11.1 / 10.4 at 8; in one round both, 4096 -> 4096 5.9 / 8.2).
+// rows and 16 warps, one an SM, where 32-row blocks, two an SM, put two on most SMs: x is read by fewer blocks. Their
+// reduction over 16 warps pays from 384 columns a bit on. (us, 32 / 48 rows, 16 tokens, to 4868 and to 7296
+// columns: 4 bits 1024 4.3 / 4.4, 4.5 / 4.4, 1536 5.2 / 4.9, 5.4 / 4.9, 4096 9.4 / 8.2, 9.7 / 8.2; 8 bits 1024 4.4 / 5.0, 4.6 /
+// 4.9, 2048 6.4 / 6.8, 6.7 / 6.7, 3200 9.0 / 8.8, 9.4 / 9.0, 7168 16.0 / 14.9, 16.3 / 15.3; one 32-row block an SM:
+// 4 bits 4096 -> 4096 5.9 / 8.2.)
 template <int kBits, int kUnit>
 static cudaError_t launch_stream_t(const LinearArgs& a, cudaStream_t stream) {
   const bool narrow = a.N <= kLinNarrowN;
+  const bool wide = a.N > kLinSms * 32 && a.N <= kLinSms * 48 && a.K >= 384 * kBits;
   if (a.T <= 8) return launch_stream_n<kBits, kUnit, 1, 1, 2, 8, 3>(a, stream);
   if (a.T <= 16)
-    return narrow                                   ? launch_stream_n<kBits, kUnit, 2, 1, 1, 8, 3>(a, stream)
-           : a.N > kLinSms * 32 && a.N <= kLinSms * 48 ? launch_stream_n<kBits, kUnit, 2, 3, 1, 16, 1>(a, stream)
-                                                    : launch_stream_n<kBits, kUnit, 2, 2, 1, 8, 2>(a, stream);
+    return narrow ? launch_stream_n<kBits, kUnit, 2, 1, 1, 8, 3>(a, stream)
+           : wide ? launch_stream_n<kBits, kUnit, 2, 3, 1, 16, 1>(a, stream)
+                  : launch_stream_n<kBits, kUnit, 2, 2, 1, 8, 2>(a, stream);
   return narrow ? launch_stream_n<kBits, kUnit, 4, 1, 1, 8, 2>(a, stream)
                 : launch_stream_n<kBits, kUnit, 4, 4, 1, 8, 1>(a, stream);
 }

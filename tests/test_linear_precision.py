@@ -92,3 +92,14 @@ def test_non_finite_rows_stay_alone(T, N):
     assert np.isnan(got[2]).all() and np.isnan(got[:, 37]).all() and not np.isfinite(got[4]).any()
     y, b = bound(ref.bf16_bits_to_f64(x[rows]), codes[cols], scales[cols], 8, 128, T)
     assert (np.abs(got[np.ix_(rows, cols)] - y) <= b).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T", [9, 16])
+@pytest.mark.parametrize("N,K", [(4864, 1536), (4865, 1408), (4865, 1536), (5003, 3200), (7296, 2944), (7297, 3200)])
+def test_blocks_of_a_wide_layer(T, N, K, bits):
+    """Both sides of the sizes at which blocks change their shape."""
+    codes, scales = make(N, K, bits, 128)
+    x = acts(T, K)
+    assert worst(run(x, codes, scales, bits, 128), ref.bf16_bits_to_f64(x), codes, scales, bits, 128) <= 1
