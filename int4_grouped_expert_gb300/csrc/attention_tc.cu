@@ -16,14 +16,16 @@
 //                  in f16 and the sums fp32), which after the first tiles is rare
 //   warps 12-19    codes -> f16 tiles in shared memory, K as it lies and V transposed (bytes of two
 //                  tokens paired with PRMT), a ring of 4 stages: (K0, K1), (V0, K2), (V1, K3), ...
-// Codes are f16 as they are, exactly; a page's scales, one pair for every 16 tokens of a tile, go to the softmax
-// (attention.cuh).
+// Codes are f16 as they are, exactly; the scales of a tile's page, or of its pages of 16 or 32 tokens, go to the
+// softmax (attention.cuh). That costs it a dozen instructions a row and tile, about 5% where it is the bound, against
+// scaling the codes to the largest page of the block; that one left small pages few bits.
 // Queries become f16 with a power of two per row; a token that no row sees or in a page that does not
 // exist becomes zeros and a masked score, so what lies there does not matter.
 //
-// Measured: 2048 queries on 8192 tokens, 32 query and 8 K/V heads of 128: 242 us, 993 TFLOP/s; a tile of 64
-// tokens takes a block 1.17 us, half of it MMA. Softmax and conversion instructions (issue 60% of active
-// cycles), shared memory (67%) and the tensor pipe (45%) wait for one another over the score buffers; none is full.
+// Measured: 2048 queries on 8192 tokens, 32 query and 8 K/V heads of 128: 252 us back to back, 954 TFLOP/s (254 as
+// a public call); 8192 more tokens take 268 us, 1.05 us a tile over both rounds of blocks. Softmax and conversion
+// instructions (issue 60% of active cycles), shared memory (66%) and the tensor pipe (46%) wait for one another over
+// the score buffers; none is full.
 // Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every
 // role leaves its loop, MMAs in flight are drained (bounded) and TMEM is freed.
 #include <algorithm>
@@ -191,6 +193,7 @@ __device__ __forceinline__ float max16(const uint32_t* x) {
 }
 
 // kGroups: pairs of scales in a tile, 1 where it lies in one page (of 64 or 128 tokens), else one for every 16 tokens.
+// (us, 1 / 4 of them, pages of 64: 2048 queries on 8192 tokens 252 / 268, 8 on 131072 141 / 144, 4096 on 4096 154 / 163.)
 template <int kD, int kGroups>
 __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a) {
   using C = AtCfg<kD>;

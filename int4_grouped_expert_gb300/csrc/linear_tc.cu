@@ -24,8 +24,9 @@
 //       a pass before copies x to f16, each row times a power of two that keeps its range; the epilogue
 //       multiplies it back.
 //
-// Measured at 4 bits: 64 tokens 7168 -> 9216 23 us (1.4 TB/s of codes); 4096 tokens 373 us, 1450 TFLOP/s (tensor pipe
-// 65%; a stage's conversion and store to TMEM and the epilogue, which no other sum overlaps, are the rest).
+// Measured at 4 bits: 64 tokens 7168 -> 9216 23 us (1.4 TB/s of codes); 4096 tokens 373 us, 1450 TFLOP/s, in short runs
+// and 400 us, 1350 TFLOP/s, once the power limit holds the clocks (tensor pipe 65%; a stage's conversion and store to
+// TMEM and the epilogue, which no other sum overlaps, are the rest).
 //
 // Every mbarrier wait is bounded in time; on time-out the kernel sets STRATA_DEV_TIMEOUT, every role
 // leaves its loop, in-flight copies and MMAs are drained (bounded) and TMEM is freed.
