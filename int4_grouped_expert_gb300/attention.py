@@ -31,8 +31,8 @@ class QuantLinear:
     (from_fp16). bias: fp32 [N] or None."""
 
     def __init__(self, codes, scales, N: int, K: int, bits: int = 4, group: int = GROUP, bias=None):
-        _held(codes, "codes", "codes", N * K * bits // 8)
-        _held(scales, "scales", "float16", N * (K // group))
+        _held(codes, "codes", "codes", N * K * (bits or 4) // 8)  # (0: the library's defaults)
+        _held(scales, "scales", "float16", N * (K // (group or GROUP)))
         if bias is not None:
             _held(bias, "bias", "float32", N)
         self.codes, self.scales, self.bias = codes, scales, bias

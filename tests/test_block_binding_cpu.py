@@ -42,6 +42,7 @@ def test_projections():
     st.QuantLinear(torch.zeros(N, K // 2, dtype=u8), torch.zeros(N, 2, dtype=f16), N, K)
     st.QuantLinear(torch.zeros(N, K, dtype=torch.int8), torch.zeros(N, 4, dtype=f16), N, K, 8, 64, torch.zeros(N))
     st.QuantLinear(1 << 12, 1 << 12, N, K)                                 # addresses
+    st.QuantLinear(torch.zeros(N, K // 2, dtype=u8), torch.zeros(N, 2, dtype=f16), N, K, 0, 0)  # (the defaults)
     for codes, scales, bias, error in (
             (torch.zeros(N, K // 2, dtype=torch.int16), torch.zeros(N, 2, dtype=f16), None, TypeError),
             (torch.zeros(N, K, dtype=u8), torch.zeros(N, 2, dtype=f16), None, ValueError),
