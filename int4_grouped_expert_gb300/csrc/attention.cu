@@ -395,7 +395,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   float o[kNT][NJ][4];
   // ref: the reference in use, or 0 before any score; limit: how much of a score above it moves it
   float ref[kNT][2], limit[kNT][2], sum[kNT][2];
+  float lv_top;  // largest log2 of a V scale
   auto reset = [&] {
+    lv_top = -INFINITY;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       ref[n][0] = ref[n][1] = 0.f;
@@ -422,6 +424,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     const uint8_t* slot = ring + i_slot * 2 * KB;
     const float2 sc0 = s_scale[warp][i_slot][0], sc1 = s_scale[warp][i_slot][1];
     const float k_scale[2] = {sc0.x, sc1.x}, lv[2] = {log2_scale(sc0.y), log2_scale(sc1.y)};
+    lv_top = fmaxf(lv_top, fmaxf(lv[0], lv[1]));
     const int lost = (sc0.y < 0.f ? 1 : 0) | (sc1.y < 0.f ? 2 : 0);
     // S^T: tokens tok_g, tok_g + 8 of each tile x columns 2t, 2t+1
     float sc[kNT][2][4];
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
           else limit[n][c] = kLag;
           ref[n][c] += up;
           const float f = had ? exp2_approx(-up) : 1.f;  // (without a reference the sums are 0, or nan)
-          sum[n][c] *= f;
+          sum[n][c] = sum_times_exp2(sum[n][c], had ? -up : 0.f);
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
             o[n][j][c] *= f;
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     for (int u = 0; u < 2; ++u) {
       uint32_t pf[kNT][2];
       const float per_scale = exp2_approx(-lv[u]);
-      const bool small = lv[u] < kSmallScale;
+      const bool small = lv[u] < lv_top - kFarScale;
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         float p[4];
@@ -624,14 +627,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
         for (int k = 0; k < 8; ++k) now = fmaxf(now, ml[k].x);
         const float ref = now == -INFINITY ? 0.f : now;
         const float f = now == -INFINITY ? 1.f : exp2_approx(top - ref);
-        l *= f;
+        l = sum_times_exp2(l, now == -INFINITY ? 0.f : top - ref);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] *= f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           // (a slot that has seen nothing holds zeros; one that has seen nothing but nan, nan)
           const float w = exp2_approx(ml[k].x - ref);
-          l = fmaf(ml[k].y, w, l);
+          l += sum_times_exp2(ml[k].y, ml[k].x - ref);
           y[0] = fmaf(v[k].x, w, y[0]); y[1] = fmaf(v[k].y, w, y[1]);
           y[2] = fmaf(v[k].z, w, y[2]); y[3] = fmaf(v[k].w, w, y[3]);
         }
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, s_ref[w][col]);
 #pragma unroll
       for (int w = 0; w < kAttWarps; ++w) {
-        l = fmaf(s_sum[w][col], top == -INFINITY ? 1.f : exp2_approx(s_ref[w][col] - top), l);
+        l += sum_times_exp2(s_sum[w][col], top == -INFINITY ? 0.f : s_ref[w][col] - top);
         const float4 v = *reinterpret_cast<const float4*>(s_o + (w * COLS + col) * OS + e);
         y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
       }

@@ -34,9 +34,16 @@ __device__ __forceinline__ float log2_scale(float s) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s < 7.88860905e-31f ? 7.88860905e-31f : s));
   return y;
 }
-// Below this log2(V scale) w may be flushed to zero (2^-126) though its part in the sum is not negligible: there the sum
-// takes 2^(score - ref) instead. (Pages of zeros have such scales.)
-constexpr float kSmallScale = -24.f;
+// Where log2(V scale) is this far below the largest met so far, w may be flushed to zero (2^-126) though its part in the
+// sum is not negligible: there the sum takes 2^(score - ref) instead. (Pages of zeros have such scales. Nearer ones are
+// flushed for weights below 2^-40 of the largest.)
+constexpr float kFarScale = 78.f;
+// A sum of the softmax times 2^d: to a reference that is -d above its own. Between pages of zeros and of large values
+// that is more than the 2^-126 that one factor reaches, and such a sum is large (w / V scale).
+__device__ __forceinline__ float sum_times_exp2(float sum, float d) {
+  const float a = fmaxf(d, -100.f);
+  return sum * exp2_approx(a) * exp2_approx(d - a);
+}
 
 // The rows and tokens of one sequence, cut to the call's limits.
 struct SeqView {

@@ -211,8 +211,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   uint64_t* drain = pv_done + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   __shared__ int abort_flag_s;
-  // of each group: K scale, log2 of the V scale, the inverse V scale (0 below kSmallScale), and whether all is well (0),
-  // the page does not exist (1), has a scale of inf or nan (2: nan for the rows that see it) or a small V scale (3)
+  // of each group: K scale, log2 of the V scale, the inverse V scale (0 for a small one), and whether all is well (0), the
+  // page does not exist (1), has a scale of inf or nan (2: nan for the rows that see it) or a small V scale (3:
+  // kFarScale below the largest up to there)
   __shared__ float4 s_scale[kAtScales][kGroups];
   __shared__ volatile int s_any_small;  // a tile so far has a page of a small V scale
   __shared__ volatile int s_end[6];  // what is wanted again at the end only: not kept in registers
@@ -423,18 +424,30 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       // -------------------------------------------------------------- scales
       int batch = 0;
       float3 now = scales_now, next = scales_next;
+      // (the largest up to the batch's end: what is called small a few tiles early is summed the other way, as well)
+      float lv, top_lv = -INFINITY;
+      bool fine;
+      auto take = [&] {
+        fine = now.x < INFINITY && now.y < INFINITY;
+        lv = fine ? fminf(log2_scale(now.y), 126.f) : 0.f;
+        float x = lv;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        top_lv = fmaxf(top_lv, x);
+      };
+      take();
       auto lay_out = [&](int t) {
         if (t >= n_tiles) return;
         if (t / kBatch > batch) {
           now = next;
           next = scales_of(++batch + 1);
+          take();
         }
-        const bool fine = now.x < INFINITY && now.y < INFINITY;
-        const float lv = fine ? log2_scale(now.y) : 0.f;
-        const bool small = lv < kSmallScale;
+        const bool small = lv < top_lv - kFarScale;
         if (lane / kGroups == t % kBatch) {
           s_scale[t % kAtScales][lane % kGroups] =
-              make_float4(fine ? now.x : 1.f, lv, small ? 0.f : exp2_approx(-lv), !fine ? 2.f : small ? 3.f : now.z);
+              make_float4(fine ? now.x : 1.f, lv, small ? 0.f : exp2_approx(-lv),
+                          now.z != 0.f ? now.z : !fine ? 2.f : small ? 3.f : 0.f);
           if (small) s_any_small = 1;
         }
       };
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         for (int c = 0; c < kAtTok; ++c) {  // (short code: it is rarely run)
           const float4 sc = scale[c * kGroups / kAtTok];
           const float score = __uint_as_float(tc::tmem_ld1(ts + c));
-          const bool on = sc.y < kSmallScale && c <= hi && c >= lo;
+          const bool on = sc.w == 3.f && c <= hi && c >= lo;
           const float x = on ? score * fmaxf(cmul * sc.x, 1.17549435e-38f) : -INFINITY, before = top;
           top = fmaxf(top, x);
           const float ref = top == -INFINITY ? 0.f : top;
@@ -524,8 +537,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       if (__any_sync(0xffffffffu, top > m + 8.f)) {
         const float now = fmaxf(m, top);
         const float f = now == -INFINITY ? 1.f : exp2_approx(m - now);
+        l = sum_times_exp2(l, now == -INFINITY ? 0.f : m - now);
         m = now;
-        l *= f;
         if (j > 0) {
           // the last product has to have added to O (the scores of this tile were issued before it)
           ok = done(tile, j - 1);
@@ -578,7 +591,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     }
     if (s_any_small) {  // (m is finite where top is)
       const float top = small_top, sum = small_sum;
-      if (top != -INFINITY || sum != 0.f) l += sum * exp2_approx(top - (m == -INFINITY ? 0.f : m));
+      if (top != -INFINITY || sum != 0.f) l += sum_times_exp2(sum, top - (m == -INFINITY ? 0.f : m));
     }
     const int q0 = s_end[2], rows = s_end[3], h = s_end[5];
     const int row = s_end[4] + tile * 128 + (warp & 3) * 32 + lane;
@@ -775,7 +788,7 @@ __global__ void __launch_bounds__(kAtJoinRows * kD / 8) attention_tc_join_kernel
       const float4 v0 = __ldcg(reinterpret_cast<const float4*>(slot) + c * 256 + r);
       const float4 v1 = __ldcg(reinterpret_cast<const float4*>(slot) + (c + 1) * 256 + r);
       const float w = exp2_approx(ml.x - ref);
-      sum = fmaf(ml.y, w, sum);
+      sum += sum_times_exp2(ml.y, ml.x - ref);
       y[0] = fmaf(v0.x, w, y[0]); y[1] = fmaf(v0.y, w, y[1]); y[2] = fmaf(v0.z, w, y[2]); y[3] = fmaf(v0.w, w, y[3]);
       y[4] = fmaf(v1.x, w, y[4]); y[5] = fmaf(v1.y, w, y[5]); y[6] = fmaf(v1.z, w, y[6]); y[7] = fmaf(v1.w, w, y[7]);
     }

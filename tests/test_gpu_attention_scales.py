@@ -170,3 +170,50 @@ def test_a_scale_that_is_not_finite_reaches_the_rows_that_see_it(n, P, value):
     hit[:n, 4:] = (np.arange(L - n, L) >= last * P)[:, None]
     assert np.isnan(got[hit]).all() and hit.any()
     assert (np.abs(got - want) <= bound)[~hit].all()
+
+
+@pytest.mark.parametrize("zeros_first", [False, True])
+@pytest.mark.parametrize("big", [0, 30, 60, 110])
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_long_stretches_of_zeros(name, big, zeros_first):
+    """Zeros over many pages in a row, so that a warp, a piece or a block meets nothing else for a while, beside values
+    as large as bf16 holds."""
+    c = shape(name, 64, 16)
+    for s, (L, _) in enumerate(c.seqs):
+        pages = -(-L // 16)
+        for i in range(pages):
+            p = c.table[s, i]
+            if (i < pages // 2) == zeros_first:
+                c.codes["v"][p] = 0
+                c.scales["v"][p] = np.float32(2.0 ** -100)
+            else:
+                c.scales["v"][p] *= np.float32(2.0 ** big)
+    check(c)
+
+
+@pytest.mark.parametrize("name", list(SHAPES))
+@pytest.mark.parametrize("P", [16, 64])
+def test_values_at_both_ends_of_the_range(name, P):
+    """Pages of 2^-90, 1 and 2^110 times the usual values, of like weights."""
+    c = shape(name, 128, P)
+    for s, (L, _) in enumerate(c.seqs):
+        for i in range(-(-L // P)):
+            c.scales["v"][c.table[s, i]] *= np.float32(2.0 ** (-90, 0, 110)[i * 7 // 3 % 3])
+    check(c)
+
+
+@pytest.mark.parametrize("name", ["few rows", "prompt", "many"])
+def test_a_missing_page_beside_huge_values(name):
+    """Its tokens count as unseen, whatever the others' scales."""
+    import int4_grouped_expert_gb300 as st
+    c = shape(name, 64, 16)
+    for kind in "v":
+        c.scales[kind] *= np.float32(2.0 ** 100)
+    c.codes["k"][c.table[0, 3]] = 0xFE                   # (as good as unseen: the largest key, against every query)
+    from workloads import gen
+    c.q_bits = gen.f32_to_bf16_bits((np.abs(ref.bf16_bits_to_f64(c.q_bits)) + 0.5).astype(np.float32))
+    c.scales["k"][c.table[0, 3]] = np.float32(2.0 ** 4)
+    want, bound = reference(c)
+    c.table[0, 3] = -1
+    got = ref.bf16_bits_to_f64(c.gpu().run(expect_status=st.STRATA_DEV_BAD_SLOT)).reshape(want.shape)
+    assert (np.abs(got - want) <= bound).all()
