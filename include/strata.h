@@ -433,6 +433,33 @@ strata_status strata_kv_append(const strata_kv_cache* cache, const void* q_bf16,
                                int64_t n_pos, int32_t rot_dim, uint32_t flags, void* q_out,
                                int64_t q_out_stride, uint32_t* dev_status, strata_stream stream);
 
+/* Norms of queries and keys, one for each head of a row. */
+typedef struct {
+  const float* q_weight; /* [head_dim] fp32 for all query heads (q_head_stride 0), or a row a head; 16-byte aligned;
+                            NULL: q is not normalised */
+  int64_t q_head_stride; /* elements from one head's row to the next: 0, or >= head_dim and a multiple of 4 */
+  const float* k_weight; /* the same for the K heads */
+  int64_t k_head_stride;
+  float eps;             /* finite, >= 2^-100 */
+} strata_qk_norm;
+
+/*
+ * strata_kv_append_normed — strata_kv_append with a norm of each head's row of q and k ahead of the rotation:
+ *   y[i] = x[i] / sqrt(mean_i(x[i]^2) + eps) * weight[i]      (i < head_dim; v is taken as it is)
+ * in fp32: nothing is rounded between the norm and the rotated result (q_out bf16, k codes e4m3). A finite row of
+ * any size has its norm: sums of squares do not overflow. A (row, head) of k that holds inf or nan, or becomes one by its
+ * weights, is treated as one of strata_kv_append; such a row of q gives nan where it is not finite.
+ * Arguments, errors and everything else as strata_kv_append; STRATA_ERR_INVALID_ARG also for a NULL norm, an eps out of
+ * range, and weights that are not aligned or whose stride is below head_dim or no multiple of 4. Without either weight
+ * the call is strata_kv_append.
+ */
+strata_status strata_kv_append_normed(const strata_kv_cache* cache, const strata_qk_norm* norm, const void* q_bf16,
+                                      int64_t q_stride, int32_t n_heads, const void* k_bf16, int64_t k_stride,
+                                      const void* v_bf16, int64_t v_stride, int64_t T, const int32_t* slots,
+                                      const int32_t* positions, const float* rope, int64_t n_pos, int32_t rot_dim,
+                                      uint32_t flags, void* q_out, int64_t q_out_stride, uint32_t* dev_status,
+                                      strata_stream stream);
+
 /* The sequences of one attention call. Arrays are on the device, int32. */
 typedef struct {
   int32_t n_seq;            /* 0 .. 65535 */
@@ -475,6 +502,22 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
                                        float scale, int32_t window, uint32_t flags, void* out_bf16,
                                        int64_t out_stride, void* workspace, size_t ws_bytes,
                                        strata_stream stream);
+
+/*
+ * strata_attention_sinks_forward — strata_attention_forward with a window and n_sinks first tokens of each sequence that
+ * stay visible: a query at position p sees tokens j <= p with j > p - window or j < n_sinks (window 0: all j <= p,
+ * whatever n_sinks is).
+ * What the cache holds between the first tokens and the first token that a row of the sequence sees through the
+ * window is not used, and the page table's entries for pages that lie there whole are not looked at: such pages may be
+ * given back (strata_kv_pages_release does, and leaves -1). n_sinks >= 0; the workspace is that of
+ * strata_attention_workspace_size, and may go from one of the two calls to the other. Arguments, errors and everything
+ * else as strata_attention_forward, which is this call with n_sinks 0.
+ */
+strata_status strata_attention_sinks_forward(const strata_kv_cache* cache, const strata_kv_batch* batch,
+                                             const void* q_bf16, int64_t q_stride, int32_t n_heads, float scale,
+                                             int32_t window, int32_t n_sinks, uint32_t flags, void* out_bf16,
+                                             int64_t out_stride, void* workspace, size_t ws_bytes,
+                                             strata_stream stream);
 
 /*
  * Device status of a route/forward workspace: synchronizes `stream`, returns the status word in

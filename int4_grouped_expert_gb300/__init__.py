@@ -72,6 +72,13 @@ class strata_kv_cache(ctypes.Structure):
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
+class strata_qk_norm(ctypes.Structure):
+    """Mirror of the C struct strata_qk_norm."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("q_head_stride", ctypes.c_int64),
+                ("k_weight", ctypes.c_void_p), ("k_head_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float)]
+
+
 class strata_kv_batch(ctypes.Structure):
     """Mirror of the C struct strata_kv_batch."""
     _fields_ = [("n_seq", ctypes.c_int32), ("max_q", ctypes.c_int32), ("T", ctypes.c_int64),
@@ -122,11 +129,17 @@ _SIGNATURES = {
                                              _P, _I64, _P, _SZ, _P]),
     "strata_kv_append": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache), _P, _I64, _I32, _P, _I64, _P,
                                         _I64, _I64, _P, _P, _P, _I64, _I32, _U32, _P, _I64, _P, _P]),
+    "strata_kv_append_normed": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache), ctypes.POINTER(strata_qk_norm), _P,
+                                               _I64, _I32, _P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I32, _U32,
+                                               _P, _I64, _P, _P]),
     "strata_attention_workspace_size": (_SZ, [ctypes.POINTER(strata_kv_cache),
                                               ctypes.POINTER(strata_kv_batch), _I32]),
     "strata_attention_forward": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache),
                                                 ctypes.POINTER(strata_kv_batch), _P, _I64, _I32,
                                                 _F32, _I32, _U32, _P, _I64, _P, _SZ, _P]),
+    "strata_attention_sinks_forward": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache),
+                                                      ctypes.POINTER(strata_kv_batch), _P, _I64, _I32,
+                                                      _F32, _I32, _I32, _U32, _P, _I64, _P, _SZ, _P]),
     "strata_workspace_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(_U32)]),
     "strata_read_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(_U32)]),
 }
@@ -316,10 +329,7 @@ def strata_linear_forward(lin: strata_linear, x, T, out, workspace, ws_bytes, x_
         lin.N if out_stride is None else out_stride, ptr(workspace), ws_bytes, stream_handle(stream))
 
 
-def strata_kv_append(cache: strata_kv_cache, k, v, T, slots, positions=None, rope=None, n_pos=0,
-                     rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
-                     q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
-    """Strides in elements; None: rows follow one another."""
+def _append_strides(cache, n_heads, k_stride, v_stride, q_stride, q_out_stride):
     if k_stride is None or v_stride is None:
         kv = cache.n_kv_heads * cache.head_dim
         k_stride = kv if k_stride is None else k_stride
@@ -328,10 +338,32 @@ def strata_kv_append(cache: strata_kv_cache, k, v, T, slots, positions=None, rop
         qd = n_heads * cache.head_dim
         q_stride = qd if q_stride is None else q_stride
         q_out_stride = qd if q_out_stride is None else q_out_stride
+    return k_stride, v_stride, q_stride, q_out_stride
+
+
+def strata_kv_append(cache: strata_kv_cache, k, v, T, slots, positions=None, rope=None, n_pos=0,
+                     rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
+                     q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
+    """Strides in elements; None: rows follow one another."""
+    k_stride, v_stride, q_stride, q_out_stride = _append_strides(cache, n_heads, k_stride, v_stride, q_stride,
+                                                                 q_out_stride)
     return (_lib or lib()).strata_kv_append(
         _byref(cache), None if q is None else ptr(q), q_stride, n_heads, ptr(k), k_stride, ptr(v), v_stride, T,
         ptr(slots), ptr(positions), ptr(rope), n_pos, rot_dim, flags, None if q_out is None else ptr(q_out),
         q_out_stride, None if dev_status is None else ptr(dev_status), stream_handle(stream))
+
+
+def strata_kv_append_normed(cache: strata_kv_cache, norm: strata_qk_norm, k, v, T, slots, positions=None, rope=None,
+                            n_pos=0, rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
+                            q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
+    """strata_kv_append with the norms that QKNorm describes. Strides in elements; None: rows follow one another."""
+    k_stride, v_stride, q_stride, q_out_stride = _append_strides(cache, n_heads, k_stride, v_stride, q_stride,
+                                                                 q_out_stride)
+    return (_lib or lib()).strata_kv_append_normed(
+        _byref(cache), _byref(norm), None if q is None else ptr(q), q_stride, n_heads, ptr(k), k_stride, ptr(v),
+        v_stride, T, ptr(slots), ptr(positions), ptr(rope), n_pos, rot_dim, flags,
+        None if q_out is None else ptr(q_out), q_out_stride, None if dev_status is None else ptr(dev_status),
+        stream_handle(stream))
 
 
 def strata_attention_workspace_size(cache: strata_kv_cache, batch: strata_kv_batch, n_heads) -> int:
@@ -351,6 +383,19 @@ def strata_attention_forward(cache: strata_kv_cache, batch: strata_kv_batch, q, 
         ptr(workspace), ws_bytes, stream_handle(stream))
 
 
+def strata_attention_sinks_forward(cache: strata_kv_cache, batch: strata_kv_batch, q, n_heads, scale, out,
+                                   workspace, ws_bytes, window=0, n_sinks=0, flags=0, q_stride=None, out_stride=None,
+                                   stream=None):
+    """strata_attention_forward with n_sinks first tokens that the window leaves visible."""
+    if q_stride is None or out_stride is None:
+        qd = n_heads * cache.head_dim
+        q_stride = qd if q_stride is None else q_stride
+        out_stride = qd if out_stride is None else out_stride
+    return (_lib or lib()).strata_attention_sinks_forward(
+        _byref(cache), _byref(batch), ptr(q), q_stride, n_heads, scale, window, n_sinks, flags, ptr(out), out_stride,
+        ptr(workspace), ws_bytes, stream_handle(stream))
+
+
 def strata_workspace_status(workspace, stream=None):
     v = _U32(0)
     st = lib().strata_workspace_status(ptr(workspace), stream_handle(stream), ctypes.byref(v))
@@ -364,4 +409,4 @@ def strata_read_status(dev_status, stream=None):
 
 
 from .layer import MoELayer  # noqa: E402,F401
-from .attention import PagedKVCache, QuantLinear, kv_batch, rope_table  # noqa: E402,F401
+from .attention import PagedKVCache, QKNorm, QuantLinear, kv_batch, rope_table  # noqa: E402,F401

@@ -1,15 +1,15 @@
 """Device storage of the attention half of a decoder block, and its C descriptors.
 
 QuantLinear holds one projection's codes and scales, PagedKVCache the pages of
-8-bit keys and values, kv_batch the lengths and page tables of one call. All hold
-torch tensors (for device memory only) and fill the C structs with their
+8-bit keys and values, QKNorm the weights of the norms of queries and keys, kv_batch the
+lengths and page tables of one call. All hold torch tensors (for device memory only) and fill the C structs with their
 addresses; the arithmetic runs in the library, which sees addresses only: element
 types and layouts are checked here.
 """
 from __future__ import annotations
 
 from . import (GROUP, StrataError, check, ptr, strata_kv_batch, strata_kv_cache, strata_linear,
-               strata_linear_workspace_size, strata_quantize_groups_bits, strata_read_status)
+               strata_linear_workspace_size, strata_qk_norm, strata_quantize_groups_bits, strata_read_status)
 
 
 def _held(t, name: str, dtype: str, numel: int):
@@ -104,6 +104,29 @@ class PagedKVCache:
         return self._struct
 
 
+class QKNorm:
+    """Norms of queries and keys for each head: fp32 weights, one row [head_dim] (or [1, head_dim]) for all heads
+    or [heads, head_dim] with a row each, or None where there is no norm. eps is added to the mean of squares."""
+
+    def __init__(self, q_weight, k_weight, head_dim: int, eps: float = 1e-6):
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        s = strata_qk_norm()
+        s.eps = eps
+        for name, w in (("q", q_weight), ("k", k_weight)):
+            if w is None:
+                continue
+            rows = 1 if w.dim() == 1 else w.shape[0]
+            if w.dim() not in (1, 2) or w.shape[-1] != head_dim:
+                raise ValueError(f"{name}_weight {tuple(w.shape)}: [{head_dim}] or [heads, {head_dim}] expected")
+            _held(w, f"{name}_weight", "float32", rows * head_dim)
+            setattr(s, f"{name}_weight", ptr(w))
+            setattr(s, f"{name}_head_stride", head_dim if rows > 1 else 0)
+        self._struct = s
+
+    def struct(self) -> strata_qk_norm:
+        return self._struct
+
+
 def kv_batch(q_start, kv_len, page_table, T: int, max_q: int, max_kv: int) -> strata_kv_batch:
     """Descriptor of one attention call: int32 device tensors q_start [n_seq + 1], kv_len [n_seq],
     page_table [n_seq, stride] (rows may lie apart), and the host's limits. It keeps the tensors alive."""
@@ -131,4 +154,4 @@ def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device: str = "c
     return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous().to(device)
 
 
-__all__ = ["QuantLinear", "PagedKVCache", "kv_batch", "rope_table"]
+__all__ = ["QuantLinear", "PagedKVCache", "QKNorm", "kv_batch", "rope_table"]

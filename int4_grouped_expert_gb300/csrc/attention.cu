@@ -82,15 +82,14 @@ __device__ __forceinline__ int slot_offset(int r, int c) {
   return r * kD + ((c ^ (kD == 128 ? r & 7 : (r >> 1) & 2)) << 4);
 }
 
-// First step of 32 tokens that a sequence's rows see, and how many; none if this kernel skips it.
-struct SeqSteps {
-  int first, n;
-};
-__device__ __forceinline__ SeqSteps seq_steps(const AttnArgs& a, const SeqView& v) {
+// The steps of 32 tokens that a sequence's rows see; none if this kernel skips it.
+template <bool kSink>
+__device__ __forceinline__ Span<kSink> seq_steps(const AttnArgs& a, const SeqView& v) {
   const int64_t rows = static_cast<int64_t>(v.n) * a.group;
-  if (rows == 0 || rows > a.rows_above) return {0, 0};
-  const int lo = first_seen(a, v.len - v.n) / kAttStep;
-  return {lo, max(1, (v.len + kAttStep - 1) / kAttStep - lo)};  // (no tokens: one empty step, zeros)
+  if (rows == 0 || rows > a.rows_above) return {0, 0, 0, 0};
+  Span<kSink> s = span_of<kSink, kAttStep>(a, first_seen(a, v.len - v.n), v.len);
+  s.n = max(1, s.n);  // (no tokens: one empty step, zeros)
+  return s;
 }
 
 __device__ __forceinline__ int pieces_of(int steps, int per) {
@@ -101,9 +100,10 @@ struct Piece {
   int seq, head, index, of;  // piece `index` of `of`
   int slot0;                 // workspace slot of the (sequence, head)'s piece 0, if of > 1
 };
+template <bool kSink>
 __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
   if (a.b.n_seq == 1) {
-    const int steps = seq_steps(a, seq_view(a, 0, blockIdx.x == 0 && threadIdx.x == 0)).n, heads = a.c.n_kv_heads;
+    const int steps = seq_steps<kSink>(a, seq_view(a, 0, blockIdx.x == 0 && threadIdx.x == 0)).n, heads = a.c.n_kv_heads;
     int k = 1;
     for (int q = 2; q <= 4; ++q) {
       const int pieces = kAttResident - heads * q / 4;
@@ -122,7 +122,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
   const int s0 = min(a.b.n_seq, lane * per_lane), s1 = min(a.b.n_seq, s0 + per_lane);
   const bool flag = blockIdx.x == 0 && threadIdx.x < 32;
   int mine = 0;
-  for (int s = s0; s < s1; ++s) mine += seq_steps(a, seq_view(a, s, flag)).n;
+  for (int s = s0; s < s1; ++s) mine += seq_steps<kSink>(a, seq_view(a, s, flag)).n;
   const int kept = mine;  // per_lane == 1: the lane's steps
   const int heads = a.c.n_kv_heads, pairs = heads * a.b.n_seq;
   const unsigned total = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)) * heads;  // < 2^31 (host)
@@ -138,7 +138,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
     const int pieces = kAttResident - pairs * q / 4;
     per = max(kAttMinSteps, static_cast<int>((total + pieces - 1) / pieces));
     blocks = slots = 0;
-    for (int s = s0; s < s1; ++s) count(per_lane == 1 ? kept : seq_steps(a, seq_view(a, s, false)).n, blocks, slots);
+    for (int s = s0; s < s1; ++s) count(per_lane == 1 ? kept : seq_steps<kSink>(a, seq_view(a, s, false)).n, blocks, slots);
     if (__reduce_add_sync(0xffffffffu, static_cast<unsigned>(blocks)) <= kAttResident) break;
   }
   int b_at = blocks, s_at = slots;  // inclusive scans
@@ -155,7 +155,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
   if (lane == owner) {
     int b0 = b_at - blocks, l0 = s_at - slots;
     for (int s = s0; s < s1; ++s) {
-      const int steps = per_lane == 1 ? kept : seq_steps(a, seq_view(a, s, false)).n;
+      const int steps = per_lane == 1 ? kept : seq_steps<kSink>(a, seq_view(a, s, false)).n;
       int nb = 0, ns = 0;
       count(steps, nb, ns);
       if (id < b0 + nb) {
@@ -178,14 +178,15 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, Piece& p) {
 }
 
 // A place in the list of all steps: step `at` of the n of (sequence, head); sequences in order, heads within.
+template <bool kSink>
 struct Walk {
   int seq, head, at;
-  SeqSteps st;
+  Span<kSink> st;
   SeqView v;
   __device__ __forceinline__ void open(const AttnArgs& a, int s) {
     seq = s;
     v = seq_view(a, s, false);
-    st = seq_steps(a, v);
+    st = seq_steps<kSink>(a, v);
   }
   // Moves on by m steps of this head, which has at least as many left. (Not called past the last step.)
   __device__ __forceinline__ void move(const AttnArgs& a, int m) {
@@ -202,13 +203,14 @@ struct Walk {
 struct Share {
   int per, total, todo;
 };
-__device__ __forceinline__ bool find_share(const AttnArgs& a, Share& sh, Walk& w) {
+template <bool kSink>
+__device__ __forceinline__ bool find_share(const AttnArgs& a, Share& sh, Walk<kSink>& w) {
   const int lane = threadIdx.x & 31, heads = a.c.n_kv_heads;
   const int per_lane = (a.b.n_seq + 31) / 32;
   const int s0 = min(a.b.n_seq, lane * per_lane), s1 = min(a.b.n_seq, s0 + per_lane);
   const bool flag = blockIdx.x == 0 && threadIdx.x < 32;
   int mine = 0;
-  for (int s = s0; s < s1; ++s) mine += seq_steps(a, seq_view(a, s, flag)).n * heads;
+  for (int s = s0; s < s1; ++s) mine += seq_steps<kSink>(a, seq_view(a, s, flag)).n * heads;
   int end = mine;  // inclusive scan
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -226,7 +228,7 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, Share& sh, Walk& w
   int seq = 0, left = begin - (end - mine);
   if (lane == owner) {
     for (seq = s0; seq < s1; ++seq) {
-      const int n = seq_steps(a, seq_view(a, seq, false)).n * heads;
+      const int n = seq_steps<kSink>(a, seq_view(a, seq, false)).n * heads;
       if (left < n) break;
       left -= n;
     }
@@ -241,7 +243,8 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, Share& sh, Walk& w
 
 // kSolo: each warp takes an even share of all steps and goes through its (sequence, head) pairs alone.
 // Otherwise a block takes one piece of a pair.
-template <int kD, int kNT, bool kSolo>
+// kSink: there is a window, and a.sinks first tokens that stay visible before it.
+template <int kD, int kNT, bool kSolo, bool kSink>
 __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a) {
   constexpr int COLS = 8 * kNT;
   constexpr int KW = kD / 64;       // 16-byte pieces of a K row per lane
@@ -262,12 +265,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = a.group;
   Piece pc;
-  Walk now{}, ahead{};  // (kSolo) the step at hand, and the next to copy
+  Walk<kSink> now{}, ahead{};  // (kSolo) the step at hand, and the next to copy
   Share share;
   int h, s, rows;   // the (sequence, head) at hand and its rows: <= COLS
   SeqView sv;
   int p_lo, p_hi;   // positions of the first and last query
-  int lo, hi;       // the tokens of the piece
+  int lo, hi;       // the tokens of the piece (kSink: numbers of steps times 32, and the sequence's tokens)
+  int to = 0;       // (kSink) the last number of the piece, times 32
+  Span<kSink> span{};
   int seen_lo = 0;  // first token that a row sees
   auto take = [&](int seq, int head, const SeqView& v) {
     s = seq, h = head, sv = v, rows = v.n * G;
@@ -277,12 +282,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     if (!find_share(a, share, now)) return;
     ahead = now;
   } else {
-    if (!find_piece(a, pc)) return;
+    if (!find_piece<kSink>(a, pc)) return;
     take(pc.seq, pc.head, seq_view(a, pc.seq, false));
-    const SeqSteps st = seq_steps(a, sv);
+    span = seq_steps<kSink>(a, sv);
     seen_lo = first_seen(a, sv.len - sv.n);
-    lo = (st.first + static_cast<int>(static_cast<int64_t>(st.n) * pc.index / pc.of)) * kAttStep;
-    hi = min(sv.len, (st.first + static_cast<int>(static_cast<int64_t>(st.n) * (pc.index + 1) / pc.of)) * kAttStep);
+    lo = (span.first + static_cast<int>(static_cast<int64_t>(span.n) * pc.index / pc.of)) * kAttStep;
+    to = (span.first + static_cast<int>(static_cast<int64_t>(span.n) * (pc.index + 1) / pc.of)) * kAttStep;
+    hi = kSink ? sv.len : min(sv.len, to);
   }
 
   // ---- copies: a lane moves piece lane % PIECES of rows lane / PIECES, + 32 / PIECES, ...
@@ -294,6 +300,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   __shared__ float2 s_scale[kAttWarps][kAttSlots][2];
   const uint32_t scale_addr = static_cast<uint32_t>(__cvta_generic_to_shared(&s_scale[warp][0][0]));
   // (tokens lo .. hi - 1 are the ones that a row sees: of the others nothing is looked up or used)
+  // where step number n / 32 of the block's pair begins, and whether it is the piece's
+  auto ours = [&](int n) { return n < (kSink ? to : hi); };
+  auto token = [&](int n) { return kSink && n >= span.gap_at * kAttStep ? n + span.gap * kAttStep : n; };
   auto issue = [&](int s, int h, int lo, int hi, int j0, int i_slot) {
     const int32_t* table = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
     const uint32_t slot = ring_addr + i_slot * 2 * KB;
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     for (int u = 0; u < 2; ++u) {
       const int j = j0 + 16 * u;
       int page = -1;
-      if (j < hi && j + 16 > lo) {
+      if (j < hi && (j + 16 > lo || (kSink && j < a.sinks))) {
         page = input(a, table + (j >> pshift));
         if (page < 0 || page >= a.c.n_pages) {
           if (lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
@@ -322,7 +331,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       for (int i = 0; i < NI / 2; ++i) {
         const int r = lane / PIECES + RPI * i;
         const uint32_t dst = slot + slot_offset<kD>(16 * u + r, lane % PIECES);
-        const bool on = r >= m && r < n;
+        const bool on = (r >= m || (kSink && j + r < a.sinks)) && r < n;
         const int64_t at = on ? base + i * 512 : 0;
         copy16(dst, a.c.k_codes + at, on);
         copy16(dst + KB, a.c.v_codes + at, on);
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   int j_next = 0, to_copy = 0;
   auto issue_ahead = [&](int i_slot) {
     issue(ahead.seq, ahead.head, first_seen(a, ahead.v.len - ahead.v.n), ahead.v.len,
-          (ahead.st.first + ahead.at) * kAttStep, i_slot);
+          ahead.st.at(ahead.at) * kAttStep, i_slot);
     if (--to_copy > 0) ahead.move(a, 1);
   };
   if constexpr (kSolo) {
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     j_next = lo + warp * kAttStep;
 #pragma unroll 1
     for (int i = 0; i < kAttSlots; ++i, j_next += kAttWarps * kAttStep) {
-      if (j_next < hi) issue(s, h, seen_lo, hi, j_next, i);
+      if (ours(j_next)) issue(s, h, seen_lo, hi, token(j_next), i);
       cp_async_commit();
     }
   }
@@ -455,8 +464,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
           for (int n = 0; n < kNT; ++n) mma_add(sc[n][u], A, qf[n][4 * w + j][0], qf[n][4 * w + j][1]);
         }
     }
-    const bool whole = j0 >= (a.window > 0 ? p_hi - a.window + 1 : 0) && j0 + kAttStep - 1 <= p_lo &&
-                       j0 + kAttStep <= hi && !lost;
+    const bool whole = (j0 >= (a.window > 0 ? p_hi - a.window + 1 : 0) || (kSink && j0 + kAttStep <= a.sinks)) &&
+                       j0 + kAttStep - 1 <= p_lo && j0 + kAttStep <= hi && !lost;
     // exponents relative to the reference (in use or 0)
     bool over = false;
 #pragma unroll
@@ -472,8 +481,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
             if (!whole) {
               const int r = tok_g + 8 * i, j = j0 + 16 * u + r;
               const int pos = p_lo + static_cast<int>(after >> (16 * n + 8 * c) & 255u);
-              const bool seen = j < hi && j <= pos && (a.window <= 0 || j > pos - a.window) &&
-                                !(lost >> u & 1);
+              const bool seen = j < hi && j <= pos &&
+                                (a.window <= 0 || j > pos - a.window || (kSink && j < a.sinks)) && !(lost >> u & 1);
               if (!seen) x = -INFINITY;
             }
             sc[n][u][2 * i + c] = x;
@@ -680,9 +689,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       hi = sv.len;
       load_queries();
       reset();
-      int j0 = (now.st.first + now.at) * kAttStep;
+      int j0 = now.st.at(now.at) * kAttStep;
 #pragma unroll 1
-      for (int i = 0; i < m; ++i, j0 += kAttStep) {
+      for (int i = 0; i < m; ++i, j0 = kSink ? now.st.at(now.at + i) * kAttStep : j0 + kAttStep) {
         cp_async_wait<kAttSlots - 1>();
         __syncwarp();
         step(j0, i_slot);
@@ -729,12 +738,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     reset();
     int i_slot = 0;
 #pragma unroll 1
-    for (int j0 = lo + warp * kAttStep; j0 < hi; j0 += kAttWarps * kAttStep, j_next += kAttWarps * kAttStep) {
+    for (int j0 = lo + warp * kAttStep; ours(j0); j0 += kAttWarps * kAttStep, j_next += kAttWarps * kAttStep) {
       cp_async_wait<kAttSlots - 1>();
       __syncwarp();
-      step(j0, i_slot);
+      step(token(j0), i_slot);
       __syncwarp();  // every lane has read the slot
-      if (j_next < hi) issue(s, h, seen_lo, hi, j_next, i_slot);
+      if (ours(j_next)) issue(s, h, seen_lo, hi, token(j_next), i_slot);
       cp_async_commit();
       i_slot = i_slot + 1 == kAttSlots ? 0 : i_slot + 1;
     }
@@ -806,7 +815,7 @@ AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_hea
   const int64_t G = n_heads / c.n_kv_heads, most_rows = b.max_q * G;
   if (most_rows > kAttStreamRows) {
     p.tc = true;
-    p.tc_slots = attn_tc_slots(c, b, G, 0);
+    p.tc_slots = attn_tc_slots(c, b, G, 0, 0);
     p.tc_part_floats = attn_tc_part_floats(c, p.tc_slots);
     // sequences of equal length: none is below the limit
     if (b.T == static_cast<int64_t>(b.n_seq) * b.max_q) return p;
@@ -831,22 +840,25 @@ AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_hea
   return p;
 }
 
-template <int kD, int kNT, bool kSolo>
+template <int kD, int kNT, bool kSolo, bool kSink>
 static cudaError_t launch_attention_t(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
   constexpr size_t slots = static_cast<size_t>(kAttWarps) * kAttSlots * 2 * kAttStep * kD;
   constexpr size_t join = kSolo ? 0 : sizeof(float) * kAttWarps * 8 * kNT * (kD + 4);
   constexpr size_t smem = slots > join ? slots : join;
-  const cudaError_t e = cudaFuncSetAttribute(attention_kernel<kD, kNT, kSolo>,
+  const cudaError_t e = cudaFuncSetAttribute(attention_kernel<kD, kNT, kSolo, kSink>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attention_kernel<kD, kNT, kSolo>, dim3(static_cast<unsigned>(grid)), dim3(kAttWarps * 32), smem,
-                       stream, true, a);
+  return launch_kernel(attention_kernel<kD, kNT, kSolo, kSink>, dim3(static_cast<unsigned>(grid)), dim3(kAttWarps * 32),
+                       smem, stream, true, a);
 }
 
 template <int kD, int kNT>
 static cudaError_t launch_attention_t(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream) {
-  return p.solo ? launch_attention_t<kD, kNT, true>(a, p.grid, stream)
-                : launch_attention_t<kD, kNT, false>(a, p.grid, stream);
+  if (a.sinks > 0)
+    return p.solo ? launch_attention_t<kD, kNT, true, true>(a, p.grid, stream)
+                  : launch_attention_t<kD, kNT, false, true>(a, p.grid, stream);
+  return p.solo ? launch_attention_t<kD, kNT, true, false>(a, p.grid, stream)
+                : launch_attention_t<kD, kNT, false, false>(a, p.grid, stream);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream) {

@@ -71,9 +71,36 @@ __device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s, bool flag)
   return v;
 }
 // First token that a row of the sequence sees whose first row stands at position p (below 0: before the first
-// token). No step of it leaves 32 bits, whatever the window.
+// token), but for the first tokens that stay visible (kSink: a.sinks of them). No step of it leaves 32 bits, whatever the window.
 __device__ __forceinline__ int first_seen(const AttnArgs& a, int p) {
   return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
+// What is walked of a sequence, in steps or tiles of `kStep` tokens that start at multiples of it: all that any of its rows
+// sees. With first tokens that stay visible (kSink) these come first, and number `gap_at` on lies `gap` further on in
+// the cache: what is between is neither looked up nor counted. A kernel goes through numbers, and asks at() where they are.
+template <bool kSink>
+struct Span {
+  int first, n, gap_at, gap;
+  __device__ __forceinline__ int at(int i) const {
+    return first + i + (kSink && i >= gap_at ? gap : 0);
+  }
+};
+// Tokens lo .. hi - 1 (and the first ones).
+template <bool kSink, int kStep>
+__device__ __forceinline__ Span<kSink> span_of(const AttnArgs& a, int lo, int hi) {
+  Span<kSink> s{lo / kStep, 0, 0, 0};
+  const int end = hi > 0 ? (hi - 1) / kStep + 1 : 0;
+  if constexpr (kSink) {
+    const int sinks = min(a.sinks, hi), own = sinks > 0 ? (sinks - 1) / kStep + 1 : 0;
+    s.gap_at = min(own, s.first);
+    s.gap = s.first - s.gap_at;
+    s.first = 0;
+    s.n = max(0, end - s.gap);
+  } else {
+    s.n = max(0, end - s.first);
+  }
+  return s;
 }
 
 }  // namespace strata

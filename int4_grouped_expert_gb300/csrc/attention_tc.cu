@@ -99,6 +99,7 @@ __device__ __forceinline__ int units_of(const AttnArgs& a, const SeqView& v) {
   const int64_t rows = static_cast<int64_t>(v.n) * a.group;
   return rows > a.rows_below ? static_cast<int>((rows + a.tc_rows - 1) / a.tc_rows) * a.c.n_kv_heads : 0;
 }
+template <bool kSink>
 __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
   Units u;
   const int lane = threadIdx.x & 31, per_lane = (a.b.n_seq + 31) / 32;
@@ -110,9 +111,12 @@ __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
     const int n = units_of(a, v);
     // tokens that a unit sees, on average
     float seen = fmaxf(0.f, __fsub_rn(static_cast<float>(v.len), __fmul_rn(0.5f, static_cast<float>(v.n))));
-    if (a.window > 0)
-      seen = fminf(seen, __fadd_rn(static_cast<float>(a.window), __fdiv_rn(static_cast<float>(a.tc_rows),
-                                                                           static_cast<float>(a.group))));
+    if (a.window > 0) {
+      float most_seen = __fadd_rn(static_cast<float>(a.window), __fdiv_rn(static_cast<float>(a.tc_rows),
+                                                                          static_cast<float>(a.group)));
+      if (kSink) most_seen = __fadd_rn(most_seen, static_cast<float>(a.sinks));
+      seen = fminf(seen, most_seen);
+    }
     const float of_unit = __fadd_rn(__fmul_rn(seen, 1.f / kAtTok), 1.f);
     u.mine += n;
     tiles = __fadd_rn(tiles, __fmul_rn(static_cast<float>(n), of_unit));
@@ -148,25 +152,30 @@ __device__ __forceinline__ Units find_units(const AttnArgs& a, bool flag) {
   return u;
 }
 // One unit, and the tiles that its rows see.
+template <bool kSink>
 struct Unit {
   int seq, head, row0, rows;  // first row; rows of the (sequence, head)
   SeqView sv;
-  int tok_lo, tok_hi, j_lo, n_tiles, of;  // tokens tok_lo .. tok_hi - 1
+  int tok_lo, tok_hi, of;  // tokens tok_lo .. tok_hi - 1 (and the first ones)
+  Span<kSink> tiles;
 };
-__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int seq, int head, int row0, int k, int per, bool flag) {
-  Unit u;
+template <bool kSink>
+__device__ __forceinline__ Unit<kSink> unit_of(const AttnArgs& a, int seq, int head, int row0, int k, int per,
+                                               bool flag) {
+  Unit<kSink> u;
   u.seq = seq, u.head = head, u.row0 = row0;
   u.sv = seq_view(a, seq, flag);
   u.rows = u.sv.n * a.group;
   const int p0 = u.sv.len - u.sv.n;  // position of the first query
   u.tok_hi = min(u.sv.len, p0 + (min(row0 + a.tc_rows, u.rows) - 1) / a.group + 1);
   u.tok_lo = first_seen(a, p0 + row0 / a.group);
-  u.j_lo = u.tok_lo / kAtTok;
-  u.n_tiles = u.tok_hi > u.tok_lo ? (u.tok_hi + kAtTok - 1) / kAtTok - u.j_lo : 0;
-  u.of = min(k, max(1, (u.n_tiles + per - 1) / per));
+  u.tiles = span_of<kSink, kAtTok>(a, u.tok_lo, u.tok_hi);
+  if (u.tok_hi <= u.tok_lo) u.tiles.n = 0;
+  u.of = min(k, max(1, (u.tiles.n + per - 1) / per));
   return u;
 }
-__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Units& us, int at) {
+template <bool kSink>
+__device__ __forceinline__ Unit<kSink> find_unit(const AttnArgs& a, const Units& us, int at) {
   const int heads = a.c.n_kv_heads;
   const int owner = __ffs(__ballot_sync(0xffffffffu, at < us.end)) - 1;
   int seq = 0, left = at - (us.end - us.mine), n = 0;
@@ -180,8 +189,8 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs& a, const Units& us, in
   seq = __shfl_sync(0xffffffffu, seq, owner);
   left = __shfl_sync(0xffffffffu, left, owner);
   n = __shfl_sync(0xffffffffu, n, owner);
-  return unit_of(a, seq, left % heads, (n / heads - 1 - left / heads) * a.tc_rows, at < us.whole ? 1 : us.k, us.per,
-                 false);
+  return unit_of<kSink>(a, seq, left % heads, (n / heads - 1 - left / heads) * a.tc_rows, at < us.whole ? 1 : us.k,
+                        us.per, false);
 }
 
 // The largest of 16 scores.
@@ -194,7 +203,8 @@ __device__ __forceinline__ float max16(const uint32_t* x) {
 
 // kGroups: pairs of scales in a tile, 1 where it lies in one page (of 64 or 128 tokens), else one for every 16 tokens.
 // (us, 1 / 4 of them, pages of 64: 2048 queries on 8192 tokens 252 / 268, 8 on 131072 141 / 144, 4096 on 4096 154 / 163.)
-template <int kD, int kGroups>
+// kSink: there is a window, and a.sinks first tokens that stay visible before it.
+template <int kD, int kGroups, bool kSink>
 __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a) {
   using C = AtCfg<kD>;
   constexpr int KC = kD / 64;   // 64-wide pieces of a head
@@ -224,17 +234,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   griddep_launch();
   const int id = blockIdx.x;
   int cut = 0, piece = 0;  // slot of the block's piece, its number among its unit's
-  Unit u;
+  Unit<kSink> u;
   if (a.tc_search) {
-    const Units us = find_units(a, id == 0 && threadIdx.x < 32);
+    const Units us = find_units<kSink>(a, id == 0 && threadIdx.x < 32);
     cut = max(0, id - us.whole);
     const int at = cut > 0 ? us.whole + cut / us.k : id;
     if (at >= us.whole + us.rest) return;
-    u = find_unit(a, us, at);
+    u = find_unit<kSink>(a, us, at);
     piece = cut - max(0, at - us.whole) * us.k;
   } else {  // the same order, as if every sequence had max_q rows
     const int heads = a.c.n_kv_heads, of_seq = gridDim.x / a.b.n_seq, left = id % of_seq;
-    u = unit_of(a, id / of_seq, left % heads, (of_seq / heads - 1 - left / heads) * a.tc_rows, 1, 1,
+    u = unit_of<kSink>(a, id / of_seq, left % heads, (of_seq / heads - 1 - left / heads) * a.tc_rows, 1, 1,
                 left == 0 && threadIdx.x == 0);
     if (u.rows <= a.rows_below || u.row0 >= u.rows) return;
   }
@@ -242,14 +252,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   const SeqView sv = u.sv;
   const int G = a.group;
   const int tok_lo = u.tok_lo;  // before it, and from tok_hi on, nothing is looked up or used
-  int j_lo = u.j_lo, n_tiles = u.n_tiles, tok_hi = u.tok_hi;
+  int n_tiles = u.tiles.n, tok_hi = u.tok_hi;
+  Span<kSink> span = u.tiles;
   if (piece >= of) return;
   if (of > 1) {
     const int from = n_tiles * piece / of, to = n_tiles * (piece + 1) / of;
-    j_lo += from;
+    span.first += from;
+    if (kSink) span.gap_at -= from;
     n_tiles = to - from;
-    tok_hi = min(tok_hi, (j_lo + n_tiles) * kAtTok);
+    if (!kSink) tok_hi = min(tok_hi, (span.first + n_tiles) * kAtTok);
   }
+  auto tile_at = [&](int t) { return span.at(t) * kAtTok; };  // the first token of the piece's tile t
   const int row_end = min(row0 + a.tc_rows, rows);        // the rows from here on are another block's
   const int n_rt = row_end - row0 > 128 ? 2 : 1;          // row tiles in use
   const int P = a.c.page_size;
@@ -325,9 +338,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   // the scales of a tile's groups: a lane a group, of kBatch tiles
   constexpr int kBatch = 32 / kGroups, kWide = kAtTok / kGroups;
   auto scales_of = [&](int batch) {
-    const int t = batch * kBatch + lane / kGroups, tok = (j_lo + t) * kAtTok + lane % kGroups * kWide;
+    const int t = batch * kBatch + lane / kGroups, tok = tile_at(t) + lane % kGroups * kWide;
     float3 x = make_float3(0.f, 1.f, 0.f);
-    if (t < n_tiles && tok < tok_hi && tok + kWide > tok_lo) {
+    if (t < n_tiles && tok < tok_hi && (tok + kWide > tok_lo || (kSink && tok < a.sinks))) {
       const int64_t page = table[tok >> (31 - __clz(P))];
       if (page >= 0 && page < a.c.n_pages) {
         x.x = a.c.k_scales[page * a.c.n_kv_heads + h];
@@ -477,9 +490,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       ok = tc::warp_wait(s_full + 2 * tile + (j & 1), (j >> 1) & 1, abort_flag, a.status);
       if (!ok) break;
       tc::tc_fence_after();
-      const int j0 = (j_lo + j) * kAtTok;
-      // columns lo .. hi of the tile are seen
+      const int j0 = tile_at(j);
+      // columns lo .. hi of the tile are seen (and those below `first`, up to hi)
       const int hi = min(pos, tok_hi - 1) - j0, lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
+      const int first = kSink ? a.sinks - j0 : 0;
+      auto sees = [&](int c) { return c <= hi && (c >= lo || (kSink && c < first)); };
       const float4* scale = s_scale[j % kAtScales];
       // what turns a product into the exponent of 2 (never 0: a masked score, -inf, stays -inf under it)
       float cg[kGroups], lv[kGroups], per_scale;
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         per_scale = s.z;  // (of several groups: looked up again, for want of registers)
         well = well && s.w == 0.f;
       }
-      const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && lo <= 0 && well);
+      const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && (lo <= 0 || (kSink && first >= kAtTok)) && well);
       const bool odd = !whole && !__all_sync(0xffffffffu, well);
       if (odd) {
         float top = small_top, sum = small_sum;
@@ -500,7 +515,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         for (int c = 0; c < kAtTok; ++c) {  // (short code: it is rarely run)
           const float4 sc = scale[c * kGroups / kAtTok];
           const float score = __uint_as_float(tc::tmem_ld1(ts + c));
-          const bool on = sc.w == 3.f && c <= hi && c >= lo;
+          const bool on = sc.w == 3.f && sees(c);
           const float x = on ? score * fmaxf(cmul * sc.x, 1.17549435e-38f) : -INFINITY, before = top;
           top = fmaxf(top, x);
           const float ref = top == -INFINITY ? 0.f : top;
@@ -516,7 +531,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < kAtTok; ++i) {
-          const bool seen = i <= hi && i >= lo;
+          const bool seen = sees(i);
           r[i / 32][i % 32] = seen ? r[i / 32][i % 32] : 0xFF800000u;  // -inf
         }
       }
@@ -525,7 +540,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         for (int i = 0; i < kAtTok; ++i) {
           const float state = scale[i * kGroups / kAtTok].w;
           if (state == 1.f) r[i / 32][i % 32] = 0xFF800000u;
-          if (state == 2.f && i <= hi && i >= lo) r[i / 32][i % 32] = 0x7FC00000u;  // nan
+          if (state == 2.f && sees(i)) r[i / 32][i % 32] = 0x7FC00000u;  // nan
         }
       }
       const float t[4] = {max16(r[0]), max16(r[0] + 16), max16(r[1]), max16(r[1] + 16)};
@@ -651,14 +666,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     // tile ahead
     constexpr int kLast = kAtTok / kGroups - 1;
     const int lo_g = tok_lo & ~kLast, n_g = ((tok_hi - 1) | kLast) + 1 - lo_g;
-    auto seen = [&](int tok) { return static_cast<unsigned>(tok - lo_g) < static_cast<unsigned>(n_g); };
+    const int first_g = kSink ? (min(a.sinks, tok_hi) - 1 | kLast) + 1 : 0;
+    auto seen = [&](int tok) {
+      return static_cast<unsigned>(tok - lo_g) < static_cast<unsigned>(n_g) || (kSink && tok < first_g);
+    };
     auto page_of = [&](int tok) { return seen(tok) ? table[tok >> pshift] : -1; };
-    auto in_span = [&](int tok) { return tok < tok_hi && tok >= tok_lo; };
+    auto in_span = [&](int tok) { return tok < tok_hi && (tok >= tok_lo || (kSink && tok < a.sinks)); };
     auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-    const int k_tok = j_lo * kAtTok + w * 8, v_tok = j_lo * kAtTok + (w & 1) * 32 + tg * 8;
-    int k_page = page_of(k_tok), v_page = page_of(v_tok);
+    const int from = kSink ? 0 : span.first * kAtTok, k_tok = from + w * 8, v_tok = from + (w & 1) * 32 + tg * 8;
+    auto on_from = [&](int j) { return kSink ? tile_at(j) : j * kAtTok; };
+    int k_page = page_of(on_from(0) + k_tok), v_page = page_of(on_from(0) + v_tok);
     auto load_k = [&](int j, uint4 (&x)[KC]) {
-      const int tok = k_tok + j * kAtTok;
+      const int tok = k_tok + on_from(j);
       const bool on = good(k_page);
       const int64_t ph = on ? static_cast<int64_t>(k_page) * a.c.n_kv_heads + h : 0;
       const uint8_t* src = a.c.k_codes + ((ph << pshift) + (tok & (P - 1)) + (lane & 7)) * kD + (lane >> 3) * 16;
@@ -666,17 +685,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       for (int c = 0; c < KC; ++c)
         x[c] = on && in_span(tok + (lane & 7)) ? __ldcg(reinterpret_cast<const uint4*>(src + c * 64))
                                                : make_uint4(0u, 0u, 0u, 0u);
-      k_page = page_of(tok + kAtTok);
+      k_page = page_of(kSink ? k_tok + on_from(j + 1) : tok + kAtTok);
     };
     auto load_v = [&](int j, uint32_t (&x)[8]) {
-      const int tok = v_tok + j * kAtTok;
+      const int tok = v_tok + on_from(j);
       const bool on = good(v_page) && v_on;
       const int64_t ph = on ? static_cast<int64_t>(v_page) * a.c.n_kv_heads + h : 0;
       const uint8_t* src = a.c.v_codes + ((ph << pshift) + (tok & (P - 1))) * kD + (w >> 1) * 32 + dg * 4;
 #pragma unroll
       for (int t = 0; t < 8; ++t)
         x[t] = on && in_span(tok + t) ? __ldcg(reinterpret_cast<const uint32_t*>(src + t * kD)) : 0u;
-      v_page = page_of(tok + kAtTok);
+      v_page = page_of(kSink ? v_tok + on_from(j + 1) : tok + kAtTok);
     };
     auto store_k = [&](uint8_t* dst, const uint4 (&x)[KC]) {
       uint8_t* rowp = dst + (w * 8 + (lane & 7)) * 128;
@@ -761,16 +780,16 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
 // Joins the pieces of the units that were cut: a block takes 16 rows of a unit at a time, so that all SMs read
 // (one SM reads 65 GB/s from L2: the last piece's block took 16 us to join four).
 constexpr int kAtJoinRows = 16;
-template <int kD>
+template <int kD, bool kSink>
 __global__ void __launch_bounds__(kAtJoinRows * kD / 8) attention_tc_join_kernel(AttnArgs a) {
   griddep_wait();
   griddep_launch();
-  const Units us = find_units(a, false);
+  const Units us = find_units<kSink>(a, false);
   if (us.k == 1) return;
   constexpr int SLICES = 256 / kAtJoinRows;
   const int r16 = threadIdx.x % kAtJoinRows, c = threadIdx.x / kAtJoinRows * 2;  // a thread: eight elements of a row
   for (int i = blockIdx.x; i < us.rest * SLICES; i += gridDim.x) {
-    const Unit u = find_unit(a, us, us.whole + i / SLICES);
+    const Unit<kSink> u = find_unit<kSink>(a, us, us.whole + i / SLICES);
     const int r = i % SLICES * kAtJoinRows + r16, row = u.row0 + r;
     if (u.of == 1 || row >= u.rows) continue;
     constexpr int64_t PART = 256 * (kD + 2);
@@ -808,17 +827,18 @@ __global__ void __launch_bounds__(kAtJoinRows * kD / 8) attention_tc_join_kernel
 template <int kD>
 cudaError_t launch_join_t(const AttnArgs& a, int64_t units, cudaStream_t stream) {
   const int64_t slices = units * (256 / kAtJoinRows);
-  return launch_kernel(attention_tc_join_kernel<kD>, dim3(static_cast<unsigned>(std::min<int64_t>(slices, kAtSms * 4))),
+  return launch_kernel(a.sinks > 0 ? attention_tc_join_kernel<kD, true> : attention_tc_join_kernel<kD, false>,
+                       dim3(static_cast<unsigned>(std::min<int64_t>(slices, kAtSms * 4))),
                        dim3(kAtJoinRows * kD / 8), 0, stream, true, a);
 }
 
 template <int kD, int kGroups>
 cudaError_t launch_tc_g(const AttnArgs& a, int64_t grid, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<kD, kGroups>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto kern = a.sinks > 0 ? attention_tc_kernel<kD, kGroups, true> : attention_tc_kernel<kD, kGroups, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(AtCfg<kD>::SMEM));
   if (e != cudaSuccess) return e;
-  return launch_kernel(attention_tc_kernel<kD, kGroups>, dim3(static_cast<unsigned>(grid)), dim3(kAtThreads),
+  return launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(kAtThreads),
                        AtCfg<kD>::SMEM, stream, true, a);
 }
 template <int kD>
@@ -838,14 +858,14 @@ static int64_t most_units(const strata_kv_cache& c, const strata_kv_batch& b, in
 // Pieces that may come to lie in the workspace; 0: no unit is cut. Above one and a half times the SMs the
 // last units fill their gaps by themselves (512 units of 33 tiles: 165 us whole, 178 with 56 cut). Batches
 // that are not cut do without the kernel that joins: 3 us.
-int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int window) {
+int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int window, int sinks) {
   const int64_t units = most_units(c, b, group);
   if (units > kAtSms * 3 / 2) return 0;
   // (of sequences of equal length the units are known)
   const bool equal = b.T == static_cast<int64_t>(b.n_seq) * b.max_q;
   const int64_t rest = units % kAtSms;
   if (equal && (rest == 0 || rest > kAtMostCut)) return 0;
-  const int64_t seen = window > 0 ? std::min<int64_t>(b.max_kv, window + 256 / group) : b.max_kv;
+  const int64_t seen = window > 0 ? std::min<int64_t>(b.max_kv, window + 256 / group + sinks) : b.max_kv;
   // What whole units take, of 128 rows where those start together, against pieces, in tiles as above; of unequal
   // sequences the longest are cut in two at least. (us, whole / cut, 1472 tokens: 64 queries 28.9 / 23.7,
   // 512 queries 29.3 / 40.0.)

@@ -52,6 +52,9 @@ struct KvAppendArgs {
   int T, n_heads, rot_dim, neighbours;
   int rows_per_block;     // rows whose runs one K/V block starts
   uint32_t* status;
+  const float *q_weight, *k_weight;          // of the norms; null: none
+  int64_t q_weight_stride, k_weight_stride;  // from head to head, 0: one row for all
+  float eps;
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int num_sms, cudaStream_t stream);
 
@@ -68,6 +71,7 @@ struct AttnArgs {
   int n_heads, group;     // query heads; query heads per K/V head
   float scale_log2;       // softmax scale * log2(e)
   int window;             // 0: none
+  int sinks;              // tokens that stay visible before the window; 0: none, or no window
   int rows_above;         // attention.cu takes the sequences with at most so many rows per K/V head,
   int rows_below;         // attention_tc.cu those with more
   // attention.cu
@@ -93,7 +97,7 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(const strata_kv_cache& c, const strata_kv_batch& b, int n_heads);
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t stream);
-int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int window);
+int attn_tc_slots(const strata_kv_cache& c, const strata_kv_batch& b, int64_t group, int window, int sinks);
 size_t attn_tc_part_floats(const strata_kv_cache& c, int slots);
 cudaError_t launch_attention_tc(AttnArgs a, cudaStream_t stream);
 cudaError_t launch_attention_tc_join(AttnArgs a, cudaStream_t stream);  // after both others

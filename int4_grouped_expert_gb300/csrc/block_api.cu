@@ -91,6 +91,80 @@ strata_status check_batch(const strata_kv_cache* c, const strata_kv_batch* b, in
   return STRATA_OK;
 }
 
+// Least eps of a norm: squares that fp32 flushes to zero are far below it.
+constexpr float kMinEps = 7.88860905e-31f;  // 2^-100
+
+strata_status check_norm(const strata_qk_norm& n, int head_dim) {
+  if (!std::isfinite(n.eps) || n.eps < kMinEps) return STRATA_ERR_INVALID_ARG;
+  const struct {
+    const float* weight;
+    int64_t stride;
+  } of[2] = {{n.q_weight, n.q_head_stride}, {n.k_weight, n.k_head_stride}};
+  for (const auto& x : of) {
+    if (!x.weight) continue;
+    if (!on(x.weight, 16) || x.stride % 4 || (x.stride != 0 && x.stride < head_dim)) return STRATA_ERR_INVALID_ARG;
+  }
+  return STRATA_OK;
+}
+
+strata_status append(const strata_kv_cache* cache, const strata_qk_norm* norm, const void* q_bf16, int64_t q_stride,
+                     int32_t n_heads, const void* k_bf16, int64_t k_stride,
+                     const void* v_bf16, int64_t v_stride, int64_t T,
+                     const int32_t* slots, const int32_t* positions, const float* rope,
+                     int64_t n_pos, int32_t rot_dim, uint32_t flags, void* q_out,
+                     int64_t q_out_stride, uint32_t* dev_status, strata_stream stream) {
+  const strata_status s = check_cache(cache);
+  if (s != STRATA_OK) return s;
+  if (flags & ~STRATA_ROPE_NEIGHBOURS) return STRATA_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxRows) return STRATA_ERR_SHAPE;
+  if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16) return STRATA_ERR_SHAPE;
+  const bool with_q = q_bf16 || q_out;
+  if (with_q && (n_heads < 1 || n_heads > 1024)) return STRATA_ERR_UNSUPPORTED;
+  if (norm) {
+    const strata_status ns = check_norm(*norm, cache->head_dim);
+    if (ns != STRATA_OK) return ns;
+  }
+  if (T == 0) return STRATA_OK;
+  const int64_t kv_len = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+  const int64_t q_len = static_cast<int64_t>(n_heads) * cache->head_dim;
+  if (!rows_ok(k_bf16, k_stride, kv_len) || !rows_ok(v_bf16, v_stride, kv_len)) return STRATA_ERR_INVALID_ARG;
+  if (with_q && (!rows_ok(q_bf16, q_stride, q_len) || !rows_ok(q_out, q_out_stride, q_len)))
+    return STRATA_ERR_INVALID_ARG;
+  if (with_q && q_bf16 == q_out && q_stride != q_out_stride) return STRATA_ERR_INVALID_ARG;
+  if (!slots || !on(slots, 4) || (dev_status && !on(dev_status, 4))) return STRATA_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!positions || !on(positions, 4) || !rope || !on(rope, 16) || n_pos < 1))
+    return STRATA_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!sm_count(&sms)) return STRATA_ERR_CUDA;
+  KvAppendArgs a{};
+  a.c = *cache;
+  a.q = static_cast<const __nv_bfloat16*>(q_bf16);
+  a.k = static_cast<const __nv_bfloat16*>(k_bf16);
+  a.v = static_cast<const __nv_bfloat16*>(v_bf16);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out_stride = q_out_stride;
+  a.slots = slots;
+  a.positions = positions;
+  a.rope = rope;
+  a.n_pos = n_pos;
+  a.T = static_cast<int>(T);
+  a.n_heads = n_heads;
+  a.rot_dim = rot_dim;
+  a.neighbours = (flags & STRATA_ROPE_NEIGHBOURS) != 0;
+  a.status = dev_status;
+  if (norm) {
+    a.q_weight = norm->q_weight;
+    a.k_weight = norm->k_weight;
+    a.q_weight_stride = norm->q_head_stride;
+    a.k_weight_stride = norm->k_head_stride;
+    a.eps = norm->eps;
+  }
+  return of(launch_kv_append(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 struct AttnLayout {
   size_t counters, part, tc_part, total;
 };
@@ -162,45 +236,19 @@ strata_status strata_kv_append(const strata_kv_cache* cache, const void* q_bf16,
                                const int32_t* slots, const int32_t* positions, const float* rope,
                                int64_t n_pos, int32_t rot_dim, uint32_t flags, void* q_out,
                                int64_t q_out_stride, uint32_t* dev_status, strata_stream stream) {
-  const strata_status s = check_cache(cache);
-  if (s != STRATA_OK) return s;
-  if (flags & ~STRATA_ROPE_NEIGHBOURS) return STRATA_ERR_INVALID_ARG;
-  if (T < 0 || T > kMaxRows) return STRATA_ERR_SHAPE;
-  if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16) return STRATA_ERR_SHAPE;
-  const bool with_q = q_bf16 || q_out;
-  if (with_q && (n_heads < 1 || n_heads > 1024)) return STRATA_ERR_UNSUPPORTED;
-  if (T == 0) return STRATA_OK;
-  const int64_t kv_len = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
-  const int64_t q_len = static_cast<int64_t>(n_heads) * cache->head_dim;
-  if (!rows_ok(k_bf16, k_stride, kv_len) || !rows_ok(v_bf16, v_stride, kv_len)) return STRATA_ERR_INVALID_ARG;
-  if (with_q && (!rows_ok(q_bf16, q_stride, q_len) || !rows_ok(q_out, q_out_stride, q_len)))
-    return STRATA_ERR_INVALID_ARG;
-  if (with_q && q_bf16 == q_out && q_stride != q_out_stride) return STRATA_ERR_INVALID_ARG;
-  if (!slots || !on(slots, 4) || (dev_status && !on(dev_status, 4))) return STRATA_ERR_INVALID_ARG;
-  if (rot_dim > 0 && (!positions || !on(positions, 4) || !rope || !on(rope, 16) || n_pos < 1))
-    return STRATA_ERR_INVALID_ARG;
-  int sms = 0;
-  if (!sm_count(&sms)) return STRATA_ERR_CUDA;
-  KvAppendArgs a{};
-  a.c = *cache;
-  a.q = static_cast<const __nv_bfloat16*>(q_bf16);
-  a.k = static_cast<const __nv_bfloat16*>(k_bf16);
-  a.v = static_cast<const __nv_bfloat16*>(v_bf16);
-  a.q_out = static_cast<__nv_bfloat16*>(q_out);
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.q_out_stride = q_out_stride;
-  a.slots = slots;
-  a.positions = positions;
-  a.rope = rope;
-  a.n_pos = n_pos;
-  a.T = static_cast<int>(T);
-  a.n_heads = n_heads;
-  a.rot_dim = rot_dim;
-  a.neighbours = (flags & STRATA_ROPE_NEIGHBOURS) != 0;
-  a.status = dev_status;
-  return of(launch_kv_append(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return append(cache, nullptr, q_bf16, q_stride, n_heads, k_bf16, k_stride, v_bf16, v_stride, T, slots, positions, rope,
+                n_pos, rot_dim, flags, q_out, q_out_stride, dev_status, stream);
+}
+
+strata_status strata_kv_append_normed(const strata_kv_cache* cache, const strata_qk_norm* norm, const void* q_bf16,
+                                      int64_t q_stride, int32_t n_heads, const void* k_bf16, int64_t k_stride,
+                                      const void* v_bf16, int64_t v_stride, int64_t T, const int32_t* slots,
+                                      const int32_t* positions, const float* rope, int64_t n_pos, int32_t rot_dim,
+                                      uint32_t flags, void* q_out, int64_t q_out_stride, uint32_t* dev_status,
+                                      strata_stream stream) {
+  if (!norm) return STRATA_ERR_INVALID_ARG;
+  return append(cache, norm, q_bf16, q_stride, n_heads, k_bf16, k_stride, v_bf16, v_stride, T, slots, positions, rope,
+                n_pos, rot_dim, flags, q_out, q_out_stride, dev_status, stream);
 }
 
 size_t strata_attention_workspace_size(const strata_kv_cache* cache, const strata_kv_batch* batch,
@@ -215,10 +263,19 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
                                        float scale, int32_t window, uint32_t flags, void* out_bf16,
                                        int64_t out_stride, void* workspace, size_t ws_bytes,
                                        strata_stream stream) {
+  return strata_attention_sinks_forward(cache, batch, q_bf16, q_stride, n_heads, scale, window, 0, flags, out_bf16,
+                                        out_stride, workspace, ws_bytes, stream);
+}
+
+strata_status strata_attention_sinks_forward(const strata_kv_cache* cache, const strata_kv_batch* batch,
+                                             const void* q_bf16, int64_t q_stride, int32_t n_heads, float scale,
+                                             int32_t window, int32_t n_sinks, uint32_t flags, void* out_bf16,
+                                             int64_t out_stride, void* workspace, size_t ws_bytes,
+                                             strata_stream stream) {
   const strata_status s = check_batch(cache, batch, n_heads);
   if (s != STRATA_OK) return s;
   if (flags & ~STRATA_WS_REUSE) return STRATA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || window < 0) return STRATA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || window < 0 || n_sinks < 0) return STRATA_ERR_INVALID_ARG;
   if (batch->n_seq == 0 || batch->T == 0) return STRATA_OK;
   const int64_t q_len = static_cast<int64_t>(n_heads) * cache->head_dim;
   if (!rows_ok(q_bf16, q_stride, q_len) || !rows_ok(out_bf16, out_stride, q_len) || q_bf16 == out_bf16)
@@ -241,12 +298,14 @@ strata_status strata_attention_forward(const strata_kv_cache* cache, const strat
   a.n_heads = n_heads;
   a.group = n_heads / cache->n_kv_heads;
   a.scale_log2 = scale * 1.4426950408889634f;
-  // (a window that no position reaches past is none: below max_kv, position - window stays in 32 bits)
-  a.window = window < batch->max_kv ? window : 0;
+  // (a window that no position reaches past, but for first tokens that stay visible, is none: below max_kv,
+  // position - window stays in 32 bits)
+  a.window = window < batch->max_kv - n_sinks ? window : 0;
+  a.sinks = a.window > 0 ? n_sinks : 0;
   a.part = reinterpret_cast<float*>(base + L.part);
   a.counters = reinterpret_cast<uint32_t*>(base + L.counters);
   // (a window shortens what is seen, and so the pieces; the workspace is laid out for none)
-  a.tc_slots = p.tc ? std::min(p.tc_slots, attn_tc_slots(*cache, *batch, a.group, window)) : 0;
+  a.tc_slots = p.tc ? std::min(p.tc_slots, attn_tc_slots(*cache, *batch, a.group, window, n_sinks)) : 0;
   a.tc_part = reinterpret_cast<float*>(base + L.tc_part);
   a.status = &reinterpret_cast<WsHeader*>(base)->status;
   a.rows_above = a.rows_below = p.stream_rows;

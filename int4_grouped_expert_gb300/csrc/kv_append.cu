@@ -1,5 +1,5 @@
-// Rotation of q and k by position and the append of k and v to a paged cache of e4m3 codes with one
-// power-of-two scale per (page, head).
+// Rotation of q and k by position, after a norm of each head's row where one is asked for (kNorm), and the append of
+// k and v to a paged cache of e4m3 codes with one power-of-two scale per (page, head).
 //
 // A run is a stretch of rows with consecutive slots in one page, found from the slots alone; one block owns a
 // run of one K/V head, so the scale of a (page, head) has one writer and needs no atomics. A row whose position
@@ -80,10 +80,8 @@ __device__ __forceinline__ void to_f32(const uint4& w, float* x) {
   x[0] = bf16_lo_f32(w.x); x[1] = bf16_hi_f32(w.x); x[2] = bf16_lo_f32(w.y); x[3] = bf16_hi_f32(w.y);
   x[4] = bf16_lo_f32(w.z); x[5] = bf16_hi_f32(w.z); x[6] = bf16_lo_f32(w.w); x[7] = bf16_hi_f32(w.w);
 }
-// The 16 elements of a pair of chunks, rotated: fp32, every product and sum rounded once.
-__device__ __forceinline__ void rotated(const uint4& wa, const uint4& wb, const Pair& p, const Turn& t, float (&y)[16]) {
-  to_f32(wa, y);
-  to_f32(wb, y + 8);
+// The 16 elements of a pair of chunks turn: fp32, every product and sum rounded once.
+__device__ __forceinline__ void turn16(const Pair& p, const Turn& t, float (&y)[16]) {
   if (p.kind == 1) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -98,6 +96,59 @@ __device__ __forceinline__ void rotated(const uint4& wa, const uint4& wb, const 
       y[2 * i] = __fsub_rn(__fmul_rn(u, t.c[i]), __fmul_rn(v, t.s[i]));
       y[2 * i + 1] = __fadd_rn(__fmul_rn(v, t.c[i]), __fmul_rn(u, t.s[i]));
     }
+  }
+}
+
+__device__ __forceinline__ void rotated(const uint4& wa, const uint4& wb, const Pair& p, const Turn& t, float (&y)[16]) {
+  to_f32(wa, y);
+  to_f32(wb, y + 8);
+  turn16(p, t, y);
+}
+
+// The norm of a head's row, y = x * inv * weight with inv = 1 / sqrt(mean(x^2) + eps), all in fp32: nothing is rounded to
+// 16 bits before the rotation. The row lies in TPR lanes, 16 elements each; each sums its squares, then
+// the lanes do. Squares of elements from 2^60 on may leave fp32: such a row is summed once more times 2^-68, and
+// its elements are held so from there on (bf16 values times a power of two: exact but for those below 2^-118
+// of the largest). Squares that fp32 flushes are below 2^-49 of eps, which is at least 2^-100. Rows of a warp part ways
+// here, and so may its heads where they end: a row's lanes wait for one another only.
+template <int TPR>
+__device__ __forceinline__ float inv_norm(uint4& wa, uint4& wb, float eps) {
+  const unsigned lanes = ((1u << TPR) - 1u) << (threadIdx.x & 31 & ~(TPR - 1));
+  auto mean = [&] {
+    float x[16], sum = 0.f;
+    to_f32(wa, x);
+    to_f32(wb, x + 8);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+    for (int d = 1; d < TPR; d <<= 1) sum += __shfl_xor_sync(lanes, sum, d);
+    return sum * (1.f / (16 * TPR));
+  };
+  float m = mean();
+  if (!(m < INFINITY)) {  // (the same in all lanes of the row)
+    const float down = exp2i(-68);
+    auto scaled = [&](uint32_t v) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(bf16_lo_f32(v) * down, bf16_hi_f32(v) * down);
+      return *reinterpret_cast<const uint32_t*>(&b);
+    };
+    wa = make_uint4(scaled(wa.x), scaled(wa.y), scaled(wa.z), scaled(wa.w));
+    wb = make_uint4(scaled(wb.x), scaled(wb.y), scaled(wb.z), scaled(wb.w));
+    m = mean();
+    eps = eps * down * down;
+  }
+  return __frsqrt_rn(m + eps);
+}
+__device__ __forceinline__ void normed(const uint4& wa, const uint4& wb, float inv, const float* weight, const Pair& p,
+                                       float (&y)[16]) {
+  to_f32(wa, y);
+  to_f32(wb, y + 8);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(weight) + 2 * (q < 2 ? p.a : p.b) + (q & 1));
+    y[4 * q] = y[4 * q] * inv * w.x;
+    y[4 * q + 1] = y[4 * q + 1] * inv * w.y;
+    y[4 * q + 2] = y[4 * q + 2] * inv * w.z;
+    y[4 * q + 3] = y[4 * q + 3] * inv * w.w;
   }
 }
 
@@ -155,7 +206,7 @@ __device__ __forceinline__ void rescale(uint8_t* codes, int bytes, float ratio) 
 }
 
 // kIter: iterations that a page of rows takes.
-template <int kD, int kIter>
+template <int kD, int kIter, bool kNorm>
 __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int head) {
   constexpr int TPR = kD / 16;              // threads per row
   constexpr int RPI = kAppThreads / TPR;    // rows per iteration
@@ -232,6 +283,16 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     const unsigned bad = __ballot_sync(0xffffffffu, !(finite16(k) && finite16(v)));
     return ((bad >> (lane / TPR * TPR)) & ((1u << TPR) - 1u)) == 0;
   };
+  const float* weight = kNorm && a.k_weight ? a.k_weight + head * a.k_weight_stride : nullptr;
+  float inv[kIter];  // (kNorm) of this thread's row of iteration j
+  auto key = [&](int j, const Turn& t, float (&y)[16]) {
+    if (kNorm && weight) {
+      normed(kw[j][0], kw[j][1], inv[j], weight, kp, y);
+      turn16(kp, t, y);
+    } else {
+      rotated(kw[j][0], kw[j][1], kp, t, y);
+    }
+  };
   float km = 0.f, vm = 0.f;
   unsigned bad_rows = 0;  // bit j: this thread's row of iteration j
 #pragma unroll
@@ -239,7 +300,8 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     if (j * RPI >= n) break;
     float k[16], v[16];
     const int i = j * RPI + ri;
-    rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : skipped >> j & 1u ? none : turn_of(a, kp, row0 + i), k);
+    if (kNorm && weight) inv[j] = inv_norm<TPR>(kw[j][0], kw[j][1], a.eps);
+    key(j, j == 0 ? t_first : skipped >> j & 1u ? none : turn_of(a, kp, row0 + i), k);
     rotated(vw[j][0], vw[j][1], vp, none, v);
     if (good_row(k, v)) {
       km = fmaxf(km, max16(k));
@@ -274,7 +336,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     if (i >= n) break;
     if (skipped >> j & 1u) continue;
     float k[16], v[16];
-    rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : turn_of(a, kp, row0 + i), k);
+    key(j, j == 0 ? t_first : turn_of(a, kp, row0 + i), k);
     rotated(vw[j][0], vw[j][1], vp, none, v);
     const bool ok = !(bad_rows >> j & 1u);
     const uint2 nan8 = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), zero = make_uint2(0u, 0u);
@@ -295,7 +357,7 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
 
 // Queries: a block takes kAppThreads / (kD / 16 * kAppHeads) rows; a thread one pair of chunks of every
 // kAppHeads-th head of a row.
-template <int kD>
+template <int kD, bool kNorm>
 __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block) {
   constexpr int TPR = kD / 16, ROWS = kAppThreads / (TPR * kAppHeads);
   const int r = block * ROWS + threadIdx.x / (TPR * kAppHeads);
@@ -319,7 +381,13 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block)
       const int h = h0 + i * kAppHeads;
       if (h >= a.n_heads) break;
       float y[16];
-      rotated(wa[i], wb[i], p, t, y);
+      if (kNorm && a.q_weight) {
+        const float inv = inv_norm<TPR>(wa[i], wb[i], a.eps);
+        normed(wa[i], wb[i], inv, a.q_weight + h * a.q_weight_stride, p, y);
+        turn16(p, t, y);
+      } else {
+        rotated(wa[i], wb[i], p, t, y);
+      }
       uint32_t o[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -333,12 +401,12 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block)
   }
 }
 
-template <int kD, int kIter>
+template <int kD, int kIter, bool kNorm>
 __global__ void __launch_bounds__(kAppThreads, kIter > 2 ? 1 : 3) kv_append_kernel(KvAppendArgs a, int kv_blocks) {
   griddep_wait();
   griddep_launch();
   if (blockIdx.x >= static_cast<unsigned>(kv_blocks)) {
-    rotate_queries<kD>(a, blockIdx.x - kv_blocks);
+    rotate_queries<kD, kNorm>(a, blockIdx.x - kv_blocks);
     return;
   }
   const int head = blockIdx.x % a.c.n_kv_heads;
@@ -351,7 +419,15 @@ __global__ void __launch_bounds__(kAppThreads, kIter > 2 ? 1 : 3) kv_append_kern
   if ((threadIdx.x & 31) == 0) s_starts[threadIdx.x >> 5] = starts;
   __syncthreads();
   for (int w = 0; w < kAppThreads / 32; ++w)
-    for (unsigned m = s_starts[w]; m; m &= m - 1) append_run<kD, kIter>(a, lo + 32 * w + __ffs(m) - 1, head);
+    for (unsigned m = s_starts[w]; m; m &= m - 1) append_run<kD, kIter, kNorm>(a, lo + 32 * w + __ffs(m) - 1, head);
+}
+
+template <bool kNorm>
+static auto kernel_for(int D, int P) {
+  return D == 64 ? (P <= 64 ? kv_append_kernel<64, 1, kNorm> : kv_append_kernel<64, 2, kNorm>)
+                 : (P <= 32   ? kv_append_kernel<128, 1, kNorm>
+                    : P <= 64 ? kv_append_kernel<128, 2, kNorm>
+                              : kv_append_kernel<128, 4, kNorm>);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a0, int num_sms, cudaStream_t stream) {
@@ -366,10 +442,7 @@ cudaError_t launch_kv_append(const KvAppendArgs& a0, int num_sms, cudaStream_t s
   const int q_rows = kAppThreads / (D / 16 * kAppHeads);
   const int64_t grid = kv_blocks + (a.q ? (a.T + q_rows - 1) / q_rows : 0);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  auto kern = D == 64 ? (P <= 64 ? kv_append_kernel<64, 1> : kv_append_kernel<64, 2>)
-                      : (P <= 32   ? kv_append_kernel<128, 1>
-                         : P <= 64 ? kv_append_kernel<128, 2>
-                                   : kv_append_kernel<128, 4>);
+  auto kern = a.q_weight || a.k_weight ? kernel_for<true>(D, P) : kernel_for<false>(D, P);
   return launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(kAppThreads), 0, stream, true, a,
                        static_cast<int>(kv_blocks));
 }
