@@ -89,7 +89,11 @@ typedef enum {
                                       [0, T_max]; the call ran with no live token */
 #define STRATA_DEV_BAD_SLOT 0x10u /* strata_kv_append: a slot or a position out of range (the row was
                                      skipped); strata_attention_forward: a page index, row range or
-                                     length out of range (what it names was left out) */
+                                     length out of range (what it names was left out);
+                                     strata_kv_pages_*, strata_kv_copy_pages: the same of a page, a
+                                     sequence, a length or a count */
+#define STRATA_DEV_NO_PAGES 0x20u /* strata_kv_pages_extend: too few free pages or rows (the sequences from
+                                     there on got none); strata_kv_pages_compact: the other pool is too small */
 
 #define STRATA_GROUP 128     /* [tuning-moe] §2.1: 128 weights share one scale */
 #define STRATA_MAX_EXPERTS 1024
@@ -518,6 +522,88 @@ strata_status strata_attention_sinks_forward(const strata_kv_cache* cache, const
                                              int32_t window, int32_t n_sinks, uint32_t flags, void* out_bf16,
                                              int64_t out_stride, void* workspace, size_t ws_bytes,
                                              strata_stream stream);
+
+/*
+ * Pages of a cache and who holds them, on the device: the caller owns the arrays, the calls below change them, and a
+ * page number means the same in every cache of a model's layers. Begin with refs and kv_len zero and page_table -1.
+ */
+typedef struct {
+  int32_t n_seq;        /* 0 .. 65535 */
+  int32_t page_size;    /* 16, 32, 64 or 128 */
+  int64_t n_pages;      /* n_pages * page_size <= 2^31 - 1 */
+  int64_t max_pages;    /* pages that a sequence can have; max_pages * page_size <= 2^31 - 1 */
+  int64_t table_stride; /* entries from one sequence's row to the next, >= max_pages */
+  int32_t* page_table;  /* [n_seq, max_pages]: a sequence's pages in order; -1 where there is none: behind its
+                           tokens, or given back */
+  int32_t* kv_len;      /* [n_seq]: tokens of each sequence */
+  int32_t* refs;        /* [n_pages], 16-byte aligned: table entries that name the page; 0: it is free */
+} strata_kv_pages;
+
+/*
+ * strata_kv_pages_extend — room for new_tokens[s] more tokens of each sequence, and their rows: what strata_kv_append
+ * and strata_attention_forward want of them.
+ * Sequence s gets the lowest free pages, the sequences in order, and kv_len[s] grows. Its new tokens are rows
+ * q_start[s] .. q_start[s+1] - 1, at positions from the old length on. An unfinished page that other sequences
+ * hold too is left to them: its place in the table gets a free page, and the pair (old page, new page) is listed
+ * in copies, to be copied (strata_kv_copy_pages) before the append.
+ * new_tokens  [n_seq] int32, >= 0.           T_max  rows of slots and positions, up to 2^22.
+ * slots, positions [T_max], q_start [n_seq + 1], copies [n_seq, 2], n_copies [1]: int32, written; rows
+ *             without a token get slot -1 (padding of strata_kv_append) and position 0, copies from n_copies on keep
+ *             what they hold.
+ * From the first sequence on for which free pages or rows run out, no sequence gets any (STRATA_DEV_NO_PAGES); one with a
+ * negative count, more tokens than its table holds, or an unfinished page that is none or that nobody counts gets
+ * nothing (STRATA_DEV_BAD_SLOT): its length stays. dev_status here and below: device uint32 or NULL.
+ */
+strata_status strata_kv_pages_extend(const strata_kv_pages* pages, const int32_t* new_tokens, int64_t T_max,
+                                     int32_t* slots, int32_t* positions, int32_t* q_start, int32_t* copies,
+                                     int32_t* n_copies, uint32_t* dev_status, strata_stream stream);
+
+/*
+ * strata_kv_pages_fork — sequences that go on from where another one is: each s with parent[s] >= 0 takes that
+ * sequence's length and pages, which both hold from then on (refs grows; nothing is copied before one of them is
+ * extended). parent [n_seq] int32, -1: s stays as it is. s has to be empty (kv_len 0), and its parent may not have a
+ * parent in the same call; otherwise, or for a parent >= n_seq, STRATA_DEV_BAD_SLOT is set and s stays as it is.
+ */
+strata_status strata_kv_pages_fork(const strata_kv_pages* pages, const int32_t* parent, uint32_t* dev_status,
+                                   strata_stream stream);
+
+/*
+ * strata_kv_pages_release — gives pages back: their table entries become -1, and a page is free when nobody holds it.
+ * keep [n_seq] int32 or NULL: sequence s is cut to min(kv_len[s], keep[s]) tokens (0: it ends), unless keep[s] < 0.
+ * window > 0: of every sequence the pages that lie whole between its n_sinks first tokens and the window of its next
+ * query (at position kv_len) go too: what strata_attention_sinks_forward with these numbers does not look at in later
+ * calls. (Rows that are in the cache already and still to be attended to have earlier windows: release after them.)
+ */
+strata_status strata_kv_pages_release(const strata_kv_pages* pages, const int32_t* keep, int32_t window, int32_t n_sinks,
+                                      uint32_t* dev_status, strata_stream stream);
+
+/*
+ * strata_kv_pages_compact — the same sequences in another pool, a smaller or larger one: pages in use get the numbers
+ * 0, 1, ... in the order of their old ones. dst's table, lengths and refs are written whole; copies
+ * [dst->n_pages, 2] lists the pairs (old page, new page) and n_copies [1] their number, for
+ * strata_kv_copy_pages from the caches of src to those of dst. src is not changed. n_seq and page_size are the same,
+ * dst->max_pages >= src's (STRATA_ERR_SHAPE otherwise), and no array serves both (STRATA_ERR_INVALID_ARG).
+ * If more pages are in use than dst has, dst is left empty and STRATA_DEV_NO_PAGES is set. An entry that names no
+ * page or one that nobody counts becomes -1 (STRATA_DEV_BAD_SLOT).
+ * workspace >= strata_kv_pages_compact_workspace_size(src) bytes (0: src is invalid), 256-byte aligned.
+ */
+size_t strata_kv_pages_compact_workspace_size(const strata_kv_pages* src);
+strata_status strata_kv_pages_compact(const strata_kv_pages* src, const strata_kv_pages* dst, int32_t* copies,
+                                      int32_t* n_copies, void* workspace, size_t ws_bytes, uint32_t* dev_status,
+                                      strata_stream stream);
+
+/*
+ * strata_kv_copy_pages — copies whole pages, codes and scales: for each pair i < n_copies, page copies[i][0] of src[c] to
+ * page copies[i][1] of dst[c], for all n_caches caches c (up to 1024, host arrays; the layers of a model).
+ * copies [max_copies, 2], n_copies [1] or NULL (max_copies): int32, device. A pair with a negative page is no copy; one
+ * with a page out of range, or a count outside 0 .. max_copies, sets STRATA_DEV_BAD_SLOT (no copy; the count is
+ * cut). The pages written differ from one another and, where dst is src, from those read: the order of copies is
+ * not defined. All caches have the same n_kv_heads, head_dim and page_size, those of src and those of dst each the
+ * same n_pages (STRATA_ERR_SHAPE otherwise). dst may be src.
+ */
+strata_status strata_kv_copy_pages(const strata_kv_cache* src, const strata_kv_cache* dst, int32_t n_caches,
+                                   const int32_t* copies, const int32_t* n_copies, int64_t max_copies,
+                                   uint32_t* dev_status, strata_stream stream);
 
 /*
  * Device status of a route/forward workspace: synchronizes `stream`, returns the status word in

@@ -30,6 +30,7 @@ STRATA_DEV_BAD_ID = 0x2
 STRATA_DEV_TIMEOUT = 0x4
 STRATA_DEV_BAD_TOKENS = 0x8
 STRATA_DEV_BAD_SLOT = 0x10
+STRATA_DEV_NO_PAGES = 0x20
 STRATA_ERR_DEVICE_STATUS = 6
 STRATA_ERR_TIMEOUT = 7
 GROUP_WORKSPACE_BYTES = 256
@@ -87,6 +88,13 @@ class strata_kv_batch(ctypes.Structure):
                 ("table_stride", ctypes.c_int64)]
 
 
+class strata_kv_pages(ctypes.Structure):
+    """Mirror of the C struct strata_kv_pages."""
+    _fields_ = [("n_seq", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("refs", ctypes.c_void_p)]
+
+
 _lib = None
 _byref = ctypes.byref
 _P = ctypes.c_void_p
@@ -140,6 +148,14 @@ _SIGNATURES = {
     "strata_attention_sinks_forward": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache),
                                                       ctypes.POINTER(strata_kv_batch), _P, _I64, _I32,
                                                       _F32, _I32, _I32, _U32, _P, _I64, _P, _SZ, _P]),
+    "strata_kv_pages_extend": (ctypes.c_int, [ctypes.POINTER(strata_kv_pages), _P, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "strata_kv_pages_fork": (ctypes.c_int, [ctypes.POINTER(strata_kv_pages), _P, _P, _P]),
+    "strata_kv_pages_release": (ctypes.c_int, [ctypes.POINTER(strata_kv_pages), _P, _I32, _I32, _P, _P]),
+    "strata_kv_pages_compact_workspace_size": (_SZ, [ctypes.POINTER(strata_kv_pages)]),
+    "strata_kv_pages_compact": (ctypes.c_int, [ctypes.POINTER(strata_kv_pages), ctypes.POINTER(strata_kv_pages), _P, _P,
+                                               _P, _SZ, _P, _P]),
+    "strata_kv_copy_pages": (ctypes.c_int, [ctypes.POINTER(strata_kv_cache), ctypes.POINTER(strata_kv_cache), _I32, _P,
+                                            _P, _I64, _P, _P]),
     "strata_workspace_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(_U32)]),
     "strata_read_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(_U32)]),
 }
@@ -396,6 +412,47 @@ def strata_attention_sinks_forward(cache: strata_kv_cache, batch: strata_kv_batc
         ptr(workspace), ws_bytes, stream_handle(stream))
 
 
+def strata_kv_pages_extend(pages: strata_kv_pages, new_tokens, T_max, slots, positions, q_start, copies, n_copies,
+                           dev_status=None, stream=None):
+    return (_lib or lib()).strata_kv_pages_extend(
+        _byref(pages), ptr(new_tokens), T_max, ptr(slots), ptr(positions), ptr(q_start), ptr(copies), ptr(n_copies),
+        None if dev_status is None else ptr(dev_status), stream_handle(stream))
+
+
+def strata_kv_pages_fork(pages: strata_kv_pages, parent, dev_status=None, stream=None):
+    return (_lib or lib()).strata_kv_pages_fork(_byref(pages), ptr(parent),
+                                                None if dev_status is None else ptr(dev_status), stream_handle(stream))
+
+
+def strata_kv_pages_release(pages: strata_kv_pages, keep=None, window=0, n_sinks=0, dev_status=None, stream=None):
+    return (_lib or lib()).strata_kv_pages_release(_byref(pages), None if keep is None else ptr(keep), window, n_sinks,
+                                                   None if dev_status is None else ptr(dev_status),
+                                                   stream_handle(stream))
+
+
+def strata_kv_pages_compact_workspace_size(src: strata_kv_pages) -> int:
+    return lib().strata_kv_pages_compact_workspace_size(ctypes.byref(src))
+
+
+def strata_kv_pages_compact(src: strata_kv_pages, dst: strata_kv_pages, copies, n_copies, workspace, ws_bytes,
+                            dev_status=None, stream=None):
+    return (_lib or lib()).strata_kv_pages_compact(
+        _byref(src), _byref(dst), ptr(copies), ptr(n_copies), ptr(workspace), ws_bytes,
+        None if dev_status is None else ptr(dev_status), stream_handle(stream))
+
+
+def strata_kv_copy_pages(src, dst, copies, n_copies, max_copies, dev_status=None, stream=None):
+    """src, dst: arrays of descriptors (cache_array), or one strata_kv_cache each."""
+    n = 1 if isinstance(src, strata_kv_cache) else len(src)
+    if n != (1 if isinstance(dst, strata_kv_cache) else len(dst)):
+        raise ValueError("as many caches to copy to as to copy from expected")
+    return (_lib or lib()).strata_kv_copy_pages(
+        _byref(src) if isinstance(src, strata_kv_cache) else src,
+        _byref(dst) if isinstance(dst, strata_kv_cache) else dst, n, ptr(copies),
+        None if n_copies is None else ptr(n_copies), max_copies, None if dev_status is None else ptr(dev_status),
+        stream_handle(stream))
+
+
 def strata_workspace_status(workspace, stream=None):
     v = _U32(0)
     st = lib().strata_workspace_status(ptr(workspace), stream_handle(stream), ctypes.byref(v))
@@ -409,4 +466,5 @@ def strata_read_status(dev_status, stream=None):
 
 
 from .layer import MoELayer  # noqa: E402,F401
-from .attention import PagedKVCache, QKNorm, QuantLinear, kv_batch, rope_table  # noqa: E402,F401
+from .attention import (PagedKVCache, PageTable, QKNorm, QuantLinear, cache_array,  # noqa: E402,F401
+                        kv_batch, rope_table)  # noqa: E402,F401

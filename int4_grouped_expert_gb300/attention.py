@@ -1,15 +1,15 @@
 """Device storage of the attention half of a decoder block, and its C descriptors.
 
 QuantLinear holds one projection's codes and scales, PagedKVCache the pages of
-8-bit keys and values, QKNorm the weights of the norms of queries and keys, kv_batch the
-lengths and page tables of one call. All hold torch tensors (for device memory only) and fill the C structs with their
+8-bit keys and values, PageTable who holds them, QKNorm the weights of the norms of queries and
+keys, kv_batch the lengths and page tables of one call. All hold torch tensors (for device memory only) and fill the C structs with their
 addresses; the arithmetic runs in the library, which sees addresses only: element
 types and layouts are checked here.
 """
 from __future__ import annotations
 
-from . import (GROUP, StrataError, check, ptr, strata_kv_batch, strata_kv_cache, strata_linear,
-               strata_linear_workspace_size, strata_qk_norm, strata_quantize_groups_bits, strata_read_status)
+from . import (GROUP, StrataError, check, ptr, strata_kv_batch, strata_kv_cache, strata_kv_pages,
+               strata_linear, strata_linear_workspace_size, strata_qk_norm, strata_quantize_groups_bits, strata_read_status)
 
 
 def _held(t, name: str, dtype: str, numel: int):
@@ -104,6 +104,47 @@ class PagedKVCache:
         return self._struct
 
 
+def cache_array(caches):
+    """A C array of the descriptors of several PagedKVCache (the layers of a model), which it keeps alive."""
+    arr = (strata_kv_cache * len(caches))(*(c.struct() for c in caches))
+    arr.tensors = list(caches)
+    return arr
+
+
+class PageTable:
+    """Who holds which pages of a pool: page_table [n_seq, max_pages], kv_len [n_seq] and refs [n_pages], int32 on the
+    device. Empty (-1, 0, 0) unless tensors are given; rows of a given page_table may lie apart."""
+
+    def __init__(self, n_pages: int, n_seq: int, max_pages: int, page_size: int, page_table=None, kv_len=None, refs=None,
+                 device: str = "cuda"):
+        import torch
+        self.n_pages, self.n_seq, self.max_pages, self.page_size = n_pages, n_seq, max_pages, page_size
+        ints = dict(dtype=torch.int32, device=device)
+        if page_table is None:
+            page_table = torch.full((n_seq, max_pages), -1, **ints)
+        elif tuple(page_table.shape) != (n_seq, max_pages):
+            raise ValueError(f"page_table {tuple(page_table.shape)}: ({n_seq}, {max_pages}) expected")
+        for row in page_table[:1]:
+            _held(row, "page_table", "int32", max_pages)
+        if n_seq > 1 and page_table.stride(0) < max_pages:
+            raise ValueError(f"page_table: rows {page_table.stride(0)} apart, {max_pages} entries each")
+        self.page_table = page_table
+        self.kv_len = torch.zeros(n_seq, **ints) if kv_len is None else _held(kv_len, "kv_len", "int32", n_seq)
+        self.refs = torch.zeros(n_pages, **ints) if refs is None else _held(refs, "refs", "int32", n_pages)
+        s = strata_kv_pages()
+        s.n_seq, s.page_size, s.n_pages, s.max_pages = n_seq, page_size, n_pages, max_pages
+        s.table_stride = page_table.stride(0) if n_seq > 1 else max_pages
+        s.page_table, s.kv_len, s.refs = ptr(self.page_table), ptr(self.kv_len), ptr(self.refs)
+        self._struct = s
+
+    def struct(self) -> strata_kv_pages:
+        return self._struct
+
+    def batch(self, q_start, T: int, max_q: int, max_kv: int) -> strata_kv_batch:
+        """kv_batch over these sequences: rows as strata_kv_pages_extend lays them out."""
+        return kv_batch(q_start, self.kv_len, self.page_table, T, max_q, max_kv)
+
+
 class QKNorm:
     """Norms of queries and keys for each head: fp32 weights, one row [head_dim] (or [1, head_dim]) for all heads
     or [heads, head_dim] with a row each, or None where there is no norm. eps is added to the mean of squares."""
@@ -154,4 +195,4 @@ def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device: str = "c
     return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous().to(device)
 
 
-__all__ = ["QuantLinear", "PagedKVCache", "QKNorm", "kv_batch", "rope_table"]
+__all__ = ["QuantLinear", "PagedKVCache", "PageTable", "QKNorm", "cache_array", "kv_batch", "rope_table"]

@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "block.cuh"
+#include "pages.cuh"
 
 namespace strata {
 namespace {
@@ -165,6 +166,32 @@ strata_status append(const strata_kv_cache* cache, const strata_qk_norm* norm, c
   return of(launch_kv_append(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+strata_status check_pages(const strata_kv_pages* p) {
+  if (!p) return STRATA_ERR_INVALID_ARG;
+  if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
+    return STRATA_ERR_UNSUPPORTED;
+  if (p->n_seq < 0 || p->n_seq > 65535 || p->n_pages < 0 || p->n_pages > 0x7FFFFFFF / p->page_size ||
+      p->max_pages < 0 || p->max_pages > 0x7FFFFFFF / p->page_size || p->table_stride < p->max_pages)
+    return STRATA_ERR_SHAPE;
+  if ((p->n_seq > 0 && (!p->kv_len || (p->max_pages > 0 && !p->page_table))) || (p->n_pages > 0 && !p->refs))
+    return STRATA_ERR_INVALID_ARG;
+  if (!on(p->page_table, 4) || !on(p->kv_len, 4) || !on(p->refs, 16)) return STRATA_ERR_INVALID_ARG;
+  return STRATA_OK;
+}
+// A word or array that a call writes or reads
+bool ints_ok(const void* p) { return p && on(p, 4); }
+
+// Caches of one shape: heads, head_dim, page_size and n_pages as the first one's
+strata_status check_caches(const strata_kv_cache* c, int n, int64_t heads, int dim, int page_size) {
+  for (int i = 0; i < n; ++i) {
+    const strata_status s = check_cache(c + i);
+    if (s != STRATA_OK) return s;
+    if (c[i].n_kv_heads != heads || c[i].head_dim != dim || c[i].page_size != page_size || c[i].n_pages != c[0].n_pages)
+      return STRATA_ERR_SHAPE;
+  }
+  return STRATA_OK;
+}
+
 struct AttnLayout {
   size_t counters, part, tc_part, total;
 };
@@ -316,6 +343,120 @@ strata_status strata_attention_sinks_forward(const strata_kv_cache* cache, const
   a.beside = p.tc;
   if (p.stream_rows > 0 && launch_attention(a, p, st) != cudaSuccess) return STRATA_ERR_CUDA;
   return a.tc_slots > 0 ? of(launch_attention_tc_join(a, st)) : STRATA_OK;
+}
+
+strata_status strata_kv_pages_extend(const strata_kv_pages* pages, const int32_t* new_tokens, int64_t T_max,
+                                     int32_t* slots, int32_t* positions, int32_t* q_start, int32_t* copies,
+                                     int32_t* n_copies, uint32_t* dev_status, strata_stream stream) {
+  const strata_status s = check_pages(pages);
+  if (s != STRATA_OK) return s;
+  if (T_max < 0 || T_max > kMaxRows) return STRATA_ERR_SHAPE;
+  if (!ints_ok(q_start) || !ints_ok(n_copies) || (dev_status && !on(dev_status, 4))) return STRATA_ERR_INVALID_ARG;
+  if (T_max > 0 && (!ints_ok(slots) || !ints_ok(positions))) return STRATA_ERR_INVALID_ARG;
+  if (pages->n_seq > 0 && (!ints_ok(new_tokens) || !ints_ok(copies))) return STRATA_ERR_INVALID_ARG;
+  PagesExtendArgs a{};
+  a.p = *pages;
+  a.new_tokens = new_tokens;
+  a.T_max = static_cast<int>(T_max);
+  a.slots = slots;
+  a.positions = positions;
+  a.q_start = q_start;
+  a.copies = copies;
+  a.n_copies = n_copies;
+  a.status = dev_status;
+  return of(launch_pages_extend(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+strata_status strata_kv_pages_fork(const strata_kv_pages* pages, const int32_t* parent, uint32_t* dev_status,
+                                   strata_stream stream) {
+  const strata_status s = check_pages(pages);
+  if (s != STRATA_OK) return s;
+  if (dev_status && !on(dev_status, 4)) return STRATA_ERR_INVALID_ARG;
+  if (pages->n_seq == 0) return STRATA_OK;
+  if (!ints_ok(parent)) return STRATA_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!sm_count(&sms)) return STRATA_ERR_CUDA;
+  return of(launch_pages_fork({*pages, parent, dev_status}, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+strata_status strata_kv_pages_release(const strata_kv_pages* pages, const int32_t* keep, int32_t window, int32_t n_sinks,
+                                      uint32_t* dev_status, strata_stream stream) {
+  const strata_status s = check_pages(pages);
+  if (s != STRATA_OK) return s;
+  if (window < 0 || n_sinks < 0 || (dev_status && !on(dev_status, 4)) || (keep && !on(keep, 4)))
+    return STRATA_ERR_INVALID_ARG;
+  if (pages->n_seq == 0 || pages->max_pages == 0 || (!keep && window == 0)) return STRATA_OK;
+  int sms = 0;
+  if (!sm_count(&sms)) return STRATA_ERR_CUDA;
+  return of(launch_pages_release({*pages, keep, window, n_sinks, dev_status}, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t strata_kv_pages_compact_workspace_size(const strata_kv_pages* src) {
+  if (check_pages(src) != STRATA_OK) return 0;
+  return round_up(sizeof(WsHeader) + sizeof(int32_t) * src->n_pages);
+}
+
+strata_status strata_kv_pages_compact(const strata_kv_pages* src, const strata_kv_pages* dst, int32_t* copies,
+                                      int32_t* n_copies, void* workspace, size_t ws_bytes, uint32_t* dev_status,
+                                      strata_stream stream) {
+  strata_status s = check_pages(src);
+  if (s == STRATA_OK) s = check_pages(dst);
+  if (s != STRATA_OK) return s;
+  if (src->n_seq != dst->n_seq || src->page_size != dst->page_size || dst->max_pages < src->max_pages)
+    return STRATA_ERR_SHAPE;
+  if ((src->page_table && src->page_table == dst->page_table) || (src->kv_len && src->kv_len == dst->kv_len) ||
+      (src->refs && src->refs == dst->refs))
+    return STRATA_ERR_INVALID_ARG;
+  if (!ints_ok(n_copies) || (dst->n_pages > 0 && !ints_ok(copies)) || (dev_status && !on(dev_status, 4)))
+    return STRATA_ERR_INVALID_ARG;
+  if (!workspace || !on(workspace, kWsAlign) || ws_bytes < strata_kv_pages_compact_workspace_size(src))
+    return STRATA_ERR_WORKSPACE;
+  int sms = 0;
+  if (!sm_count(&sms)) return STRATA_ERR_CUDA;
+  PagesCompactArgs a{};
+  a.src = *src;
+  a.dst = *dst;
+  a.copies = copies;
+  a.n_copies = n_copies;
+  a.live = &static_cast<WsHeader*>(workspace)->nseg;
+  a.map = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + sizeof(WsHeader));
+  a.status = dev_status;
+  return of(launch_pages_compact(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+strata_status strata_kv_copy_pages(const strata_kv_cache* src, const strata_kv_cache* dst, int32_t n_caches,
+                                   const int32_t* copies, const int32_t* n_copies, int64_t max_copies,
+                                   uint32_t* dev_status, strata_stream stream) {
+  if (n_caches < 0 || n_caches > 1024 || max_copies < 0 || max_copies > 0x7FFFFFFF / 16) return STRATA_ERR_SHAPE;
+  if (n_caches > 0 && (!src || !dst)) return STRATA_ERR_INVALID_ARG;
+  if (n_caches > 0) {
+    strata_status s = check_caches(src, n_caches, src->n_kv_heads, src->head_dim, src->page_size);
+    if (s == STRATA_OK) s = check_caches(dst, n_caches, src->n_kv_heads, src->head_dim, src->page_size);
+    if (s != STRATA_OK) return s;
+  }
+  if ((n_copies && !on(n_copies, 4)) || (dev_status && !on(dev_status, 4))) return STRATA_ERR_INVALID_ARG;
+  if (n_caches == 0 || max_copies == 0) return STRATA_OK;
+  if (!ints_ok(copies)) return STRATA_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!sm_count(&sms)) return STRATA_ERR_CUDA;
+  CopyPagesArgs a{};
+  a.n_kv_heads = src->n_kv_heads;
+  a.page_bytes = static_cast<int64_t>(src->n_kv_heads) * src->page_size * src->head_dim;
+  a.src_pages = src->n_pages;
+  a.dst_pages = dst->n_pages;
+  a.copies = copies;
+  a.n_copies = n_copies;
+  a.max_copies = static_cast<int>(max_copies);
+  a.status = dev_status;
+  for (int at = 0; at < n_caches; at += kCopyCaches) {
+    a.n_caches = std::min(n_caches - at, kCopyCaches);
+    for (int i = 0; i < a.n_caches; ++i) {
+      const strata_kv_cache &x = src[at + i], &y = dst[at + i];
+      a.cache[i] = {x.k_codes, x.v_codes, x.k_scales, x.v_scales, y.k_codes, y.v_codes, y.k_scales, y.v_scales};
+    }
+    if (launch_copy_pages(a, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return STRATA_ERR_CUDA;
+  }
+  return STRATA_OK;
 }
 
 }  // extern "C"
