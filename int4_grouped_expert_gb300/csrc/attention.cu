@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
     for (int u = 0; u < 2; ++u) {
       const int j = j0 + 16 * u;
       int page = -1;
-      if (j < hi && (j + 16 > lo || (kSink && j < a.sinks))) {
+      if (j < hi && (kSink ? j + 16 > lo || j < a.sinks : j + 16 > lo)) {
         page = input(a, table + (j >> pshift));
         if (page < 0 || page >= a.c.n_pages) {
           if (lane == 0) set_status(a.status, STRATA_DEV_BAD_SLOT);
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
       for (int i = 0; i < NI / 2; ++i) {
         const int r = lane / PIECES + RPI * i;
         const uint32_t dst = slot + slot_offset<kD>(16 * u + r, lane % PIECES);
-        const bool on = (r >= m || (kSink && j + r < a.sinks)) && r < n;
+        const bool on = (kSink ? r >= m || j + r < a.sinks : r >= m) && r < n;
         const int64_t at = on ? base + i * 512 : 0;
         copy16(dst, a.c.k_codes + at, on);
         copy16(dst + KB, a.c.v_codes + at, on);
@@ -464,8 +464,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
           for (int n = 0; n < kNT; ++n) mma_add(sc[n][u], A, qf[n][4 * w + j][0], qf[n][4 * w + j][1]);
         }
     }
-    const bool whole = (j0 >= (a.window > 0 ? p_hi - a.window + 1 : 0) || (kSink && j0 + kAttStep <= a.sinks)) &&
-                       j0 + kAttStep - 1 <= p_lo && j0 + kAttStep <= hi && !lost;
+    const int from = a.window > 0 ? p_hi - a.window + 1 : 0;  // (the last row's window)
+    const bool whole = (kSink ? j0 >= from || j0 + kAttStep <= a.sinks : j0 >= from) && j0 + kAttStep - 1 <= p_lo &&
+                       j0 + kAttStep <= hi && !lost;
     // exponents relative to the reference (in use or 0)
     bool over = false;
 #pragma unroll
@@ -481,8 +482,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
             if (!whole) {
               const int r = tok_g + 8 * i, j = j0 + 16 * u + r;
               const int pos = p_lo + static_cast<int>(after >> (16 * n + 8 * c) & 255u);
-              const bool seen = j < hi && j <= pos &&
-                                (a.window <= 0 || j > pos - a.window || (kSink && j < a.sinks)) && !(lost >> u & 1);
+              const bool near = a.window <= 0 || j > pos - a.window;
+              const bool seen = j < hi && j <= pos && (kSink ? near || j < a.sinks : near) && !(lost >> u & 1);
               if (!seen) x = -INFINITY;
             }
             sc[n][u][2 * i + c] = x;

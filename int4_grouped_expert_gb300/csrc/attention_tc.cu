@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     n_tiles = to - from;
     if (!kSink) tok_hi = min(tok_hi, (span.first + n_tiles) * kAtTok);
   }
-  auto tile_at = [&](int t) { return span.at(t) * kAtTok; };  // the first token of the piece's tile t
+  const int j_lo = span.first;
+  auto tile_at = [&](int t) { return (kSink ? span.at(t) : j_lo + t) * kAtTok; };  // the first token of the piece's tile t
   const int row_end = min(row0 + a.tc_rows, rows);        // the rows from here on are another block's
   const int n_rt = row_end - row0 > 128 ? 2 : 1;          // row tiles in use
   const int P = a.c.page_size;
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
   auto scales_of = [&](int batch) {
     const int t = batch * kBatch + lane / kGroups, tok = tile_at(t) + lane % kGroups * kWide;
     float3 x = make_float3(0.f, 1.f, 0.f);
-    if (t < n_tiles && tok < tok_hi && (tok + kWide > tok_lo || (kSink && tok < a.sinks))) {
+    if (t < n_tiles && tok < tok_hi && (kSink ? tok + kWide > tok_lo || tok < a.sinks : tok + kWide > tok_lo)) {
       const int64_t page = table[tok >> (31 - __clz(P))];
       if (page >= 0 && page < a.c.n_pages) {
         x.x = a.c.k_scales[page * a.c.n_kv_heads + h];
@@ -494,7 +495,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       // columns lo .. hi of the tile are seen (and those below `first`, up to hi)
       const int hi = min(pos, tok_hi - 1) - j0, lo = a.window > 0 ? pos - a.window + 1 - j0 : 0;
       const int first = kSink ? a.sinks - j0 : 0;
-      auto sees = [&](int c) { return c <= hi && (c >= lo || (kSink && c < first)); };
+      auto sees = [hi, lo, first](int c) {
+        return kSink ? c <= hi && (c >= lo || c < first) : c <= hi && c >= lo;
+      };
       const float4* scale = s_scale[j % kAtScales];
       // what turns a product into the exponent of 2 (never 0: a masked score, -inf, stays -inf under it)
       float cg[kGroups], lv[kGroups], per_scale;
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
         per_scale = s.z;  // (of several groups: looked up again, for want of registers)
         well = well && s.w == 0.f;
       }
-      const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && (lo <= 0 || (kSink && first >= kAtTok)) && well);
+      const bool whole = __all_sync(0xffffffffu, hi >= kAtTok - 1 && (kSink ? lo <= 0 || first >= kAtTok : lo <= 0) && well);
       const bool odd = !whole && !__all_sync(0xffffffffu, well);
       if (odd) {
         float top = small_top, sum = small_sum;
@@ -668,12 +671,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
     const int lo_g = tok_lo & ~kLast, n_g = ((tok_hi - 1) | kLast) + 1 - lo_g;
     const int first_g = kSink ? (min(a.sinks, tok_hi) - 1 | kLast) + 1 : 0;
     auto seen = [&](int tok) {
-      return static_cast<unsigned>(tok - lo_g) < static_cast<unsigned>(n_g) || (kSink && tok < first_g);
+      const bool in = static_cast<unsigned>(tok - lo_g) < static_cast<unsigned>(n_g);
+      return kSink ? in || tok < first_g : in;
     };
     auto page_of = [&](int tok) { return seen(tok) ? table[tok >> pshift] : -1; };
-    auto in_span = [&](int tok) { return tok < tok_hi && (tok >= tok_lo || (kSink && tok < a.sinks)); };
+    auto in_span = [&](int tok) { return tok < tok_hi && (kSink ? tok >= tok_lo || tok < a.sinks : tok >= tok_lo); };
     auto good = [&](int page) { return page >= 0 && page < a.c.n_pages; };
-    const int from = kSink ? 0 : span.first * kAtTok, k_tok = from + w * 8, v_tok = from + (w & 1) * 32 + tg * 8;
+    const int from = kSink ? 0 : j_lo * kAtTok, k_tok = from + w * 8, v_tok = from + (w & 1) * 32 + tg * 8;
     auto on_from = [&](int j) { return kSink ? tile_at(j) : j * kAtTok; };
     int k_page = page_of(on_from(0) + k_tok), v_page = page_of(on_from(0) + v_tok);
     auto load_k = [&](int j, uint4 (&x)[KC]) {

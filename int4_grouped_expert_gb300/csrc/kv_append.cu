@@ -138,18 +138,18 @@ __device__ __forceinline__ float inv_norm(uint4& wa, uint4& wb, float eps) {
   }
   return __frsqrt_rn(m + eps);
 }
-__device__ __forceinline__ void normed(const uint4& wa, const uint4& wb, float inv, const float* weight, const Pair& p,
-                                       float (&y)[16]) {
+__device__ __forceinline__ void load_weights(const float* weight, const Pair& p, float (&w)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(weight) + 2 * (q < 2 ? p.a : p.b) + (q & 1));
+    w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
+  }
+}
+__device__ __forceinline__ void normed(const uint4& wa, const uint4& wb, float inv, const float (&w)[16], float (&y)[16]) {
   to_f32(wa, y);
   to_f32(wb, y + 8);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(weight) + 2 * (q < 2 ? p.a : p.b) + (q & 1));
-    y[4 * q] = y[4 * q] * inv * w.x;
-    y[4 * q + 1] = y[4 * q + 1] * inv * w.y;
-    y[4 * q + 2] = y[4 * q + 2] * inv * w.z;
-    y[4 * q + 3] = y[4 * q + 3] * inv * w.w;
-  }
+  for (int i = 0; i < 16; ++i) y[i] = y[i] * inv * w[i];
 }
 
 __device__ __forceinline__ bool finite16(const float (&y)[16]) {
@@ -287,7 +287,9 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   float inv[kIter];  // (kNorm) of this thread's row of iteration j
   auto key = [&](int j, const Turn& t, float (&y)[16]) {
     if (kNorm && weight) {
-      normed(kw[j][0], kw[j][1], inv[j], weight, kp, y);
+      float w[16];
+      load_weights(weight, kp, w);
+      normed(kw[j][0], kw[j][1], inv[j], w, y);
       turn16(kp, t, y);
     } else {
       rotated(kw[j][0], kw[j][1], kp, t, y);
@@ -366,7 +368,9 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block)
   const Turn t = turn_of(a, p, r);
   const __nv_bfloat16* src = a.q + r * a.q_stride;
   __nv_bfloat16* dst = a.q_out + r * a.q_out_stride;
-  constexpr int U = 4;  // heads on their way
+  float w[16];  // (kNorm) one row of weights for all heads is kept, others are loaded with each head
+  if (kNorm && a.q_weight) load_weights(a.q_weight, p, w);
+  constexpr int U = kNorm ? 2 : 4;  // heads on their way
   for (int h0 = threadIdx.x / TPR % kAppHeads; h0 < a.n_heads; h0 += U * kAppHeads) {
     uint4 wa[U], wb[U];
 #pragma unroll
@@ -383,7 +387,8 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block)
       float y[16];
       if (kNorm && a.q_weight) {
         const float inv = inv_norm<TPR>(wa[i], wb[i], a.eps);
-        normed(wa[i], wb[i], inv, a.q_weight + h * a.q_weight_stride, p, y);
+        if (a.q_weight_stride != 0) load_weights(a.q_weight + h * a.q_weight_stride, p, w);
+        normed(wa[i], wb[i], inv, w, y);
         turn16(p, t, y);
       } else {
         rotated(wa[i], wb[i], p, t, y);
