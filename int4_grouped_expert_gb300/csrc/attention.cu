@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 3) attention_kernel(AttnArgs a
   };
   // what a team does after it has left a piece in its slot
   auto meet = [&](int index, int of) {
-    int gs = min(8, of);
+    int gs = min(kSink ? 16 : 8, of);
     while (gs * gs < of) ++gs;
     const int groups = (of + gs - 1) / gs, gi = index / gs, g0 = gi * gs, gn = min(gs, of - g0);
     if (!arrive_last(a.counters + slot_of(g0), gn)) return;

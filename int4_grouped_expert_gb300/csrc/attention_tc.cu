@@ -532,9 +532,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attention_tc_kernel(AttnArgs a)
       tc::tmem_ld32(ts + 32, r[1]);
       tc::tmem_ld_wait();
       if (!whole) {
+        uint32_t seen_bits[2];  // (three bounds a token as bits of a word)
+        if constexpr (kSink) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            auto below = [&](int c) { return c <= 32 * q ? 0u : c >= 32 * q + 32 ? 0xffffffffu : (1u << (c - 32 * q)) - 1u; };
+            seen_bits[q] = below(hi + 1) & (~below(lo) | below(first));
+          }
+        }
 #pragma unroll
         for (int i = 0; i < kAtTok; ++i) {
-          const bool seen = sees(i);
+          const bool seen = kSink ? (seen_bits[i / 32] >> (i % 32) & 1) != 0 : sees(i);
           r[i / 32][i % 32] = seen ? r[i / 32][i % 32] : 0xFF800000u;  // -inf
         }
       }

@@ -55,6 +55,7 @@ struct KvAppendArgs {
   const float *q_weight, *k_weight;          // of the norms; null: none
   int64_t q_weight_stride, k_weight_stride;  // from head to head, 0: one row for all
   float eps;
+  int norm_heads;         // query heads of a row that a block normalises at a time: 4, 8 or 16
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int num_sms, cudaStream_t stream);
 

@@ -9,7 +9,7 @@
 // the rotation is elementwise in fp32 with each product and sum rounded once, so both times give the
 // same values. The call moves each byte of q, k and v once and is bound by memory for prompts, by the
 // chain slot -> position -> table row -> codes for single tokens. Measured: 10798 tokens of 56 query and 8
-// K/V heads of 128 68 us, 5.6 TB/s; 16 single tokens 4.1 us. Pages of 16 tokens leave most of a block idle: 2 prompts of
+// K/V heads of 128 68 us, 5.6 TB/s, with norms 74; 16 single tokens 4.1 us, with norms 4.9. Pages of 16 tokens leave most of a block idle: 2 prompts of
 // up to 2184 tokens, 8 heads of 64, 21 us, 1.5 TB/s.
 //
 // A thread takes two chunks of 8 elements of a head's row that the rotation keeps to themselves: chunks c
@@ -105,6 +105,32 @@ __device__ __forceinline__ void rotated(const uint4& wa, const uint4& wb, const 
   turn16(p, t, y);
 }
 
+// Two values in one operand of the packed fp32 instructions, which round each of them as the single ones do.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ void to_pairs(const uint4& w, uint64_t* x) {
+  x[0] = pair_of(bf16_lo_f32(w.x), bf16_hi_f32(w.x));
+  x[1] = pair_of(bf16_lo_f32(w.y), bf16_hi_f32(w.y));
+  x[2] = pair_of(bf16_lo_f32(w.z), bf16_hi_f32(w.z));
+  x[3] = pair_of(bf16_lo_f32(w.w), bf16_hi_f32(w.w));
+}
+
 // The norm of a head's row, y = x * inv * weight with inv = 1 / sqrt(mean(x^2) + eps), all in fp32: nothing is rounded to
 // 16 bits before the rotation. The row lies in TPR lanes, 16 elements each; each sums its squares, then
 // the lanes do. Squares of elements from 2^60 on may leave fp32: such a row is summed once more times 2^-68, and
@@ -115,11 +141,18 @@ template <int TPR>
 __device__ __forceinline__ float inv_norm(uint4& wa, uint4& wb, float eps) {
   const unsigned lanes = ((1u << TPR) - 1u) << (threadIdx.x & 31 & ~(TPR - 1));
   auto mean = [&] {
-    float x[16], sum = 0.f;
-    to_f32(wa, x);
-    to_f32(wb, x + 8);
+    uint64_t x[8], s0 = 0, s1 = 0;  // (pairs of zeros)
+    to_pairs(wa, x);
+    to_pairs(wb, x + 4);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+    for (int i = 0; i < 8; i += 2) {
+      s0 = fma2(x[i], x[i], s0);
+      s1 = fma2(x[i + 1], x[i + 1], s1);
+    }
+    float a, b, c, d;
+    unpair(s0, a, b);
+    unpair(s1, c, d);
+    float sum = (a + b) + (c + d);
 #pragma unroll
     for (int d = 1; d < TPR; d <<= 1) sum += __shfl_xor_sync(lanes, sum, d);
     return sum * (1.f / (16 * TPR));
@@ -138,18 +171,37 @@ __device__ __forceinline__ float inv_norm(uint4& wa, uint4& wb, float eps) {
   }
   return __frsqrt_rn(m + eps);
 }
-__device__ __forceinline__ void load_weights(const float* weight, const Pair& p, float (&w)[16]) {
+__device__ __forceinline__ void load_weights(const float* weight, const Pair& p, uint64_t (&w)[8]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const float4 x = __ldg(reinterpret_cast<const float4*>(weight) + 2 * (q < 2 ? p.a : p.b) + (q & 1));
-    w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
+    w[2 * q] = pair_of(x.x, x.y);
+    w[2 * q + 1] = pair_of(x.z, x.w);
   }
 }
-__device__ __forceinline__ void normed(const uint4& wa, const uint4& wb, float inv, const float (&w)[16], float (&y)[16]) {
-  to_f32(wa, y);
-  to_f32(wb, y + 8);
+// The 16 elements of a pair of chunks, normalised and rotated. (A product and a fused one where halves are paired: the
+// rounding of one product is saved.)
+__device__ __forceinline__ void normed(const uint4& wa, const uint4& wb, float inv, const uint64_t (&w)[8], const Pair& p,
+                                       const Turn& t, float (&y)[16]) {
+  uint64_t x[8];
+  to_pairs(wa, x);
+  to_pairs(wb, x + 4);
+  const uint64_t i2 = pair_of(inv, inv);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] = y[i] * inv * w[i];
+  for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(x[i], i2), w[i]);
+  if (p.kind == 1) {
+    const uint64_t minus = pair_of(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t c = pair_of(t.c[2 * i], t.c[2 * i + 1]), s = pair_of(t.s[2 * i], t.s[2 * i + 1]);
+      const uint64_t u = x[i], v = x[4 + i];
+      x[i] = fma2(u, c, mul2(mul2(v, s), minus));
+      x[4 + i] = fma2(v, c, mul2(u, s));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) unpair(x[i], y[2 * i], y[2 * i + 1]);
+  if (p.kind == 2) turn16(p, t, y);
 }
 
 __device__ __forceinline__ bool finite16(const float (&y)[16]) {
@@ -220,7 +272,6 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the rows that may be the run's, on their way while its length is found
   const Pair kp = pair_of(threadIdx.x % TPR, a.rot_dim, a.neighbours);
-  const Pair vp = {kp.a, kp.b, 0, 0};
   const int ri = threadIdx.x / TPR;
   const Turn none = {};
   uint4 kw[kIter][2], vw[kIter][2];
@@ -279,35 +330,40 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     kw[j][0] = kw[j][1] = vw[j][0] = vw[j][1] = make_uint4(0u, 0u, 0u, 0u);
   }
   // a row is good when all its threads hold finite values
-  auto good_row = [&](const float (&k)[16], const float (&v)[16]) {
-    const unsigned bad = __ballot_sync(0xffffffffu, !(finite16(k) && finite16(v)));
+  auto good_row = [&](const float (&k)[16], uint32_t v_mag) {
+    const unsigned bad = __ballot_sync(0xffffffffu, !(finite16(k) && v_mag < 0x7F80u));
     return ((bad >> (lane / TPR * TPR)) & ((1u << TPR) - 1u)) == 0;
   };
   const float* weight = kNorm && a.k_weight ? a.k_weight + head * a.k_weight_stride : nullptr;
-  float inv[kIter];  // (kNorm) of this thread's row of iteration j
-  auto key = [&](int j, const Turn& t, float (&y)[16]) {
-    if (kNorm && weight) {
-      float w[16];
-      load_weights(weight, kp, w);
-      normed(kw[j][0], kw[j][1], inv[j], w, y);
-      turn16(kp, t, y);
-    } else {
-      rotated(kw[j][0], kw[j][1], kp, t, y);
-    }
-  };
+  // (kNorm) The keys as they are stored, but for the scale, wait in shared memory for it: turned once instead of twice,
+  // and out of the registers. (us, 10798 tokens of 8 heads, keys and values alone: 27.4, turned twice 34.8; without a norm 22.1.)
+  extern __shared__ uint4 norm_smem[];  // [kIter][4][kAppThreads]
+  float4* ready = reinterpret_cast<float4*>(norm_smem) + threadIdx.x;
   float km = 0.f, vm = 0.f;
   unsigned bad_rows = 0;  // bit j: this thread's row of iteration j
 #pragma unroll
   for (int j = 0; j < kIter; ++j) {
     if (j * RPI >= n) break;
-    float k[16], v[16];
+    float k[16];
     const int i = j * RPI + ri;
-    if (kNorm && weight) inv[j] = inv_norm<TPR>(kw[j][0], kw[j][1], a.eps);
-    key(j, j == 0 ? t_first : skipped >> j & 1u ? none : turn_of(a, kp, row0 + i), k);
-    rotated(vw[j][0], vw[j][1], vp, none, v);
-    if (good_row(k, v)) {
+    const Turn t = j == 0 ? t_first : skipped >> j & 1u ? none : turn_of(a, kp, row0 + i);
+    if (kNorm && weight) {
+      uint64_t w[8];
+      load_weights(weight, kp, w);
+      const float inv = inv_norm<TPR>(kw[j][0], kw[j][1], a.eps);
+      normed(kw[j][0], kw[j][1], inv, w, kp, t, k);
+    } else {
+      rotated(kw[j][0], kw[j][1], kp, t, k);
+    }
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        ready[(4 * j + q) * kAppThreads] = make_float4(k[4 * q], k[4 * q + 1], k[4 * q + 2], k[4 * q + 3]);
+    }
+    const uint32_t v_mag = max(bf16x8_mag(vw[j][0]), bf16x8_mag(vw[j][1]));  // (V is stored as it came)
+    if (good_row(k, v_mag)) {
       km = fmaxf(km, max16(k));
-      vm = fmaxf(vm, max16(v));
+      vm = fmaxf(vm, __uint_as_float(v_mag << 16));
     } else if (!(skipped >> j & 1u)) {
       bad_rows |= 1u << j;
     }
@@ -337,17 +393,26 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
     const int i = j * RPI + ri;
     if (i >= n) break;
     if (skipped >> j & 1u) continue;
-    float k[16], v[16];
-    key(j, j == 0 ? t_first : turn_of(a, kp, row0 + i), k);
-    rotated(vw[j][0], vw[j][1], vp, none, v);
     const bool ok = !(bad_rows >> j & 1u);
     const uint2 nan8 = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), zero = make_uint2(0u, 0u);
     uint2* kd = reinterpret_cast<uint2*>(kc + static_cast<int64_t>(off + i) * kD);
     uint2* vd = reinterpret_cast<uint2*>(vc + static_cast<int64_t>(off + i) * kD);
-    kd[kp.a] = ok ? codes8(k, ki) : nan8;
-    kd[kp.b] = ok ? codes8(k + 8, ki) : nan8;
-    vd[kp.a] = ok ? codes8(v, vi) : zero;
-    vd[kp.b] = ok ? codes8(v + 8, vi) : zero;
+    float y[16];
+    to_f32(vw[j][0], y);
+    to_f32(vw[j][1], y + 8);
+    vd[kp.a] = ok ? codes8(y, vi) : zero;
+    vd[kp.b] = ok ? codes8(y + 8, vi) : zero;
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 x = ready[(4 * j + q) * kAppThreads];
+        y[4 * q] = x.x; y[4 * q + 1] = x.y; y[4 * q + 2] = x.z; y[4 * q + 3] = x.w;
+      }
+    } else {
+      rotated(kw[j][0], kw[j][1], kp, j == 0 ? t_first : turn_of(a, kp, row0 + i), y);
+    }
+    kd[kp.a] = ok ? codes8(y, ki) : nan8;
+    kd[kp.b] = ok ? codes8(y + 8, ki) : nan8;
   }
   __syncthreads();  // every thread has read the old scales (and the shared words, for the next run)
   if (threadIdx.x == 0) {
@@ -357,9 +422,20 @@ __device__ __forceinline__ void append_run(const KvAppendArgs& a, int row0, int 
   if (__any_sync(0xffffffffu, bad_rows != 0) && lane == 0) set_status(a.status, STRATA_DEV_NONFINITE);
 }
 
+__device__ __forceinline__ void store16(__nv_bfloat16* head, const Pair& p, const float (&y)[16]) {
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
+    o[k] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  // (q_out may be q: nobody else reads these chunks)
+  reinterpret_cast<uint4*>(head)[p.a] = make_uint4(o[0], o[1], o[2], o[3]);
+  reinterpret_cast<uint4*>(head)[p.b] = make_uint4(o[4], o[5], o[6], o[7]);
+}
 // Queries: a block takes kAppThreads / (kD / 16 * kAppHeads) rows; a thread one pair of chunks of every
 // kAppHeads-th head of a row.
-template <int kD, bool kNorm>
+template <int kD>
 __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block) {
   constexpr int TPR = kD / 16, ROWS = kAppThreads / (TPR * kAppHeads);
   const int r = block * ROWS + threadIdx.x / (TPR * kAppHeads);
@@ -368,9 +444,7 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block)
   const Turn t = turn_of(a, p, r);
   const __nv_bfloat16* src = a.q + r * a.q_stride;
   __nv_bfloat16* dst = a.q_out + r * a.q_out_stride;
-  float w[16];  // (kNorm) one row of weights for all heads is kept, others are loaded with each head
-  if (kNorm && a.q_weight) load_weights(a.q_weight, p, w);
-  constexpr int U = kNorm ? 2 : 4;  // heads on their way
+  constexpr int U = 4;  // heads on their way
   for (int h0 = threadIdx.x / TPR % kAppHeads; h0 < a.n_heads; h0 += U * kAppHeads) {
     uint4 wa[U], wb[U];
 #pragma unroll
@@ -385,25 +459,60 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block)
       const int h = h0 + i * kAppHeads;
       if (h >= a.n_heads) break;
       float y[16];
-      if (kNorm && a.q_weight) {
-        const float inv = inv_norm<TPR>(wa[i], wb[i], a.eps);
-        if (a.q_weight_stride != 0) load_weights(a.q_weight + h * a.q_weight_stride, p, w);
-        normed(wa[i], wb[i], inv, w, y);
-        turn16(p, t, y);
-      } else {
-        rotated(wa[i], wb[i], p, t, y);
-      }
-      uint32_t o[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
-        o[k] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      // (q_out may be q: nobody else reads these chunks)
-      reinterpret_cast<uint4*>(dst + h * kD)[p.a] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4*>(dst + h * kD)[p.b] = make_uint4(o[4], o[5], o[6], o[7]);
+      rotated(wa[i], wb[i], p, t, y);
+      store16(dst + h * kD, p, y);
     }
   }
+}
+
+// The same with norms. A thread copies its chunks of the next kNormAhead heads to shared memory while it works on one:
+// a row's sum has to go round its lanes before anything can be stored, and loads that wait in registers for that are
+// too few to keep the memory busy. (us, 10798 tokens of 56 heads, with the keys: 94 from registers, 84 so; 3 heads or 5
+// ahead are the same. More than three blocks an SM would spill the keys' half, two take 99.)
+constexpr int kNormAhead = 5;
+constexpr size_t kNormSmem = static_cast<size_t>(kNormAhead) * kAppThreads * 32;
+template <int kD>
+__device__ __forceinline__ void norm_queries(const KvAppendArgs& a, int block) {
+  extern __shared__ uint4 norm_smem[];  // [kNormAhead][2][kAppThreads]
+  constexpr int TPR = kD / 16;
+  const int rows = kAppThreads / TPR / a.norm_heads;
+  const int r = block * rows + threadIdx.x / TPR / a.norm_heads;
+  if (r >= a.T) return;
+  const Pair p = pair_of(threadIdx.x % TPR, a.rot_dim, a.neighbours);
+  const __nv_bfloat16* src = a.q + r * a.q_stride;
+  __nv_bfloat16* dst = a.q_out + r * a.q_out_stride;
+  uint4* mine = norm_smem + threadIdx.x;
+  auto fetch = [&](int h, int slot) {
+    if (h < a.n_heads) {
+      const uint4* at = reinterpret_cast<const uint4*>(src + h * kD);
+      cp_async16(mine + 2 * slot * kAppThreads, at + p.a, true);
+      cp_async16(mine + (2 * slot + 1) * kAppThreads, at + p.b, true);
+    }
+    cp_async_commit();
+  };
+  const int h0 = threadIdx.x / TPR % a.norm_heads;
+#pragma unroll
+  for (int i = 0; i < kNormAhead; ++i) fetch(h0 + i * a.norm_heads, i);  // (while the row is looked up)
+  if (row_state(a, r) != 1) {
+    cp_async_wait<0>();
+    return;
+  }
+  const Turn t = turn_of(a, p, r);
+  uint64_t w[8];  // one row of weights for all heads is kept, others are loaded with each head
+  load_weights(a.q_weight, p, w);
+  int slot = 0;
+  for (int h = h0; h < a.n_heads; h += a.norm_heads) {
+    if (a.q_weight_stride != 0) load_weights(a.q_weight + h * a.q_weight_stride, p, w);
+    cp_async_wait<kNormAhead - 1>();
+    uint4 wa = mine[2 * slot * kAppThreads], wb = mine[(2 * slot + 1) * kAppThreads];
+    const float inv = inv_norm<TPR>(wa, wb, a.eps);
+    fetch(h + kNormAhead * a.norm_heads, slot);  // (what was there is in registers)
+    slot = slot + 1 == kNormAhead ? 0 : slot + 1;
+    float y[16];
+    normed(wa, wb, inv, w, p, t, y);
+    store16(dst + h * kD, p, y);
+  }
+  cp_async_wait<0>();
 }
 
 template <int kD, int kIter, bool kNorm>
@@ -411,7 +520,8 @@ __global__ void __launch_bounds__(kAppThreads, kIter > 2 ? 1 : 3) kv_append_kern
   griddep_wait();
   griddep_launch();
   if (blockIdx.x >= static_cast<unsigned>(kv_blocks)) {
-    rotate_queries<kD, kNorm>(a, blockIdx.x - kv_blocks);
+    if (kNorm && a.q_weight) norm_queries<kD>(a, blockIdx.x - kv_blocks);
+    else rotate_queries<kD>(a, blockIdx.x - kv_blocks);
     return;
   }
   const int head = blockIdx.x % a.c.n_kv_heads;
@@ -444,11 +554,23 @@ cudaError_t launch_kv_append(const KvAppendArgs& a0, int num_sms, cudaStream_t s
   const int64_t share = (static_cast<int64_t>(a.T) * a.c.n_kv_heads + 4 * num_sms - 1) / (4 * num_sms);
   a.rows_per_block = static_cast<int>(share < P ? share : P);
   const int64_t kv_blocks = static_cast<int64_t>((a.T + a.rows_per_block - 1) / a.rows_per_block) * a.c.n_kv_heads;
-  const int q_rows = kAppThreads / (D / 16 * kAppHeads);
+  // Many heads of a row at a time where there are few rows, few where there are many: the block's rows are looked up
+  // once. (us, 4 / 8 / 16 heads: 16 tokens 5.7 / 4.9 / 4.8, 231 tokens of 16 heads of 64 8.9 / 7.8 / 7.2, 10798 tokens
+  // 74 / 77 / 91.)
+  const int64_t lanes = static_cast<int64_t>(a.T) * D / 16;
+  const int most = 4 * num_sms * kAppThreads;
+  a.norm_heads = lanes * 16 <= most ? 16 : lanes * 8 <= most ? 8 : 4;
+  const int q_rows = kAppThreads / (D / 16) / (a.q_weight ? a.norm_heads : kAppHeads);
   const int64_t grid = kv_blocks + (a.q ? (a.T + q_rows - 1) / q_rows : 0);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  auto kern = a.q_weight || a.k_weight ? kernel_for<true>(D, P) : kernel_for<false>(D, P);
-  return launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(kAppThreads), 0, stream, true, a,
+  const bool norm = a.q_weight || a.k_weight;
+  const size_t rows = sizeof(float) * D * P, smem = !norm ? 0 : rows > kNormSmem ? rows : kNormSmem;
+  auto kern = norm ? kernel_for<true>(D, P) : kernel_for<false>(D, P);
+  if (smem > 40 << 10) {  // (128 tokens of 128)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(kAppThreads), smem, stream, true, a,
                        static_cast<int>(kv_blocks));
 }
 

@@ -6,8 +6,9 @@
 //
 // What these calls move is small (4 bytes a page of the pool, 4 to 12 bytes a table entry): the chain of dependent
 // steps is the time. Allocation needs sums over all pages and over all sequences before anybody can write, so one
-// cluster of eight blocks does a whole call, with the cluster's barrier between its steps: one launch, no workspace,
-// no counters in memory to wait for. Eight SMs read a pool of 65536 pages in about a microsecond.
+// block does a whole call, or one cluster of eight with the cluster's barrier between its steps: one launch, no
+// workspace, no counters in memory to wait for. (The figures are at kAlonePages; a release or a fork of 288 sequences takes
+// 2 us. A first version, the cluster for every size with its sums one block after another, took 11 us for 8 sequences.)
 #include <algorithm>
 
 #include "pages.cuh"
@@ -19,13 +20,12 @@ namespace {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
 }
-// A 64-bit word of block `rank` of the cluster, at this block's address of it.
-__device__ __forceinline__ uint64_t cluster_load(const uint64_t* p, int rank) {
+// A word of block `rank` of the cluster, at this block's address of it.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, int rank) {
   const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-  uint32_t theirs;
-  uint64_t v;
+  uint32_t theirs, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(theirs) : "r"(mine), "r"(rank));
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(theirs) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(theirs) : "memory");
   return v;
 }
 
@@ -70,11 +70,13 @@ __device__ __forceinline__ T block_scan(T v, T* s, T& total) {
 struct Range {
   int64_t lo, hi;
 };
-__device__ __forceinline__ int64_t share_of(int64_t n, int chunk) {
-  return ((n + kPagesCluster - 1) / kPagesCluster + chunk - 1) / chunk * chunk;
+template <int kBlocks>
+__host__ __device__ __forceinline__ int64_t share_of(int64_t n, int chunk) {
+  return ((n + kBlocks - 1) / kBlocks + chunk - 1) / chunk * chunk;
 }
+template <int kBlocks>
 __device__ __forceinline__ Range range_of(int64_t n, int chunk, int rank) {
-  const int64_t per = share_of(n, chunk), lo = min(n, rank * per);
+  const int64_t per = share_of<kBlocks>(n, chunk), lo = min(n, rank * per);
   return {lo, min(n, lo + per)};
 }
 // The counts of four pages, and how many of them `want` holds for. Pages from hi on count as neither free nor in use.
@@ -117,121 +119,123 @@ __device__ __forceinline__ Ask ask_of(const PagesExtendArgs& a, int s) {
 
 // Sequences in order get room while pages and rows last. need <= rows for each (a page is for one new token at
 // least, the page that a shared one moves to among them), so the list of pages has room where the rows' slots
-// will be.
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads) pages_extend_kernel(PagesExtendArgs a) {
+// will be. Sums stop at kMost, which is above every limit: what is beyond is refused, and nothing overflows.
+// kBlocks: a cluster, or one block where a barrier between its threads costs less than the SMs that it does without.
+constexpr uint32_t kMost = 1u << 28;
+__device__ __forceinline__ uint32_t add_most(uint32_t a, uint32_t b) { return min(a + b, kMost); }
+
+template <int kBlocks>
+__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kPagesThreads) pages_extend_kernel(PagesExtendArgs a) {
   extern __shared__ int32_t seq_smem[];  // [3][share]: rows (negative: and the page moves), first row, first page
-  __shared__ uint64_t s_rows[32], s_need[32];
-  __shared__ int s_free[32];
-  __shared__ uint64_t s_total[3], s_got[2];  // for the cluster: free pages, rows, pages; rows and pages that are given
-  __shared__ uint32_t s_moves;
+  __shared__ uint32_t s_a[32], s_b[32], s_c[32], s_d[32];
+  __shared__ int s_scan[32];
+  __shared__ uint32_t s_total[3], s_got[3];  // for the cluster: free pages, rows, pages; rows, pages, moves that are given
   griddep_wait();
   griddep_launch();
   const strata_kv_pages& p = a.p;
-  const int rank = blockIdx.x, shift = shift_of(p);
-  const int n_seq = p.n_seq, share = static_cast<int>(share_of(n_seq, kPagesThreads));
+  const int rank = kBlocks == 1 ? 0 : blockIdx.x, shift = shift_of(p), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n_seq = p.n_seq, share = static_cast<int>(share_of<kBlocks>(n_seq, kPagesThreads));
   int32_t *rows_of = seq_smem, *row_at = seq_smem + share, *page_at = seq_smem + 2 * share;
-  const Range seqs = range_of(n_seq, kPagesThreads, rank), pages = range_of(p.n_pages, kPageChunk, rank);
-  constexpr int kMoveBits = 17;  // (at most 65535 sequences move a page)
+  const Range seqs = range_of<kBlocks>(n_seq, kPagesThreads, rank);
+  const Range pages = range_of<kBlocks>(p.n_pages, kPageChunk, rank);
+  const int my_seqs = static_cast<int>(seqs.hi - seqs.lo);
 
   // ---- free pages of this block's share, and what its sequences ask for
-  int free = 0;
+  uint32_t free = 0;
   for (int64_t at = pages.lo + 4 * threadIdx.x; at < pages.hi; at += kPageChunk) {
     const int4 r = four_refs(p.refs, at, pages.hi);
     free += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
   }
-  uint64_t rows_sum = 0, need_sum = 0;  // (64 bits: nothing is cut before it is added)
-  for (int64_t s0 = seqs.lo; s0 < seqs.hi; s0 += kPagesThreads) {
-    const int s = static_cast<int>(s0) + threadIdx.x, i = s - static_cast<int>(seqs.lo);
-    const Ask k = s < seqs.hi ? ask_of(a, s) : Ask{0, 0, 0};
-    uint64_t rt, nt;
-    const uint64_t rows = rows_sum + block_scan<uint64_t>(k.rows, s_rows, rt);
-    const uint64_t need =
-        need_sum + block_scan<uint64_t>(static_cast<uint64_t>(k.need) << kMoveBits | k.moved, s_need, nt);
-    if (s < seqs.hi) {
-      rows_of[i] = k.moved ? -k.rows : k.rows;
-      // (sums beyond any limit are all the same: refused)
-      row_at[i] = static_cast<int>(min(rows - k.rows, uint64_t(0x40000000)));
-      page_at[i] = static_cast<int>(min((need >> kMoveBits) - k.need, uint64_t(0x40000000)));
+  free = __reduce_add_sync(0xffffffffu, free);
+  if (lane == 0) s_c[warp] = free;
+  uint32_t rows_sum = 0, need_sum = 0;
+  for (int i0 = 0; i0 < my_seqs; i0 += kPagesThreads) {
+    const int i = i0 + threadIdx.x;
+    const Ask k = i < my_seqs ? ask_of(a, static_cast<int>(seqs.lo) + i) : Ask{0, 0, 0};
+    const uint32_t rows = min(static_cast<uint32_t>(k.rows), kMost), need = k.need;
+    uint32_t r1 = rows, n1 = need;  // inclusive sums
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, r1, d), y = __shfl_up_sync(0xffffffffu, n1, d);
+      if (lane >= d) r1 = add_most(r1, x), n1 = add_most(n1, y);
     }
-    rows_sum += rt;
-    need_sum += nt;
+    if (lane == 31) s_a[warp] = r1, s_b[warp] = n1;
+    __syncthreads();
+    uint32_t rw = s_a[lane], nw = s_b[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, rw, d), y = __shfl_up_sync(0xffffffffu, nw, d);
+      if (lane >= d) rw = add_most(rw, x), nw = add_most(nw, y);
+    }
+    const uint32_t r_before = __shfl_sync(0xffffffffu, rw, max(warp - 1, 0)), n_before = __shfl_sync(0xffffffffu, nw, max(warp - 1, 0));
+    if (warp > 0) r1 = add_most(r1, r_before), n1 = add_most(n1, n_before);
+    if (i < my_seqs) {
+      rows_of[i] = k.moved ? -k.rows : k.rows;
+      // (exact below kMost, and refused from there on)
+      row_at[i] = add_most(rows_sum, r1) < kMost ? rows_sum + r1 - rows : kMost;
+      page_at[i] = add_most(need_sum, n1) < kMost ? need_sum + n1 - need : kMost;
+    }
+    rows_sum = add_most(rows_sum, __shfl_sync(0xffffffffu, rw, 31));
+    need_sum = add_most(need_sum, __shfl_sync(0xffffffffu, nw, 31));
     __syncthreads();
   }
-  int free_total;
-  block_scan(free, s_free, free_total);
-  if (threadIdx.x == 0) {
-    s_total[0] = free_total;
-    s_total[1] = rows_sum;
-    s_total[2] = need_sum;
-    s_moves = 0;
+  __syncthreads();
+  free = __reduce_add_sync(0xffffffffu, s_c[lane]);
+  // what the blocks before this one have, and all of them (lane b asks block b)
+  uint32_t free_before = 0, rows_before = 0, pages_before = 0, free_all = free;
+  if constexpr (kBlocks > 1) {
+    if (threadIdx.x == 0) s_total[0] = free, s_total[1] = rows_sum, s_total[2] = need_sum;
+    cluster_sync();
+    const uint32_t f = lane < kBlocks ? cluster_load(s_total, lane) : 0;
+    free_all = __reduce_add_sync(0xffffffffu, f);
+    free_before = __reduce_add_sync(0xffffffffu, lane < rank ? f : 0);
+    rows_before = __reduce_add_sync(0xffffffffu, lane < rank ? cluster_load(s_total + 1, lane) : 0);
+    pages_before = __reduce_add_sync(0xffffffffu, lane < rank ? cluster_load(s_total + 2, lane) : 0);
   }
-  cluster_sync();
-  uint64_t free_before = 0, rows_before = 0, need_before = 0, free_all = 0;
-  for (int b = 0; b < kPagesCluster; ++b) {
-    const uint64_t f = cluster_load(s_total, b);
-    if (b < rank) {
-      free_before += f;
-      rows_before += cluster_load(s_total + 1, b);
-      need_before += cluster_load(s_total + 2, b);
-    }
-    free_all += f;
-  }
-  const uint64_t pages_before = need_before >> kMoveBits;
   // ---- who gets room: sums only grow, so it is the sequences up to some place. Rows and pages up to there.
-  uint64_t rows_got = 0, pages_got = 0;
-  for (int i = threadIdx.x; i < seqs.hi - seqs.lo; i += kPagesThreads) {
+  uint32_t rows_got = 0, pages_got = 0, moves = 0;
+  for (int i = threadIdx.x; i < my_seqs; i += kPagesThreads) {
     const int n = abs(rows_of[i]);
-    // (recomputed from the stored sums: the pages of sequence i end where the next one's begin)
-    const uint64_t r1 = rows_before + row_at[i] + n;
+    const uint32_t r1 = rows_before + row_at[i] + min(static_cast<uint32_t>(n), kMost);
     const int len = length_of(p, p.kv_len[seqs.lo + i], nullptr);
     const int need = n > 0 ? pages_of(len + n, shift) - pages_of(len, shift) + (rows_of[i] < 0) : 0;
-    const uint64_t p1 = pages_before + page_at[i] + need;
-    if (r1 <= static_cast<uint64_t>(a.T_max) && p1 <= free_all) {
+    const uint32_t p1 = pages_before + page_at[i] + need;
+    if (r1 <= static_cast<uint32_t>(a.T_max) && p1 <= free_all) {
       rows_got = max(rows_got, r1);
       pages_got = max(pages_got, p1);
-      if (rows_of[i] < 0) atomicAdd(&s_moves, 1u);
+      moves += rows_of[i] < 0;
     } else {
       if (n > 0) set_status(a.status, STRATA_DEV_NO_PAGES);
       rows_of[i] = 0;
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    rows_got = max(rows_got, __shfl_xor_sync(0xffffffffu, rows_got, d));
-    pages_got = max(pages_got, __shfl_xor_sync(0xffffffffu, pages_got, d));
-  }
-  if ((threadIdx.x & 31) == 0) {
-    s_rows[threadIdx.x >> 5] = rows_got;
-    s_need[threadIdx.x >> 5] = pages_got;
-  }
+  rows_got = __reduce_max_sync(0xffffffffu, rows_got);
+  pages_got = __reduce_max_sync(0xffffffffu, pages_got);
+  moves = __reduce_add_sync(0xffffffffu, moves);
+  if (lane == 0) s_a[warp] = rows_got, s_b[warp] = pages_got, s_d[warp] = moves;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 32; ++w) {
-      rows_got = max(rows_got, s_rows[w]);
-      pages_got = max(pages_got, s_need[w]);
-    }
-    s_got[0] = rows_got;
-    s_got[1] = pages_got << 32 | s_moves;
-  }
-  cluster_sync();
-  uint32_t moves_before = 0, moves_all = 0;
-  rows_got = pages_got = 0;
-  for (int b = 0; b < kPagesCluster; ++b) {
-    const uint64_t g = cluster_load(s_got + 1, b);
-    rows_got = max(rows_got, cluster_load(s_got, b));
-    pages_got = max(pages_got, g >> 32);
-    if (b < rank) moves_before += static_cast<uint32_t>(g);
-    moves_all += static_cast<uint32_t>(g);
+  rows_got = __reduce_max_sync(0xffffffffu, s_a[lane]);
+  pages_got = __reduce_max_sync(0xffffffffu, s_b[lane]);
+  moves = __reduce_add_sync(0xffffffffu, s_d[lane]);
+  uint32_t moves_before = 0;
+  if constexpr (kBlocks > 1) {
+    if (threadIdx.x == 0) s_got[0] = rows_got, s_got[1] = pages_got, s_got[2] = moves;
+    cluster_sync();
+    rows_got = __reduce_max_sync(0xffffffffu, lane < kBlocks ? cluster_load(s_got, lane) : 0);
+    pages_got = __reduce_max_sync(0xffffffffu, lane < kBlocks ? cluster_load(s_got + 1, lane) : 0);
+    const uint32_t m = lane < kBlocks ? cluster_load(s_got + 2, lane) : 0;
+    moves_before = __reduce_add_sync(0xffffffffu, lane < rank ? m : 0);
+    moves = __reduce_add_sync(0xffffffffu, m);
   }
   const int R = static_cast<int>(rows_got);
   // ---- the lowest free pages, in order: noted where the slots will be
-  uint64_t at_free = free_before;
+  uint32_t at_free = free_before;
   for (int64_t c = pages.lo; c < pages.hi && at_free < pages_got; c += kPageChunk) {
     const int64_t at = c + 4 * threadIdx.x;
     const int4 r = at < pages.hi ? four_refs(p.refs, at, pages.hi) : make_int4(-1, -1, -1, -1);
     const int here = (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
     int total;
-    uint64_t k = at_free + block_scan(here, s_free, total) - here;
+    uint32_t k = at_free + block_scan(here, s_scan, total) - here;
     const int v[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -245,27 +249,32 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
     at_free += total;
     __syncthreads();
   }
-  cluster_sync();
+  if constexpr (kBlocks > 1) cluster_sync();
+  else __syncthreads();
   // ---- tables and lengths: a lane a sequence, a warp where one has many pages
-  uint32_t moves = moves_before;
-  for (int64_t s0 = seqs.lo; s0 < seqs.hi; s0 += kPagesThreads) {
-    const int s = static_cast<int>(s0) + threadIdx.x, i = s - static_cast<int>(seqs.lo);
-    const bool on = s < seqs.hi;
+  for (int i0 = 0; i0 < my_seqs; i0 += kPagesThreads) {
+    const int i = i0 + threadIdx.x, s = static_cast<int>(seqs.lo) + i;
+    const bool on = i < my_seqs;
     const int n = on ? abs(rows_of[i]) : 0, moved = on && rows_of[i] < 0;
     const int len = n > 0 ? length_of(p, p.kv_len[s], nullptr) : 0;
-    int first = pages_of(len, shift) - moved;
-    int need = n > 0 ? pages_of(len + n, shift) - first : 0;
-    int from = n > 0 ? static_cast<int>(pages_before) + page_at[i] : 0;
-    uint32_t total;
-    const uint32_t m = moves + block_scan<uint32_t>(moved, reinterpret_cast<uint32_t*>(s_free), total) - moved;
-    moves += total;
-    if (on) a.q_start[s] = static_cast<int>(min(rows_before + row_at[i], rows_got));
+    const int first = pages_of(len, shift) - moved;
+    const int need = n > 0 ? pages_of(len + n, shift) - first : 0;
+    const int from = n > 0 ? static_cast<int>(pages_before) + page_at[i] : 0;
     int32_t* row = p.page_table + static_cast<int64_t>(on ? s : 0) * p.table_stride;
-    if (moved) {
-      const int old = row[first], page = __ldcg(a.slots + from);
-      atomicAdd(p.refs + old, -1);
-      a.copies[2 * m] = old;
-      a.copies[2 * m + 1] = page;
+    if (moves > 0) {
+      int total;
+      const uint32_t m = moves_before + block_scan(moved, s_scan, total) - moved;
+      moves_before += total;
+      if (moved) {
+        const int old = row[first], page = __ldcg(a.slots + from);
+        atomicAdd(p.refs + old, -1);
+        a.copies[2 * m] = old;
+        a.copies[2 * m + 1] = page;
+      }
+    }
+    if (on) {
+      const int q = static_cast<int>(min(rows_before + row_at[i], rows_got));
+      a.q_start[s] = row_at[i] = q;  // (the block's place for it is read again below, if it is alone)
     }
     if (n > 0) p.kv_len[s] = len + n;
     if (need == 1) row[first] = __ldcg(a.slots + from);
@@ -274,26 +283,28 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
       const int64_t at = __shfl_sync(0xffffffffu, static_cast<int64_t>(row - p.page_table), l);
       const int f = __shfl_sync(0xffffffffu, first, l), k = __shfl_sync(0xffffffffu, need, l);
       const int src = __shfl_sync(0xffffffffu, from, l);
-      for (int e = threadIdx.x & 31; e < k; e += 32) p.page_table[at + f + e] = __ldcg(a.slots + src + e);
+      for (int e = lane; e < k; e += 32) p.page_table[at + f + e] = __ldcg(a.slots + src + e);
     }
     __syncthreads();
   }
   if (rank == 0 && threadIdx.x == 0) {
     a.q_start[n_seq] = R;
-    *a.n_copies = static_cast<int32_t>(moves_all);
+    *a.n_copies = static_cast<int32_t>(moves);
   }
-  cluster_sync();
+  if constexpr (kBlocks > 1) cluster_sync();
+  else __syncthreads();
   // ---- the rows, each by itself (the list of pages is not needed any more)
-  for (int r = rank * kPagesThreads + threadIdx.x; r < a.T_max; r += kPagesCluster * kPagesThreads) {
+  auto start_of = [&](int s) { return kBlocks == 1 ? row_at[s] : __ldcg(a.q_start + s); };
+  for (int r = rank * kPagesThreads + threadIdx.x; r < a.T_max; r += kBlocks * kPagesThreads) {
     int slot = -1, pos = 0;
     if (r < R) {
-      int lo = 0, hi = n_seq;  // the last sequence whose first row is not after r: q_start[lo] <= r < q_start[hi]
+      int lo = 0, hi = n_seq;  // the last sequence whose first row is not after r: start_of(lo) <= r < start_of(hi)
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldcg(a.q_start + mid) <= r) lo = mid;
+        if (start_of(mid) <= r) lo = mid;
         else hi = mid;
       }
-      pos = __ldcg(p.kv_len + lo) - (__ldcg(a.q_start + lo + 1) - r);
+      pos = __ldcg(p.kv_len + lo) - ((lo + 1 < n_seq ? start_of(lo + 1) : R) - r);
       slot = (__ldcg(p.page_table + lo * p.table_stride + (pos >> shift)) << shift) + (pos & (p.page_size - 1));
     }
     a.slots[r] = slot;
@@ -387,26 +398,30 @@ __global__ void __launch_bounds__(kReleaseThreads) pages_release_kernel(PagesRel
 }
 
 // ------------------------------------------------------------------------------------------------ compact
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads) pages_map_kernel(PagesCompactArgs a) {
-  __shared__ uint64_t s_total;
+template <int kBlocks>
+__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kPagesThreads) pages_map_kernel(PagesCompactArgs a) {
+  __shared__ uint32_t s_total;
   __shared__ int s_scan[32];
   griddep_wait();
   griddep_launch();
-  const int rank = blockIdx.x;
-  const Range pages = range_of(a.src.n_pages, kPageChunk, rank);
+  const int rank = kBlocks == 1 ? 0 : blockIdx.x;
+  const Range pages = range_of<kBlocks>(a.src.n_pages, kPageChunk, rank);
   int live = 0, total;
   for (int64_t at = pages.lo + 4 * threadIdx.x; at < pages.hi; at += kPageChunk) {
     const int4 r = four_refs(a.src.refs, at, pages.hi);
     live += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
   }
   block_scan(live, s_scan, total);
-  if (threadIdx.x == 0) s_total = total;
-  cluster_sync();
-  int64_t before = 0, all = 0;
-  for (int b = 0; b < kPagesCluster; ++b) {
-    const int64_t n = static_cast<int64_t>(cluster_load(&s_total, b));
-    if (b < rank) before += n;
-    all += n;
+  uint32_t before = 0, all = total;
+  if constexpr (kBlocks > 1) {
+    if (threadIdx.x == 0) s_total = total;
+    cluster_sync();
+    const int lane = threadIdx.x & 31;
+    const uint32_t n = lane < kBlocks ? cluster_load(&s_total, lane) : 0;
+    before = __reduce_add_sync(0xffffffffu, lane < rank ? n : 0);
+    all = __reduce_add_sync(0xffffffffu, n);
+  } else {
+    __syncthreads();  // (all have read the sums)
   }
   const bool fits = all <= a.dst.n_pages;
   for (int64_t c = pages.lo; c < pages.hi; c += kPageChunk) {
@@ -431,14 +446,14 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
     __syncthreads();
   }
   for (int64_t i = (fits ? all : 0) + rank * kPagesThreads + threadIdx.x; i < a.dst.n_pages;
-       i += kPagesCluster * kPagesThreads)
+       i += kBlocks * kPagesThreads)
     a.dst.refs[i] = 0;
   if (rank == 0 && threadIdx.x == 0) {
     *a.n_copies = fits ? static_cast<int32_t>(all) : 0;
     *a.live = fits ? static_cast<int32_t>(all) : -1;
     if (!fits) set_status(a.status, STRATA_DEV_NO_PAGES);
   }
-  cluster_sync();  // (nobody leaves while another reads its total)
+  if constexpr (kBlocks > 1) cluster_sync();  // (nobody leaves while another reads its total)
 }
 
 constexpr int kTableThreads = 256, kTableEntries = 4 * kTableThreads;
@@ -473,17 +488,28 @@ __global__ void __launch_bounds__(kTableThreads) pages_table_kernel(PagesCompact
   }
 }
 
+// Up to so many pages and rows, and a sequence a thread, one block makes room alone. (us, alone / the cluster: 256 pages, 8
+// sequences 4.7 / 9.0; 16384, 256 7.4 / 11.7; 32768, 256 9.2 / 11.7; 65536, 256 13.5 / 12.7; 262144, 8 36 / 16; 8000 rows and
+// 4096 pages 9.8 / 10.8, 16384 12.1 / 12.0.) Numbering pages goes over each of them twice: 500 pages 3.9 / 5.2,
+// 12000 11.8 / 7.7.
+constexpr int64_t kAlonePages = 32768, kAloneMapPages = 4096;
+constexpr int kAloneRows = 4096;
+
 }  // namespace
 
-cudaError_t launch_pages_extend(const PagesExtendArgs& a, cudaStream_t stream) {
-  const int64_t share = ((a.p.n_seq + kPagesCluster - 1) / kPagesCluster + kPagesThreads - 1) / kPagesThreads * kPagesThreads;
-  const size_t smem = 3 * sizeof(int32_t) * share;  // up to 96 KB
+template <int kBlocks>
+static cudaError_t launch_extend(const PagesExtendArgs& a, cudaStream_t stream) {
+  const size_t smem = 3 * sizeof(int32_t) * share_of<kBlocks>(a.p.n_seq, kPagesThreads);  // up to 96 KB
   if (smem > 40 << 10) {
-    const cudaError_t e = cudaFuncSetAttribute(pages_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(pages_extend_kernel<kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  return launch_kernel(pages_extend_kernel, dim3(kPagesCluster), dim3(kPagesThreads), smem, stream, true, a);
+  return launch_kernel(pages_extend_kernel<kBlocks>, dim3(kBlocks), dim3(kPagesThreads), smem, stream, true, a);
+}
+cudaError_t launch_pages_extend(const PagesExtendArgs& a, cudaStream_t stream) {
+  const bool alone = a.p.n_seq <= kPagesThreads && a.p.n_pages <= kAlonePages && a.T_max <= kAloneRows;
+  return alone ? launch_extend<1>(a, stream) : launch_extend<kPagesCluster>(a, stream);
 }
 
 cudaError_t launch_pages_fork(const PagesForkArgs& a, int num_sms, cudaStream_t stream) {
@@ -498,7 +524,9 @@ cudaError_t launch_pages_release(const PagesReleaseArgs& a, int num_sms, cudaStr
 }
 
 cudaError_t launch_pages_compact(const PagesCompactArgs& a, int num_sms, cudaStream_t stream) {
-  const cudaError_t e = launch_kernel(pages_map_kernel, dim3(kPagesCluster), dim3(kPagesThreads), 0, stream, true, a);
+  const bool alone = a.src.n_pages <= kAloneMapPages && a.dst.n_pages <= kAloneMapPages;
+  const cudaError_t e = launch_kernel(alone ? pages_map_kernel<1> : pages_map_kernel<kPagesCluster>,
+                                      dim3(alone ? 1 : kPagesCluster), dim3(kPagesThreads), 0, stream, true, a);
   if (e != cudaSuccess || a.src.n_seq == 0) return e;
   const int64_t stretches = (a.dst.max_pages + kTableEntries - 1) / kTableEntries;
   const int64_t grid = std::min<int64_t>(a.src.n_seq * stretches, 8 * num_sms);
