@@ -551,8 +551,8 @@ typedef struct {
  *             without a token get slot -1 (padding of strata_kv_append) and position 0, copies from n_copies on keep
  *             what they hold.
  * From the first sequence on for which free pages or rows run out, no sequence gets any (STRATA_DEV_NO_PAGES); one with a
- * negative count, more tokens than its table holds, or an unfinished page that is none or that nobody counts gets
- * nothing (STRATA_DEV_BAD_SLOT): its length stays. dev_status here and below: device uint32 or NULL.
+ * negative count or length, more tokens than its table holds, or an unfinished page that is none or that nobody counts
+ * gets nothing (STRATA_DEV_BAD_SLOT): its length stays. dev_status here and below: device uint32 or NULL.
  */
 strata_status strata_kv_pages_extend(const strata_kv_pages* pages, const int32_t* new_tokens, int64_t T_max,
                                      int32_t* slots, int32_t* positions, int32_t* q_start, int32_t* copies,

@@ -153,6 +153,7 @@ class QKNorm:
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
         s = strata_qk_norm()
         s.eps = eps
+        s.rows = {}  # heads that have a row of their own
         for name, w in (("q", q_weight), ("k", k_weight)):
             if w is None:
                 continue
@@ -162,6 +163,8 @@ class QKNorm:
             _held(w, f"{name}_weight", "float32", rows * head_dim)
             setattr(s, f"{name}_weight", ptr(w))
             setattr(s, f"{name}_head_stride", head_dim if rows > 1 else 0)
+            if rows > 1:
+                s.rows[name] = rows
         self._struct = s
 
     def struct(self) -> strata_qk_norm:

@@ -94,12 +94,10 @@ struct Ask {
 };
 __device__ __forceinline__ Ask ask_of(const PagesExtendArgs& a, int s) {
   const strata_kv_pages& p = a.p;
-  const int shift = shift_of(p), fresh = a.new_tokens[s];
-  const int len = length_of(p, p.kv_len[s], a.status);
+  const int shift = shift_of(p), fresh = a.new_tokens[s], len = p.kv_len[s];
   Ask k{0, 0, 0};
   if (fresh == 0) return k;
-  const int64_t most = p.max_pages * p.page_size;
-  if (fresh < 0 || fresh > most - len) {
+  if (fresh < 0 || len < 0 || fresh > p.max_pages * p.page_size - len) {
     set_status(a.status, STRATA_DEV_BAD_SLOT);
     return k;
   }

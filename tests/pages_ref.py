@@ -22,7 +22,7 @@ class Pages:
         rows = need = 0
         for s, n in enumerate(new):
             L, n = int(self.length[s]), int(n)
-            bad = n < 0 or L + n > self.E * P
+            bad = n < 0 or (n > 0 and (L < 0 or L + n > self.E * P))
             last = int(self.table[s, L // P]) if L % P and not bad and n else 0
             if L % P and n and not bad:
                 bad = not 0 <= last < self.n_pages or refs[last] < 1

@@ -56,3 +56,13 @@ def test_weights_that_are_taken_and_refused():
             st.QKNorm(w, None, 64)
         with pytest.raises(error):
             st.QKNorm(None, w, 64)
+
+
+def test_fewer_rows_of_weights_than_heads(st):  # noqa: F811
+    C = cache(st, head_dim=64, n_kv_heads=4)
+    f = st.strata_kv_append_normed
+    for q, k in ((torch.ones(7, 64), None), (torch.ones(8, 64), torch.ones(3, 64))):
+        with pytest.raises(ValueError):
+            f(C, st.QKNorm(q, k, 64).struct(), A, A, 4, A, q=A, n_heads=8, q_out=2 * A)
+    assert f(C, st.QKNorm(torch.ones(8, 64), torch.ones(4, 64), 64).struct(), A, A, 0, A, q=A, n_heads=8, q_out=2 * A) == 0
+    assert f(C, st.QKNorm(torch.ones(7, 64), torch.ones(5, 64), 64).struct(), A, A, 0, A) == 0
