@@ -115,12 +115,53 @@ __device__ __forceinline__ Ask ask_of(const PagesExtendArgs& a, int s) {
   return k;
 }
 
+// Slots and positions of rows: a thread looks for the last sequence whose first row is not after its row.
+template <int kBlocks, int U>
+__device__ __forceinline__ void lay_out_rows(const PagesExtendArgs& a, const int32_t* row_at, int R, int rank) {
+  const strata_kv_pages& p = a.p;
+  const int n_seq = p.n_seq, shift = shift_of(p);
+  auto start_of = [&](int s) { return kBlocks == 1 ? row_at[s] : __ldcg(a.q_start + s); };
+  const int top = n_seq > 1 ? 1 << (31 - __clz(n_seq - 1)) : 0;
+#pragma unroll 1
+  for (int r0 = rank * kPagesThreads + threadIdx.x; r0 < a.T_max; r0 += U * kBlocks * kPagesThreads) {
+    int of[U] = {}, pos[U], slot[U];
+    auto row = [&](int j) { return r0 + j * kBlocks * kPagesThreads; };
+#pragma unroll 1
+    for (int d = top; d > 0; d >>= 1)
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int s = of[j] + d;
+        if (row(j) < R && s < n_seq && start_of(s) <= row(j)) of[j] = s;
+      }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      pos[j] = 0;
+      if (row(j) < R)
+        pos[j] = __ldcg(p.kv_len + of[j]) - ((of[j] + 1 < n_seq ? start_of(of[j] + 1) : R) - row(j));
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      slot[j] = -1;
+      if (row(j) < R)
+        slot[j] = (__ldcg(p.page_table + of[j] * p.table_stride + (pos[j] >> shift)) << shift) + (pos[j] & (p.page_size - 1));
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (row(j) >= a.T_max) break;
+      a.slots[row(j)] = slot[j];
+      a.positions[row(j)] = pos[j];
+    }
+  }
+}
+
 // Sequences in order get room while pages and rows last. need <= rows for each (a page is for one new token at
 // least, the page that a shared one moves to among them), so the list of pages has room where the rows' slots
 // will be. Sums stop at kMost, which is above every limit: what is beyond is refused, and nothing overflows.
 // kBlocks: a cluster, or one block where a barrier between its threads costs less than the SMs that it does without.
 constexpr uint32_t kMost = 1u << 28;
 __device__ __forceinline__ uint32_t add_most(uint32_t a, uint32_t b) { return min(a + b, kMost); }
+
+constexpr int kLaneNeed = 2;  // pages that a lane writes for its sequence by itself
 
 template <int kBlocks>
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kPagesThreads) pages_extend_kernel(PagesExtendArgs a) {
@@ -275,8 +316,15 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kPagesThreads)
       a.q_start[s] = row_at[i] = q;  // (the block's place for it is read again below, if it is alone)
     }
     if (n > 0) p.kv_len[s] = len + n;
-    if (need == 1) row[first] = __ldcg(a.slots + from);
-    for (unsigned many = __ballot_sync(0xffffffffu, need > 1); many; many &= many - 1) {
+    if (need <= kLaneNeed) {
+      int page[kLaneNeed];
+#pragma unroll
+      for (int e = 0; e < kLaneNeed; ++e) page[e] = e < need ? __ldcg(a.slots + from + e) : 0;
+#pragma unroll
+      for (int e = 0; e < kLaneNeed; ++e)
+        if (e < need) row[first + e] = page[e];
+    }
+    for (unsigned many = __ballot_sync(0xffffffffu, need > kLaneNeed); many; many &= many - 1) {
       const int l = __ffs(many) - 1;
       const int64_t at = __shfl_sync(0xffffffffu, static_cast<int64_t>(row - p.page_table), l);
       const int f = __shfl_sync(0xffffffffu, first, l), k = __shfl_sync(0xffffffffu, need, l);
@@ -291,23 +339,9 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kPagesThreads)
   }
   if constexpr (kBlocks > 1) cluster_sync();
   else __syncthreads();
-  // ---- the rows, each by itself (the list of pages is not needed any more)
-  auto start_of = [&](int s) { return kBlocks == 1 ? row_at[s] : __ldcg(a.q_start + s); };
-  for (int r = rank * kPagesThreads + threadIdx.x; r < a.T_max; r += kBlocks * kPagesThreads) {
-    int slot = -1, pos = 0;
-    if (r < R) {
-      int lo = 0, hi = n_seq;  // the last sequence whose first row is not after r: start_of(lo) <= r < start_of(hi)
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start_of(mid) <= r) lo = mid;
-        else hi = mid;
-      }
-      pos = __ldcg(p.kv_len + lo) - ((lo + 1 < n_seq ? start_of(lo + 1) : R) - r);
-      slot = (__ldcg(p.page_table + lo * p.table_stride + (pos >> shift)) << shift) + (pos & (p.page_size - 1));
-    }
-    a.slots[r] = slot;
-    a.positions[r] = pos;
-  }
+  // ---- the rows, each by itself (the list of pages is not needed any more); four of a thread at a time if it has some
+  if (a.T_max <= kBlocks * kPagesThreads) lay_out_rows<kBlocks, 1>(a, row_at, R, rank);
+  else lay_out_rows<kBlocks, 4>(a, row_at, R, rank);
 }
 
 // ------------------------------------------------------------------------------------------------ fork
