@@ -103,15 +103,18 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 
 // ---------------------------------------------------------------------------- cp.async
+// All three touch memory as the compiler sees it: a thread's own reads of what was copied stay behind the wait, and its reads
+// of a place that the next copy fills ahead of that copy. (The append with norms has no barrier in between.)
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem, bool pred) {
   uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   int sz = pred ? 16 : 0;  // zero-fill when the source row does not exist
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem), "r"(sz));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem), "r"(sz)
+               : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N));
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
 // L2 policy for data a kernel streams once per call (expert weights and scales, router weights):
