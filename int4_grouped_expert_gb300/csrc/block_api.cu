@@ -170,7 +170,7 @@ strata_status check_pages(const strata_kv_pages* p) {
   if (!p) return STRATA_ERR_INVALID_ARG;
   if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
     return STRATA_ERR_UNSUPPORTED;
-  if (p->n_seq < 0 || p->n_seq > 65535 || p->n_pages < 0 || p->n_pages > 0x7FFFFFFF / p->page_size ||
+  if (p->n_seq < 0 || p->n_seq > kPagesMostSeq || p->n_pages < 0 || p->n_pages > 0x7FFFFFFF / p->page_size ||
       p->max_pages < 0 || p->max_pages > 0x7FFFFFFF / p->page_size || p->table_stride < p->max_pages)
     return STRATA_ERR_SHAPE;
   if ((p->n_seq > 0 && (!p->kv_len || (p->max_pages > 0 && !p->page_table))) || (p->n_pages > 0 && !p->refs))

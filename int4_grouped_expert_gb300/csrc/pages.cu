@@ -71,7 +71,7 @@ struct Range {
   int64_t lo, hi;
 };
 template <int kBlocks>
-__host__ __device__ __forceinline__ int64_t share_of(int64_t n, int chunk) {
+__host__ __device__ constexpr int64_t share_of(int64_t n, int chunk) {
   return ((n + kBlocks - 1) / kBlocks + chunk - 1) / chunk * chunk;
 }
 template <int kBlocks>
@@ -530,11 +530,17 @@ constexpr int kAloneRows = 4096;
 }  // namespace
 
 template <int kBlocks>
+constexpr size_t extend_smem(int n_seq) {  // (up to 96 KB)
+  return 3 * sizeof(int32_t) * share_of<kBlocks>(n_seq, kPagesThreads);
+}
+template <int kBlocks>
 static cudaError_t launch_extend(const PagesExtendArgs& a, cudaStream_t stream) {
-  const size_t smem = 3 * sizeof(int32_t) * share_of<kBlocks>(a.p.n_seq, kPagesThreads);  // up to 96 KB
+  const size_t smem = extend_smem<kBlocks>(a.p.n_seq);
+  // The limit is what the largest call takes, not this one: threads with calls of different sizes share it.
+  constexpr size_t most = extend_smem<kBlocks>(kBlocks == 1 ? kPagesThreads : kPagesMostSeq);
   if (smem > 40 << 10) {
     const cudaError_t e = cudaFuncSetAttribute(pages_extend_kernel<kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+                                               static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }
   return launch_kernel(pages_extend_kernel<kBlocks>, dim3(kBlocks), dim3(kPagesThreads), smem, stream, true, a);

@@ -7,6 +7,7 @@ namespace strata {
 
 constexpr int kPagesCluster = 8;     // blocks of the cluster that settles one call's allocation
 constexpr int kPagesThreads = 1024;
+constexpr int kPagesMostSeq = 65535;  // sequences of a call
 
 struct PagesExtendArgs {
   strata_kv_pages p;
