@@ -13,8 +13,10 @@ __global__ void __launch_bounds__(1024) permute_kernel(PermuteArgs a) {
 cudaError_t launch_permute(const PermuteArgs& a, cudaStream_t stream) {
   const size_t smem = group_smem_ints(32, a.E) * sizeof(int);
   if (smem > 48 * 1024) {
+    // what the most experts take, not this call's: threads with calls of different sizes share the limit
+    constexpr size_t most = group_smem_ints(32, STRATA_MAX_EXPERTS) * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(permute_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }
   permute_kernel<<<1, 1024, smem, stream>>>(a);

@@ -14,6 +14,8 @@
 //
 // Top-k order: descending logit, ties to the lower expert id; gates = softmax probabilities of the
 // chosen experts (fp32, expf), renormalised over the k only with STRATA_RENORM.
+#include <algorithm>
+
 #include "group_rows.cuh"
 
 namespace strata {
@@ -404,12 +406,16 @@ cudaError_t launch_route_small(const RouteSmallArgs& a, cudaStream_t stream) {
   const dim3 grid((a.E + a.epc - 1) / a.epc);
   const size_t smem = route_small_smem(a);
   if (smem > 48 * 1024) {
+    // above every call's, not this one's: threads with calls of different sizes share the limit
+    constexpr size_t most = 4 * std::max(group_small_ints(kRsWarps, STRATA_MAX_EXPERTS, kGroupSmallMaxR),
+                                         group_smem_ints(kRsWarps, STRATA_MAX_EXPERTS)) +
+                            15 + kRouteSmallMaxT * STRATA_MAX_TOPK * 8;
     cudaError_t e = cudaFuncSetAttribute(route_small_kernel<false>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(most));
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(route_small_kernel<true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }
   if (a.wr_fp16)
