@@ -566,7 +566,8 @@ cudaError_t launch_pages_compact(const PagesCompactArgs& a, int num_sms, cudaStr
   const cudaError_t e = launch_kernel(alone ? pages_map_kernel<1> : pages_map_kernel<kPagesCluster>,
                                       dim3(alone ? 1 : kPagesCluster), dim3(kPagesThreads), 0, stream, true, a);
   if (e != cudaSuccess || a.src.n_seq == 0) return e;
-  const int64_t stretches = (a.dst.max_pages + kTableEntries - 1) / kTableEntries;
+  // (a table without entries has its lengths written)
+  const int64_t stretches = std::max<int64_t>(1, (a.dst.max_pages + kTableEntries - 1) / kTableEntries);
   const int64_t grid = std::min<int64_t>(a.src.n_seq * stretches, 8 * num_sms);
   return launch_kernel(pages_table_kernel, dim3(static_cast<unsigned>(grid)), dim3(kTableThreads), 0, stream, true, a,
                        static_cast<int>(stretches));
