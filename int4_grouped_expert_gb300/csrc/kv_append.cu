@@ -133,9 +133,9 @@ __device__ __forceinline__ void to_pairs(const uint4& w, uint64_t* x) {
 
 // The norm of a head's row, y = x * inv * weight with inv = 1 / sqrt(mean(x^2) + eps), all in fp32: nothing is rounded to
 // 16 bits before the rotation. The row lies in TPR lanes, 16 elements each; each sums its squares, then
-// the lanes do. Squares of elements from 2^60 on may leave fp32: such a row is summed once more times 2^-68, and
-// its elements are held so from there on (bf16 values times a power of two: exact but for those below 2^-118
-// of the largest). Squares that fp32 flushes are below 2^-49 of eps, which is at least 2^-100. Rows of a warp part ways
+// the lanes do. Squares of elements from 2^60 on may leave fp32, and so may their mean with a large eps: such a row is summed
+// once more times 2^-68, and its elements are held so from there on (bf16 values times a power of two: exact but for those below
+// 2^-109 of the largest). Squares that fp32 flushes are below 2^-49 of eps, which is at least 2^-100. Rows of a warp part ways
 // here, and so may its heads where they end: a row's lanes wait for one another only.
 template <int TPR>
 __device__ __forceinline__ float inv_norm(uint4& wa, uint4& wb, float eps) {
@@ -158,7 +158,7 @@ __device__ __forceinline__ float inv_norm(uint4& wa, uint4& wb, float eps) {
     return sum * (1.f / (16 * TPR));
   };
   float m = mean();
-  if (!(m < INFINITY)) {  // (the same in all lanes of the row)
+  if (!(m + eps < INFINITY)) {  // (the same in all lanes of the row)
     const float down = exp2i(-68);
     auto scaled = [&](uint32_t v) {
       const __nv_bfloat162 b = __floats2bfloat162_rn(bf16_lo_f32(v) * down, bf16_hi_f32(v) * down);
