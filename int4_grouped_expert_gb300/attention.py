@@ -158,7 +158,7 @@ class QKNorm:
             if w is None:
                 continue
             rows = 1 if w.dim() == 1 else w.shape[0]
-            if w.dim() not in (1, 2) or w.shape[-1] != head_dim:
+            if w.dim() not in (1, 2) or w.shape[-1] != head_dim or w.numel() == 0:  # (nothing: an address that means no norm)
                 raise ValueError(f"{name}_weight {tuple(w.shape)}: [{head_dim}] or [heads, {head_dim}] expected")
             _held(w, f"{name}_weight", "float32", rows * head_dim)
             setattr(s, f"{name}_weight", ptr(w))
