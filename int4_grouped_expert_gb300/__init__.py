@@ -373,7 +373,10 @@ def strata_kv_append_normed(cache: strata_kv_cache, norm: strata_qk_norm, k, v, 
                             n_pos=0, rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
                             q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
     """strata_kv_append with the norms that QKNorm describes. Strides in elements; None: rows follow one another."""
-    rows = getattr(norm, "rows", None)  # (of a QKNorm: the library cannot see how many rows of weights there are)
+    # (of a QKNorm: the library cannot see how wide its weights are, and how many rows there are)
+    if getattr(norm, "head_dim", cache.head_dim) != cache.head_dim:
+        raise ValueError(f"weights for heads of {norm.head_dim}, but heads of {cache.head_dim} in the cache")
+    rows = getattr(norm, "rows", None)
     if rows and (rows.get("q", n_heads) < n_heads or rows.get("k", cache.n_kv_heads) < cache.n_kv_heads):
         raise ValueError(f"weights for {rows} heads, but {n_heads} query and {cache.n_kv_heads} K/V heads")
     k_stride, v_stride, q_stride, q_out_stride = _append_strides(cache, n_heads, k_stride, v_stride, q_stride,

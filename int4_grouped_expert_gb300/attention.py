@@ -162,6 +162,7 @@ class QKNorm:
                 raise ValueError(f"{name}_weight {tuple(w.shape)}: [{head_dim}] or [heads, {head_dim}] expected")
             _held(w, f"{name}_weight", "float32", rows * head_dim)
             setattr(s, f"{name}_weight", ptr(w))
+            s.head_dim = head_dim
             setattr(s, f"{name}_head_stride", head_dim if rows > 1 else 0)
             if rows > 1:
                 s.rows[name] = rows

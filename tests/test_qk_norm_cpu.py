@@ -13,3 +13,15 @@ def test_weights_without_rows_are_refused(w):
     for q, k in ((w, None), (None, w), (torch.ones(64), w)):
         with pytest.raises(ValueError):
             st.QKNorm(q, k, w.shape[-1])
+
+
+@pytest.mark.parametrize("dim,other", [(64, 128), (128, 64)])
+def test_weights_of_another_width_than_the_heads(st, dim, other):  # noqa: F811
+    C = cache(st, head_dim=other, n_kv_heads=4)
+    f = st.strata_kv_append_normed
+    for q, k in ((torch.ones(dim), None), (None, torch.ones(dim)), (torch.ones(8, dim), torch.ones(4, dim))):
+        n = st.QKNorm(q, k, dim).struct()
+        with pytest.raises(ValueError):
+            f(C, n, A, A, 4, A, q=A, n_heads=8, q_out=2 * A)
+        assert f(cache(st, head_dim=dim, n_kv_heads=4), n, A, A, 0, A, q=A, n_heads=8, q_out=2 * A) == 0
+    assert f(C, st.QKNorm(None, None, dim).struct(), A, A, 0, A) == 0  # (no weights: no width)
