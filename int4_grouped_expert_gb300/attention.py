@@ -3,7 +3,7 @@
 QuantLinear holds one projection's codes and scales, PagedKVCache the pages of
 8-bit keys and values, PageTable who holds them, QKNorm the weights of the norms of queries and
 keys, kv_batch the lengths and page tables of one call. All hold torch tensors (for device memory only) and fill the C structs with their
-addresses; the arithmetic runs in the library, which sees addresses only: element
+addresses, and the structs keep the tensors alive; the arithmetic runs in the library, which sees addresses only: element
 types and layouts are checked here.
 """
 from __future__ import annotations
@@ -40,6 +40,7 @@ class QuantLinear:
         s = strata_linear()
         s.N, s.K, s.group_size, s.bits = N, K, group, bits
         s.codes, s.scales, s.bias = ptr(codes), ptr(scales), ptr(bias)
+        s.tensors = (codes, scales, bias)
         self._struct = s
 
     @classmethod
@@ -98,6 +99,7 @@ class PagedKVCache:
         s.n_kv_heads, s.head_dim, s.page_size, s.n_pages = n_kv_heads, head_dim, page_size, n_pages
         s.k_codes, s.v_codes = ptr(self.k_codes), ptr(self.v_codes)
         s.k_scales, s.v_scales = ptr(self.k_scales), ptr(self.v_scales)
+        s.tensors = (self.k_codes, self.v_codes, self.k_scales, self.v_scales)
         self._struct = s
 
     def struct(self) -> strata_kv_cache:
@@ -135,6 +137,7 @@ class PageTable:
         s.n_seq, s.page_size, s.n_pages, s.max_pages = n_seq, page_size, n_pages, max_pages
         s.table_stride = page_table.stride(0) if n_seq > 1 else max_pages
         s.page_table, s.kv_len, s.refs = ptr(self.page_table), ptr(self.kv_len), ptr(self.refs)
+        s.tensors = (self.page_table, self.kv_len, self.refs)
         self._struct = s
 
     def struct(self) -> strata_kv_pages:
@@ -153,6 +156,7 @@ class QKNorm:
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
         s = strata_qk_norm()
         s.eps = eps
+        s.tensors = (q_weight, k_weight)
         s.rows = {}  # heads that have a row of their own
         for name, w in (("q", q_weight), ("k", k_weight)):
             if w is None:
