@@ -573,6 +573,9 @@ strata_status strata_kv_pages_fork(const strata_kv_pages* pages, const int32_t* 
  * window > 0: of every sequence the pages that lie whole between its n_sinks first tokens and the window of its next
  * query (at position kv_len) go too: what strata_attention_sinks_forward with these numbers does not look at in later
  * calls. (Rows that are in the cache already and still to be attended to have earlier windows: release after them.)
+ * A later cut moves the next query's window back, and what was before it is gone: attention leaves such tokens out, and
+ * strata_kv_pages_extend gives nothing to a sequence whose unfinished page it was (both set STRATA_DEV_BAD_SLOT). Where a
+ * sequence may come back to a length up to c tokens below one that it was released at (rejected drafts), release with window + c.
  */
 strata_status strata_kv_pages_release(const strata_kv_pages* pages, const int32_t* keep, int32_t window, int32_t n_sinks,
                                       uint32_t* dev_status, strata_stream stream);
