@@ -345,7 +345,10 @@ def strata_linear_forward(lin: strata_linear, x, T, out, workspace, ws_bytes, x_
         lin.N if out_stride is None else out_stride, ptr(workspace), ws_bytes, stream_handle(stream))
 
 
-def _append_strides(cache, n_heads, k_stride, v_stride, q_stride, q_out_stride):
+def strata_kv_append(cache: strata_kv_cache, k, v, T, slots, positions=None, rope=None, n_pos=0,
+                     rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
+                     q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
+    """Strides in elements; None: rows follow one another."""
     if k_stride is None or v_stride is None:
         kv = cache.n_kv_heads * cache.head_dim
         k_stride = kv if k_stride is None else k_stride
@@ -354,15 +357,6 @@ def _append_strides(cache, n_heads, k_stride, v_stride, q_stride, q_out_stride):
         qd = n_heads * cache.head_dim
         q_stride = qd if q_stride is None else q_stride
         q_out_stride = qd if q_out_stride is None else q_out_stride
-    return k_stride, v_stride, q_stride, q_out_stride
-
-
-def strata_kv_append(cache: strata_kv_cache, k, v, T, slots, positions=None, rope=None, n_pos=0,
-                     rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
-                     q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
-    """Strides in elements; None: rows follow one another."""
-    k_stride, v_stride, q_stride, q_out_stride = _append_strides(cache, n_heads, k_stride, v_stride, q_stride,
-                                                                 q_out_stride)
     return (_lib or lib()).strata_kv_append(
         _byref(cache), None if q is None else ptr(q), q_stride, n_heads, ptr(k), k_stride, ptr(v), v_stride, T,
         ptr(slots), ptr(positions), ptr(rope), n_pos, rot_dim, flags, None if q_out is None else ptr(q_out),
@@ -373,14 +367,18 @@ def strata_kv_append_normed(cache: strata_kv_cache, norm: strata_qk_norm, k, v, 
                             n_pos=0, rot_dim=0, q=None, n_heads=0, q_out=None, k_stride=None, v_stride=None,
                             q_stride=None, q_out_stride=None, flags=0, dev_status=None, stream=None):
     """strata_kv_append with the norms that QKNorm describes. Strides in elements; None: rows follow one another."""
-    # (of a QKNorm: the library cannot see how wide its weights are, and how many rows there are)
-    if getattr(norm, "head_dim", cache.head_dim) != cache.head_dim:
-        raise ValueError(f"weights for heads of {norm.head_dim}, but heads of {cache.head_dim} in the cache")
-    rows = getattr(norm, "rows", None)
-    if rows and (rows.get("q", n_heads) < n_heads or rows.get("k", cache.n_kv_heads) < cache.n_kv_heads):
-        raise ValueError(f"weights for {rows} heads, but {n_heads} query and {cache.n_kv_heads} K/V heads")
-    k_stride, v_stride, q_stride, q_out_stride = _append_strides(cache, n_heads, k_stride, v_stride, q_stride,
-                                                                 q_out_stride)
+    serves = getattr(norm, "serves", None)  # (of a QKNorm: the library sees neither the width nor the rows of its weights)
+    if serves and (serves[0] != cache.head_dim or serves[1] < n_heads or serves[2] < cache.n_kv_heads):
+        raise ValueError(f"weights of {serves[0]} for {serves[1]} query and {serves[2]} K/V heads at most, but {n_heads} and "
+                         f"{cache.n_kv_heads} heads of {cache.head_dim}")
+    if k_stride is None or v_stride is None:
+        kv = cache.n_kv_heads * cache.head_dim
+        k_stride = kv if k_stride is None else k_stride
+        v_stride = kv if v_stride is None else v_stride
+    if q_stride is None or q_out_stride is None:
+        qd = n_heads * cache.head_dim
+        q_stride = qd if q_stride is None else q_stride
+        q_out_stride = qd if q_out_stride is None else q_out_stride
     return (_lib or lib()).strata_kv_append_normed(
         _byref(cache), _byref(norm), None if q is None else ptr(q), q_stride, n_heads, ptr(k), k_stride, ptr(v),
         v_stride, T, ptr(slots), ptr(positions), ptr(rope), n_pos, rot_dim, flags,

@@ -148,6 +148,9 @@ class PageTable:
         return kv_batch(q_start, self.kv_len, self.page_table, T, max_q, max_kv)
 
 
+_ANY_HEADS = 1 << 30  # more than any call has
+
+
 class QKNorm:
     """Norms of queries and keys for each head: fp32 weights, one row [head_dim] (or [1, head_dim]) for all heads
     or [heads, head_dim] with a row each, or None where there is no norm. eps is added to the mean of squares."""
@@ -157,7 +160,7 @@ class QKNorm:
         s = strata_qk_norm()
         s.eps = eps
         s.tensors = (q_weight, k_weight)
-        s.rows = {}  # heads that have a row of their own
+        serves = {"q": _ANY_HEADS, "k": _ANY_HEADS}
         for name, w in (("q", q_weight), ("k", k_weight)):
             if w is None:
                 continue
@@ -166,10 +169,11 @@ class QKNorm:
                 raise ValueError(f"{name}_weight {tuple(w.shape)}: [{head_dim}] or [heads, {head_dim}] expected")
             _held(w, f"{name}_weight", "float32", rows * head_dim)
             setattr(s, f"{name}_weight", ptr(w))
-            s.head_dim = head_dim
             setattr(s, f"{name}_head_stride", head_dim if rows > 1 else 0)
             if rows > 1:
-                s.rows[name] = rows
+                serves[name] = rows
+        if q_weight is not None or k_weight is not None:
+            s.serves = (head_dim, serves["q"], serves["k"])  # width, and how many query and K/V heads
         self._struct = s
 
     def struct(self) -> strata_qk_norm:
