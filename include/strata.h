@@ -545,7 +545,8 @@ typedef struct {
  * Sequence s gets the lowest free pages, the sequences in order, and kv_len[s] grows. Its new tokens are rows
  * q_start[s] .. q_start[s+1] - 1, at positions from the old length on. An unfinished page that other sequences
  * hold too is left to them: its place in the table gets a free page, and the pair (old page, new page) is listed
- * in copies, to be copied (strata_kv_copy_pages) before the append.
+ * in copies, to be copied (strata_kv_copy_pages) before the append. Sequences that are extended in the same call count as
+ * others: if all that hold the page are extended, all of them leave it, a free page each, and it is free.
  * new_tokens  [n_seq] int32, >= 0.           T_max  rows of slots and positions, up to 2^22.
  * slots, positions [T_max], q_start [n_seq + 1], copies [n_seq, 2], n_copies [1]: int32, written; rows
  *             without a token get slot -1 (padding of strata_kv_append) and position 0, copies from n_copies on keep

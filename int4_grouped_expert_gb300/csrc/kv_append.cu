@@ -467,8 +467,9 @@ __device__ __forceinline__ void rotate_queries(const KvAppendArgs& a, int block)
 
 // The same with norms. A thread copies its chunks of the next kNormAhead heads to shared memory while it works on one:
 // a row's sum has to go round its lanes before anything can be stored, and loads that wait in registers for that are
-// too few to keep the memory busy. (us, 10798 tokens of 56 heads, with the keys: 94 from registers, 84 so; 3 heads or 5
-// ahead are the same. More than three blocks an SM would spill the keys' half, two take 99.)
+// too few to keep the memory busy. (us, 10798 tokens of 56 heads, with the keys: 92 with four heads at a time in registers, 74 so,
+// 74.4 with three ahead. Three blocks an SM: two take 79 and four 92, as the keys' half then spills; 16 single tokens 4.9, 4.6
+// and 6.0.)
 constexpr int kNormAhead = 5;
 constexpr size_t kNormSmem = static_cast<size_t>(kNormAhead) * kAppThreads * 32;
 template <int kD>

@@ -520,10 +520,12 @@ __global__ void __launch_bounds__(kTableThreads) pages_table_kernel(PagesCompact
   }
 }
 
-// Up to so many pages and rows, and a sequence a thread, one block makes room alone. (us, alone / the cluster: 256 pages, 8
-// sequences 4.7 / 9.0; 16384, 256 7.4 / 11.7; 32768, 256 9.2 / 11.7; 65536, 256 13.5 / 12.7; 262144, 8 36 / 16; 8000 rows and
-// 4096 pages 9.8 / 10.8, 16384 12.1 / 12.0.) Numbering pages goes over each of them twice: 500 pages 3.9 / 5.2,
-// 12000 11.8 / 7.7.
+// Up to so many pages and rows, and a sequence a thread, one block makes room alone. (us, alone / the cluster, a row a sequence:
+// 256 pages, 8 sequences 5.3 / 10.0; 16384, 256 7.1 / 10.6; 32768, 256 9.3 / 11.1; 49152, 256 11.4 / 12.5; 65536, 256 13.6 / 12.1;
+// 262144, 8 37 / 17. More rows: 4096 pages, 8 sequences, 4096 rows 9.1 / 12.4, 8000 10.8 / 12.5, 16384 14.8 / 13.1; 16384 pages,
+// 288 sequences, 3456 rows 9.7 / 11.8, 8064 13.1 / 12.0; 1000 sequences, 4000 rows 10.4 / 12.8, 16000 18.6 / 13.4.) Numbering pages
+// goes over each of them twice (with the tables of 60 sequences: 500 pages 4.6 / 5.9, 4096 9.7 / 10.8, 6000 12.6 / 11.1, 12000
+// 21.9 / 10.9).
 constexpr int64_t kAlonePages = 32768, kAloneMapPages = 4096;
 constexpr int kAloneRows = 4096;
 
