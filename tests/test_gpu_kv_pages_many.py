@@ -29,7 +29,7 @@ def test_two_threads_make_room_for_different_numbers_of_sequences():
     """Every call is taken: what one thread's launch needs of shared memory does not go by the other's."""
     import torch
     import int4_grouped_expert_gb300 as st
-    sizes, refused = (25000, 65535), [0, 0]
+    sizes, refused = (25000, 65535), [None, None]
     i32 = dict(dtype=torch.int32, device="cuda")
 
     def work(i):
@@ -38,9 +38,9 @@ def test_two_threads_make_room_for_different_numbers_of_sequences():
         with torch.cuda.stream(side):
             p, new = st.PageTable(n, n, 1, 16), torch.zeros(n, **i32)
             out = [torch.zeros(k, **i32) for k in (8, 8, n + 1, 2 * n, 1)]
-            for _ in range(3000):
-                refused[i] += st.strata_kv_pages_extend(p.struct(), new, 8, *out, stream=side) != 0
+            n = sum(st.strata_kv_pages_extend(p.struct(), new, 8, *out, stream=side) != 0 for _ in range(3000))
             side.synchronize()
+            refused[i] = n
 
     threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
     for t in threads:

@@ -9,15 +9,15 @@ pytestmark = pytest.mark.gpu
 def refused(sizes, make, calls):
     """How many calls of each thread failed. make(size) gives a call on the thread's own stream and tensors."""
     import torch
-    count = [0] * len(sizes)
+    count = [None] * len(sizes)
 
     def work(i):
         side = torch.cuda.Stream()
         with torch.cuda.stream(side):
             call = make(sizes[i])
-            for _ in range(calls):
-                count[i] += call(side) != 0
+            n = sum(call(side) != 0 for _ in range(calls))
             side.synchronize()
+            count[i] = n
 
     threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sizes))]
     for t in threads:
